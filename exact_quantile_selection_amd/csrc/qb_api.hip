@@ -677,6 +677,227 @@ QB_API int qb_lei_grad(float* g, const int32_t* load, int64_t N, int E, int K, f
   return hip_status(qbk::launch_lei(g, load, N, E, K, eta, stream), fn);
 }
 
+// ---------------------------------------------------------------------------
+// the expert layer: routing with a balance loss, the exchange, 8-bit products
+
+static int check_balance(const char* fn, const float* s, int64_t N, int E, int K, const int32_t* seq_off, int B) {
+  if (int rc = check_pass(fn, s, 1, N, E)) return rc;
+  if (N > (int64_t(1) << 30)) return fail(QB_EINVAL, "%s: N=%lld, expected N <= 2^30", fn, (long long)N);
+  if (K < 1 || K >= E) return fail(QB_EINVAL, "%s: K=%d, expected 1 <= K < E=%d", fn, K, E);
+  if (K > kMaxK) return fail(QB_EUNSUPPORTED, "%s: K=%d, compiled for K <= %d", fn, K, kMaxK);
+  if (B < 1 || B > (1 << 20)) return fail(QB_EINVAL, "%s: B=%d sequences, expected 1 <= B <= 2^20", fn, B);
+  if (!seq_off && B != 1) return fail(QB_EINVAL, "%s: B=%d sequences need seq_off (int32 [B + 1])", fn, B);
+  return QB_OK;
+}
+
+QB_API int64_t qb_balance_workspace_bytes(int64_t N, int E, int B) {
+  if (N < 1 || N > (int64_t(1) << 30) || !qbk::supported_E(E) || B < 1 || B > (1 << 20)) return QB_EINVAL;
+  return qbk::balance_ws_layout(N, E, B).bytes;
+}
+
+QB_API int qb_balance_forward(const float* s, const float* b, int64_t N, int E, int K, const int32_t* seq_off, int B,
+                              const uint8_t* valid, float coef, int32_t* topk, float* gate, int32_t* count,
+                              float* weight, float* loss, void* ws, int64_t ws_bytes, qb_stream_t stream) {
+  const char* fn = "qb_balance_forward";
+  if (int rc = check_balance(fn, s, N, E, K, seq_off, B)) return rc;
+  if (!b || !topk)
+    return fail(QB_EINVAL, "%s: b (float [E=%d]) and topk (int32 [N=%lld][K=%d]) are required", fn, E, (long long)N, K);
+  const bool stats = count || weight || loss;
+  if (stats) {
+    const int64_t need = qbk::balance_ws_layout(N, E, B).bytes;
+    if (!ws || ws_bytes < need)
+      return fail(QB_EINVAL, "%s: ws_bytes=%lld, this shape needs %lld (qb_balance_workspace_bytes)", fn,
+                  ws ? (long long)ws_bytes : 0LL, (long long)need);
+    if (!aligned16(ws)) return fail(QB_EINVAL, "%s: ws must be 16-byte aligned", fn);
+    if (weight && !aligned16(weight)) return fail(QB_EINVAL, "%s: weight must be 16-byte aligned", fn);
+  }
+  if (int rc = check_elem_align(fn, {b, seq_off, topk, gate, count, loss})) return rc;
+  const qbk::BalFwd a{s, b, N, E, K, seq_off, B, valid, coef, topk, gate, count, weight, loss,
+                      stats ? static_cast<uint8_t*>(ws) : nullptr};
+  return hip_status(qbk::launch_balance_fwd(a, stream), fn);
+}
+
+QB_API int qb_balance_backward(const float* s, const int32_t* topk, int64_t N, int E, int K, const int32_t* seq_off,
+                               int B, const uint8_t* valid, const float* weight, const float* dloss,
+                               const float* dgate, float* dlogits, qb_stream_t stream) {
+  const char* fn = "qb_balance_backward";
+  if (int rc = check_balance(fn, s, N, E, K, seq_off, B)) return rc;
+  if (!dlogits) return fail(QB_EINVAL, "%s: dlogits (float [N=%lld][E=%d]) is required", fn, (long long)N, E);
+  if (!weight && !dgate) return fail(QB_EINVAL, "%s: nothing to differentiate (weight and dgate are NULL)", fn);
+  if (dgate && !topk) return fail(QB_EINVAL, "%s: dgate needs topk (int32 [N][K])", fn);
+  if (!aligned16(dlogits) || (weight && !aligned16(weight)))
+    return fail(QB_EINVAL, "%s: weight and dlogits must be 16-byte aligned", fn);
+  if (int rc = check_elem_align(fn, {topk, seq_off, dloss, dgate})) return rc;
+  const qbk::BalBwd a{s, topk, N, E, K, seq_off, B, valid, weight, dloss, dgate, dlogits};
+  return hip_status(qbk::launch_balance_bwd(a, stream), fn);
+}
+
+static int check_dispatch(const char* fn, int64_t N, int K, int E, int align) {
+  if (N < 0 || K < 1 || N > int64_t(INT32_MAX) / K)
+    return fail(QB_EINVAL, "%s: N=%lld, K=%d; expected N >= 0, K >= 1 and N K < 2^31", fn, (long long)N, K);
+  if (E < 1 || E > 256) return fail(QB_EUNSUPPORTED, "%s: E=%d, expected 1 <= E <= 256", fn, E);
+  if (align < 1 || align > (1 << 20)) return fail(QB_EINVAL, "%s: align=%d, expected 1 <= align <= 2^20", fn, align);
+  return QB_OK;
+}
+
+QB_API int64_t qb_dispatch_rows(int64_t N, int K, int E, int align) {
+  if (int rc = check_dispatch("qb_dispatch_rows", N, K, E, align)) return rc;
+  const int64_t pairs = N * K;
+  return (pairs + std::min<int64_t>(E, pairs) * (align - 1)) / align * align;
+}
+
+QB_API int64_t qb_dispatch_workspace_bytes(int64_t N, int K, int E) {
+  if (int rc = check_dispatch("qb_dispatch_workspace_bytes", N, K, E, 1)) return rc;
+  return qbk::dispatch_ws_bytes(N * K, E);
+}
+
+QB_API int qb_dispatch(const int32_t* topk, int64_t N, int K, int E, int align, int32_t* off, int64_t R,
+                       int32_t* row_src, int32_t* pos, void* ws, int64_t ws_bytes, qb_stream_t stream) {
+  const char* fn = "qb_dispatch";
+  if (int rc = check_dispatch(fn, N, K, E, align)) return rc;
+  const int64_t rows = qb_dispatch_rows(N, K, E, align);
+  if (R < rows || R > INT32_MAX)
+    return fail(QB_EINVAL, "%s: R=%lld rows, this shape needs %lld (qb_dispatch_rows) and R < 2^31", fn, (long long)R,
+                (long long)rows);
+  if (!off || (N > 0 && (!topk || !pos)) || (R > 0 && !row_src))
+    return fail(QB_EINVAL,
+                "%s: topk (int32 [N=%lld][K=%d]), off (int32 [E + 1]), row_src (int32 [R=%lld]) and pos (int32 [N][K]) are required",
+                fn, (long long)N, K, (long long)R);
+  const int64_t need = qbk::dispatch_ws_bytes(N * K, E);
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(QB_EINVAL, "%s: ws_bytes=%lld, this shape needs %lld (qb_dispatch_workspace_bytes)", fn,
+                ws ? (long long)ws_bytes : 0LL, (long long)need);
+  if (need > 0 && !aligned16(ws)) return fail(QB_EINVAL, "%s: ws must be 16-byte aligned", fn);
+  if (int rc = check_elem_align(fn, {topk, off, row_src, pos})) return rc;
+  const qbk::Dispatch a{topk, N * K, K, E, align, off, R, row_src, pos, static_cast<int32_t*>(ws)};
+  return hip_status(qbk::launch_dispatch(a, stream), fn);
+}
+
+static int check_combine(const char* fn, int64_t N, int K, int H, int64_t R) {
+  if (N < 0 || N > (1 << 24) || K < 1 || H < 1 || H > (1 << 20) || R < 0 || R > INT32_MAX ||
+      N * K > int64_t(INT32_MAX))
+    return fail(QB_EINVAL,
+                "%s: N=%lld, K=%d, H=%d, R=%lld; expected 0 <= N <= 2^24, K >= 1, 1 <= H <= 2^20, N K and R below 2^31",
+                fn, (long long)N, K, H, (long long)R);
+  return QB_OK;
+}
+
+QB_API int qb_combine(const uint16_t* rows, int64_t R, const int32_t* pos, const float* gate, int64_t N, int K, int H,
+                      uint16_t* out, qb_stream_t stream) {
+  const char* fn = "qb_combine";
+  if (int rc = check_combine(fn, N, K, H, R)) return rc;
+  if (N == 0) return ok();
+  if ((R > 0 && !rows) || !pos || !out)
+    return fail(QB_EINVAL, "%s: rows (bf16 [R=%lld][H=%d]), pos (int32 [N=%lld][K=%d]) and out (bf16 [N][H]) are required",
+                fn, (long long)R, H, (long long)N, K);
+  if (!aligned_all(2, {rows, out})) return fail(QB_EINVAL, "%s: bf16 arrays must be 2-byte aligned", fn);
+  if (int rc = check_elem_align(fn, {pos, gate})) return rc;
+  return hip_status(qbk::launch_combine(rows, R, pos, gate, N, K, H, out, stream), fn);
+}
+
+QB_API int qb_combine_backward(const uint16_t* dout, const uint16_t* rows, int64_t R, const int32_t* pos,
+                               const int32_t* row_src, const float* gate, int64_t N, int K, int H, uint16_t* drows,
+                               float* dgate, qb_stream_t stream) {
+  const char* fn = "qb_combine_backward";
+  if (int rc = check_combine(fn, N, K, H, R)) return rc;
+  if (N == 0 && R == 0) return ok();
+  if ((N > 0 && (!dout || !pos)) || (R > 0 && (!row_src || !drows)))
+    return fail(QB_EINVAL,
+                "%s: dout (bf16 [N=%lld][H=%d]), pos (int32 [N][K=%d]), row_src (int32 [R=%lld]) and drows (bf16 [R][H]) are required",
+                fn, (long long)N, H, K, (long long)R);
+  if (dgate && R > 0 && !rows) return fail(QB_EINVAL, "%s: dgate needs rows (bf16 [R][H])", fn);
+  if (!aligned_all(2, {dout, rows, drows})) return fail(QB_EINVAL, "%s: bf16 arrays must be 2-byte aligned", fn);
+  if (int rc = check_elem_align(fn, {pos, row_src, gate, dgate})) return rc;
+  return hip_status(qbk::launch_combine_bwd(dout, rows, R, pos, row_src, gate, N, K, H, drows, dgate, stream), fn);
+}
+
+constexpr int64_t kFp8Most = int64_t(1) << 22;
+
+static int check_fp8(const char* fn, int64_t M, int64_t N, int64_t C, int G) {
+  if (M < 0 || M > kFp8Most || N < 1 || N > kFp8Most || C < 1 || C > kFp8Most)
+    return fail(QB_EINVAL, "%s: M=%lld, N=%lld, C=%lld; expected 0 <= M <= 2^22 and 1 <= N, C <= 2^22", fn,
+                (long long)M, (long long)N, (long long)C);
+  if (G < 1 || G > 256) return fail(QB_EUNSUPPORTED, "%s: G=%d matrices, expected 1 <= G <= 256", fn, G);
+  return QB_OK;
+}
+
+static int check_quantize(const char* fn, const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M, int C,
+                          const uint8_t* q, const uint8_t* sc) {
+  if (int rc = check_fp8(fn, M, 1, C, 1)) return rc;
+  if (Mx < 0 || Mx > kFp8Most || (!row_src && Mx != M))
+    return fail(QB_EINVAL, "%s: x has Mx=%lld rows; expected M=%lld, or row_src (int32 [M])", fn, (long long)Mx,
+                (long long)M);
+  if (M == 0) return QB_OK;
+  if ((Mx > 0 && !x) || !q || !sc)
+    return fail(QB_EINVAL, "%s: x (bf16 [Mx=%lld][C=%d]), the e4m3 matrix and its scales are required", fn,
+                (long long)Mx, C);
+  if (!aligned_all(2, {x})) return fail(QB_EINVAL, "%s: x must be 2-byte aligned", fn);
+  if (!aligned16(q) || !aligned4(sc))
+    return fail(QB_EINVAL, "%s: e4m3 matrices must be 16-byte and scales 4-byte aligned", fn);
+  return check_elem_align(fn, {row_src});
+}
+
+QB_API int qb_fp8_quantize(const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M, int C, uint8_t* xq,
+                           uint8_t* xs, qb_stream_t stream) {
+  const char* fn = "qb_fp8_quantize";
+  if (int rc = check_quantize(fn, x, Mx, row_src, M, C, xq, xs)) return rc;
+  if (M == 0) return ok();
+  return hip_status(qbk::launch_fp8_quantize(x, Mx, row_src, M, C, xq, xs, stream), fn);
+}
+
+QB_API int qb_fp8_quantize_cols(const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M, int C, uint8_t* xt,
+                                uint8_t* xts, qb_stream_t stream) {
+  const char* fn = "qb_fp8_quantize_cols";
+  if (int rc = check_quantize(fn, x, Mx, row_src, M, C, xt, xts)) return rc;
+  if (M == 0) return ok();
+  return hip_status(qbk::launch_fp8_quantize_cols(x, Mx, row_src, M, C, xt, xts, stream), fn);
+}
+
+QB_API int qb_fp8_quantize_weight(const float* w, int G, int N, int C, uint8_t* wq, uint8_t* ws, uint8_t* wt,
+                                  uint8_t* wts, qb_stream_t stream) {
+  const char* fn = "qb_fp8_quantize_weight";
+  if (int rc = check_fp8(fn, 0, N, C, G)) return rc;
+  if (!w || !wq || !ws || !wt != !wts)
+    return fail(QB_EINVAL,
+                "%s: w (float [G=%d][N=%d][C=%d]), wq and ws are required, and wt and wts both or neither", fn, G, N, C);
+  if (!aligned16(wq) || !aligned4(ws) || (wt && (!aligned16(wt) || !aligned4(wts))))
+    return fail(QB_EINVAL, "%s: e4m3 matrices must be 16-byte and scales 4-byte aligned", fn);
+  if (int rc = check_elem_align(fn, {w})) return rc;
+  return hip_status(qbk::launch_fp8_quantize_weight(w, G, N, C, wq, ws, wt, wts, stream), fn);
+}
+
+QB_API int qb_fp8_product(const uint8_t* xq, const uint8_t* xs, const uint8_t* w, const uint8_t* w_scale, int64_t M,
+                          int N, int C, const int32_t* off, int G, int exact, uint16_t* y, qb_stream_t stream) {
+  const char* fn = "qb_fp8_product";
+  if (int rc = check_fp8(fn, M, N, C, G)) return rc;
+  if (!off && G != 1) return fail(QB_EINVAL, "%s: G=%d matrices need off (int32 [G + 1])", fn, G);
+  if (exact != 0 && exact != 1) return fail(QB_EINVAL, "%s: exact=%d, expected 0 or 1", fn, exact);
+  if (M == 0) return ok();
+  if (!xq || !xs || !w || !w_scale || !y)
+    return fail(QB_EINVAL, "%s: xq, xs, w, w_scale and y (bf16 [M=%lld][N=%d]) are required", fn, (long long)M, N);
+  if (!aligned16(xq) || !aligned16(w) || !aligned4(xs) || !aligned4(w_scale))
+    return fail(QB_EINVAL, "%s: e4m3 matrices must be 16-byte and scales 4-byte aligned", fn);
+  if (!aligned_all(2, {y})) return fail(QB_EINVAL, "%s: y must be 2-byte aligned", fn);
+  if (int rc = check_elem_align(fn, {off})) return rc;
+  return hip_status(qbk::launch_fp8_product(xq, xs, w, w_scale, M, N, qbk::fp8_ld(C), off, G, exact != 0, y, stream),
+                    fn);
+}
+
+QB_API int qb_fp8_weight_grad(const uint8_t* dyt, const uint8_t* dyts, const uint8_t* xt, const uint8_t* xts,
+                              int64_t M, int N, int C, const int32_t* off, int G, float* dw, qb_stream_t stream) {
+  const char* fn = "qb_fp8_weight_grad";
+  if (int rc = check_fp8(fn, M, N, C, G)) return rc;
+  if (!off && G != 1) return fail(QB_EINVAL, "%s: G=%d matrices need off (int32 [G + 1])", fn, G);
+  if (!dw || (M > 0 && (!dyt || !dyts || !xt || !xts)))
+    return fail(QB_EINVAL, "%s: dyt, dyts, xt, xts and dw (float [G=%d][N=%d][C=%d]) are required", fn, G, N, C);
+  if (!aligned16(dyt) || !aligned16(xt) || !aligned4(dyts) || !aligned4(xts))
+    return fail(QB_EINVAL, "%s: e4m3 matrices must be 16-byte and scales 4-byte aligned", fn);
+  if (int rc = check_elem_align(fn, {off, dw})) return rc;
+  return hip_status(qbk::launch_fp8_weight_grad(dyt, dyts, xt, xts, N, C, qbk::fp8_ld(M), M > 0 ? off : nullptr, G,
+                                                dw, stream),
+                    fn);
+}
+
 QB_API const char* qb_status_string(int status) {
   switch (status) {
     case QB_OK: return "QB_OK";

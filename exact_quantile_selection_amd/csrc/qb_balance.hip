@@ -1,0 +1,588 @@
+// qb_balance.hip -- routing with a sequence-wise balance loss: the K experts
+// of every token by biased score, their normalised gates, the per-expert
+// counts of every sequence, the loss, and the gradient of gates and loss
+// through the sigmoid.
+//
+// For token i of sequence q (T_q live tokens, B sequences, n of them with a
+// live token), scores s, bias b:
+//   topk[i]  = the K largest of fl32(s_i + b), larger first, equal values by
+//              lower expert index;  gate_ik = s_ik / sum_k s_ik
+//   z_i = sum_e s_ie,  p_ie = s_ie / z_i          (0 where z_i = 0)
+//   c_qe = number of live tokens of q that chose e,  f_qe = c_qe E / (K T_q)
+//   loss = (coef / n) sum_q sum_e f_qe (1 / T_q) sum_{i in q} p_ie
+// f is held constant in the gradient.  With g the gradient of the gates:
+//   dloss/ds_ie = (w_qe - sum_e' w_qe' p_ie') / z_i,  w_qe = coef (f_qe - 1) / (n T_q)
+//   (sum_e p = 1, so subtracting 1 from every f changes nothing and keeps the
+//   small differences that carry the signal in 32 bits)
+//   dgate/ds_ik = (g_ik - sum_k' g_ik' gate_ik') / sum_k s_ik
+//   dlogit = ds s (1 - s).
+//
+// Both passes read the scores once from HBM and are bound by that stream.  A
+// row is held by LPR lanes in registers (V = E / LPR scores a lane), so
+// column sums of p stay in a lane's registers from row to row and only the
+// end of a sequence's stretch of rows reduces them across lanes.  A workgroup
+// takes a chunk of T consecutive rows and leaves one partial row (E counts,
+// E sums) for every sequence that meets its chunk, at slot chunk + sequence
+// (both only grow along the rows, so no two stretches share a slot).  A
+// second kernel adds each sequence's slots in order in 64 bits: the same
+// result on every run, no atomics on floating-point numbers.
+#include <algorithm>
+
+#include "qb_device.hpp"
+#include "qb_internal.hpp"
+
+namespace qbk {
+
+constexpr int kBalThreads = 256;
+constexpr int kBalWaves = kBalThreads / kWave;
+
+template <int E>
+struct BalShape {
+  static constexpr int LPR = E >= 256 ? 8 : 4;   // lanes per row
+  static constexpr int V = E / LPR;              // scores per lane and row
+  static constexpr int F4 = V / 4;
+  static constexpr int RPW = kWave / LPR;        // rows per wave and step
+  static constexpr int R = RPW * kBalWaves;      // rows per workgroup and step
+  static_assert(V >= 4 && V <= 32, "scores per lane");
+};
+
+template <int LPR>
+__device__ __forceinline__ float bal_row_sum(float x) {
+  x += quad_mov<kQuadXor1>(x);
+  x += quad_mov<kQuadXor2>(x);
+  if constexpr (LPR >= 8) x += quad_mov<kHalfMirror>(x);
+  return x;
+}
+template <int LPR>
+__device__ __forceinline__ int bal_row_sum_i(int x) {
+  x += quad_mov_i<kQuadXor1>(x);
+  x += quad_mov_i<kQuadXor2>(x);
+  if constexpr (LPR >= 8) x += quad_mov_i<kHalfMirror>(x);
+  return x;
+}
+
+// The sequence that row r belongs to: the number of ends off[1..B] at or
+// below r (B: past the last sequence).  off need not be sorted for this to
+// stay within [0, B].
+__device__ __forceinline__ int bal_find(const int32_t* off, int B, int r) {
+  int lo = 0, hi = B;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (off[mid + 1] <= r)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// Rows per chunk: short chunks keep all CUs busy on few tokens, longer ones
+// keep the partial rows small beside the scores (128 rows of 256 experts:
+// 2 KiB of partials for 128 KiB of scores).
+int balance_chunk_rows(int64_t N) { return N <= 32768 ? 32 : 128; }
+
+BalWs balance_ws_layout(int64_t N, int E, int B) {
+  BalWs w;
+  w.T = balance_chunk_rows(N);
+  w.chunks = (N + w.T - 1) / w.T;
+  w.slots = w.chunks + B;
+  w.groups = int64_t(B) * (E / 16);
+  w.part = 16;  // the arrival counter comes first
+  w.psum = w.part + (w.groups * 8 + 15) / 16 * 16;
+  w.cnt = w.psum + w.slots * E * 4;
+  w.live = w.cnt + w.slots * E * 4;
+  w.bytes = w.live + (w.slots * 4 + 15) / 16 * 16;
+  return w;
+}
+
+// The K first of the row's order, element by element: only for rows with
+// equal values among (or at the end of) the K largest.
+template <int E>
+__device__ __forceinline__ void bal_select_ties(const float4 (&x)[BalShape<E>::F4], const float* lds_b, int ql, int K,
+                                                uint32_t* stage_id) {
+  using S = BalShape<E>;
+  constexpr int LPR = S::LPR;
+  uint32_t rem = S::V >= 32 ? ~0u : (1u << (S::V & 31)) - 1u;
+  for (int k = 0; k < K; ++k) {
+    float best = -__builtin_inff();
+    int at = E;
+#pragma unroll
+    for (int t = 0; t < S::F4; ++t) {
+      const float4 bb = *reinterpret_cast<const float4*>(lds_b + 4 * (LPR * t + ql));
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float v = comp(x[t], c) + comp(bb, c);
+        const bool take = ((rem >> (4 * t + c)) & 1u) && (v > best || at == E);
+        best = take ? v : best;
+        at = take ? 4 * (LPR * t + ql) + c : at;
+      }
+    }
+    auto join = [&](float ov, int oa) {
+      const bool take = oa < E && (at == E || ov > best || (ov == best && oa < at));
+      best = take ? ov : best;
+      at = take ? oa : at;
+    };
+    join(quad_mov<kQuadXor1>(best), quad_mov_i<kQuadXor1>(at));
+    join(quad_mov<kQuadXor2>(best), quad_mov_i<kQuadXor2>(at));
+    if constexpr (LPR >= 8) join(quad_mov<kHalfMirror>(best), quad_mov_i<kHalfMirror>(at));
+    if (at < E) {
+      const int quad = at >> 2;
+      if (quad % LPR == ql) {
+        rem &= ~(1u << (4 * (quad / LPR) + (at & 3)));
+        stage_id[k] = uint32_t(at);
+      }
+    }
+  }
+}
+
+template <int E, int P, bool STATS>
+__global__ __launch_bounds__(kBalThreads) void k_balance_fwd(
+    const float* __restrict__ s, const float* __restrict__ b, int N, int K, const int32_t* __restrict__ seq_off, int B,
+    const uint8_t* __restrict__ valid, int T, int32_t* __restrict__ topk, float* __restrict__ gate,
+    float* __restrict__ psum, int32_t* __restrict__ cnt, int32_t* __restrict__ live, uint32_t* __restrict__ arrivals) {
+  using S = BalShape<E>;
+  constexpr int LPR = S::LPR, F4 = S::F4, RPW = S::RPW, R = S::R;
+  __shared__ __align__(16) float lds_b[E];
+  __shared__ uint32_t stage[kBalWaves][RPW][16];   // the row's chosen experts in order
+  __shared__ int lds_cnt[STATS ? E : 1];
+  __shared__ int lds_live[kBalWaves];
+  __shared__ __align__(16) float lds_p[STATS ? kBalWaves : 1][E];
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int rho = lane / LPR, ql = lane % LPR;
+  const int r0 = int(blockIdx.x) * T;
+  const int r1 = N - r0 < T ? N : r0 + T;
+  for (int j = tid; j < E; j += kBalThreads) {
+    lds_b[j] = b[j];
+    if constexpr (STATS) lds_cnt[j] = 0;
+  }
+  if constexpr (STATS)
+    if (blockIdx.x == 0 && tid == 0) *arrivals = 0;
+  __syncthreads();
+
+  int q = seq_off ? bal_find(seq_off, B, r0) : 0;
+  for (int row0 = r0; row0 < r1;) {
+    // rows [row0, end) belong to sequence q, or to none
+    int end = r1, begin = 0;
+    bool in_seq = true;
+    if (seq_off) {
+      in_seq = q < B;
+      if (in_seq) {
+        end = seq_off[q + 1];
+        end = end < r1 ? end : r1;
+        begin = q == 0 ? seq_off[0] : 0;
+      }
+    }
+    float4 acc[STATS ? F4 : 1];
+    if constexpr (STATS)
+#pragma unroll
+      for (int t = 0; t < F4; ++t) acc[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+    int n_live = 0;
+    for (int rb = row0; rb < end; rb += R) {
+      if (rb + wave * RPW >= end) continue;  // nothing for this wave (no barrier below)
+      const int row = rb + wave * RPW + rho;
+      const bool here = row < end;
+      const int64_t ld_row = here ? row : end - 1;
+      const float* src = s + ld_row * E;
+      float4 x[F4];
+#pragma unroll
+      for (int t = 0; t < F4; ++t) x[t] = ld4(src + 4 * (LPR * t + ql));
+      const bool lv = here && in_seq && row >= begin && (!valid || valid[ld_row] != 0);
+      float top[P];
+#pragma unroll
+      for (int k = 0; k < P; ++k) top[k] = -__builtin_inff();
+      float z = 0.f;
+#pragma unroll
+      for (int t = 0; t < F4; ++t) {
+        const float4 bb = *reinterpret_cast<const float4*>(lds_b + 4 * (LPR * t + ql));
+        top_insert<P>(top, x[t].x + bb.x);
+        top_insert<P>(top, x[t].y + bb.y);
+        top_insert<P>(top, x[t].z + bb.z);
+        top_insert<P>(top, x[t].w + bb.w);
+        if constexpr (STATS) z += (x[t].x + x[t].y) + (x[t].z + x[t].w);
+      }
+      top_merge<P, kQuadXor1>(top);
+      top_merge<P, kQuadXor2>(top);
+      if constexpr (LPR >= 8) top_merge<P, kHalfMirror>(top);
+      float a = top[0];
+      bool tie = false;
+#pragma unroll
+      for (int k = 1; k < P; ++k) {
+        a = k < K ? top[k] : a;
+        tie |= k < K && top[k] == top[k - 1];
+      }
+      uint32_t mem = 0;  // bit 4 t + c: expert 4 (LPR t + ql) + c is among the K largest
+#pragma unroll
+      for (int t = 0; t < F4; ++t) {
+        const float4 bb = *reinterpret_cast<const float4*>(lds_b + 4 * (LPR * t + ql));
+        mem |= (x[t].x + bb.x >= a ? 1u : 0u) << (4 * t);
+        mem |= (x[t].y + bb.y >= a ? 1u : 0u) << (4 * t + 1);
+        mem |= (x[t].z + bb.z >= a ? 1u : 0u) << (4 * t + 2);
+        mem |= (x[t].w + bb.w >= a ? 1u : 0u) << (4 * t + 3);
+      }
+      tie |= bal_row_sum_i<LPR>(__popc(mem)) != K;
+      uint32_t* mine = stage[wave][rho];
+      if (!tie) {
+        while (mem) {
+          const int bit = __builtin_ctz(mem);
+          mem &= mem - 1;
+          const int e = 4 * (LPR * (bit >> 2) + ql) + (bit & 3);
+          const float v = src[e] + lds_b[e];
+          int rank = 0;
+#pragma unroll
+          for (int k = 0; k < P; ++k) rank += (k < K && top[k] > v) ? 1 : 0;
+          mine[rank] = uint32_t(e);
+        }
+      }
+      if (__ballot(tie) != 0) {
+        // every row of the wave takes the slow way; it gives the same order
+        bal_select_ties<E>(x, lds_b, ql, K, mine);
+      }
+      __builtin_amdgcn_wave_barrier();
+      asm volatile("" ::: "memory");
+      // lane ql writes ranks ql, ql + LPR, ...
+      float sv[(16 + LPR - 1) / LPR], total = 0.f;
+      int id[(16 + LPR - 1) / LPR];
+#pragma unroll
+      for (int u = 0; u < 16 / LPR; ++u) {
+        const int k = ql + u * LPR;
+        id[u] = k < K ? int(mine[k] & uint32_t(E - 1)) : 0;
+        sv[u] = k < K ? src[id[u]] : 0.f;
+        total += sv[u];
+      }
+      total = bal_row_sum<LPR>(total);
+      const float per = total > 0.f ? 1.0f / total : 0.f;
+#pragma unroll
+      for (int u = 0; u < 16 / LPR; ++u) {
+        const int k = ql + u * LPR;
+        if (here && k < K) {
+          const int64_t o = int64_t(row) * K + k;
+          topk[o] = lv ? id[u] : -1;
+          if (gate) gate[o] = lv ? sv[u] * per : 0.f;
+          if constexpr (STATS)
+            if (lv) atomicAdd(&lds_cnt[id[u]], 1);
+        }
+      }
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_wave_barrier();
+      if constexpr (STATS) {
+        z = bal_row_sum<LPR>(z);
+        if (lv) {  // a dead row's scores may be anything
+          const float inv = z > 0.f ? 1.0f / z : 0.f;
+#pragma unroll
+          for (int t = 0; t < F4; ++t) {
+            acc[t].x = fmaf(x[t].x, inv, acc[t].x);
+            acc[t].y = fmaf(x[t].y, inv, acc[t].y);
+            acc[t].z = fmaf(x[t].z, inv, acc[t].z);
+            acc[t].w = fmaf(x[t].w, inv, acc[t].w);
+          }
+        }
+        n_live += lv && ql == 0 ? 1 : 0;
+      }
+    }
+    if constexpr (STATS) {
+      if (in_seq && end > row0) {
+        // the lanes of one wave that hold the same columns, then the waves
+#pragma unroll
+        for (int t = 0; t < F4; ++t) {
+#pragma unroll
+          for (int d = LPR; d < kWave; d <<= 1) {
+            acc[t].x += __shfl_xor(acc[t].x, d);
+            acc[t].y += __shfl_xor(acc[t].y, d);
+            acc[t].z += __shfl_xor(acc[t].z, d);
+            acc[t].w += __shfl_xor(acc[t].w, d);
+          }
+          if (rho == 0) *reinterpret_cast<float4*>(&lds_p[wave][4 * (LPR * t + ql)]) = acc[t];
+        }
+#pragma unroll
+        for (int d = 1; d < kWave; d <<= 1) n_live += __shfl_xor(n_live, d);
+        if (lane == 0) lds_live[wave] = n_live;
+        __syncthreads();
+        const int64_t slot = int64_t(blockIdx.x) + q;
+        for (int j = tid; j < E; j += kBalThreads) {
+          psum[slot * E + j] = (lds_p[0][j] + lds_p[1][j]) + (lds_p[2][j] + lds_p[3][j]);
+          cnt[slot * E + j] = lds_cnt[j];
+          lds_cnt[j] = 0;
+        }
+        if (tid == 0) live[slot] = (lds_live[0] + lds_live[1]) + (lds_live[2] + lds_live[3]);
+        __syncthreads();
+      }
+    }
+    row0 = end > row0 ? end : row0;
+    ++q;
+    if (!in_seq) break;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The sums of each sequence's slots, its weights and its share of the loss:
+// one workgroup for 16 experts of one sequence.  Every workgroup counts the
+// sequences that have a live token itself (a scan of a few live words); the
+// last one to arrive adds the shares of the loss in a fixed order.
+constexpr int kBalFinThreads = 256;
+constexpr int kBalFinWays = kBalFinThreads / 16;
+
+__device__ __forceinline__ void bal_slots(const int32_t* seq_off, int N, int T, int q, int64_t& s0, int64_t& s1) {
+  int lo = 0, hi = N;
+  if (seq_off) {
+    lo = seq_off[q];
+    lo = lo < 0 ? 0 : (lo > N ? N : lo);
+    hi = seq_off[q + 1];
+    hi = hi < lo ? lo : (hi > N ? N : hi);
+  }
+  s0 = int64_t(lo / T) + q;
+  s1 = hi > lo ? int64_t((hi - 1) / T) + q + 1 : s0;
+}
+
+__global__ __launch_bounds__(kBalFinThreads) void k_balance_fin(
+    const int32_t* __restrict__ seq_off, int B, int N, int E, int K, int T, float coef, const float* __restrict__ psum,
+    const int32_t* __restrict__ cnt, const int32_t* __restrict__ live, double* __restrict__ part,
+    uint32_t* __restrict__ arrivals, int32_t* __restrict__ count, float* __restrict__ weight,
+    float* __restrict__ loss) {
+  __shared__ double sh_p[kBalFinWays][16];
+  __shared__ int sh_c[kBalFinWays][16];
+  __shared__ int sh_filled, sh_tok;
+  __shared__ bool sh_last;
+  const int tid = threadIdx.x, col = tid & 15, way = tid >> 4;
+  const int eg = E / 16;
+  const int q = int(blockIdx.x) / eg, e = (int(blockIdx.x) % eg) * 16 + col;
+  if (tid == 0) {
+    sh_filled = 0;
+    sh_tok = 0;
+  }
+  __syncthreads();
+  int64_t s0, s1;
+  bal_slots(seq_off, N, T, q, s0, s1);
+  double p = 0.0;
+  int c = 0;
+  for (int64_t t = s0 + way; t < s1; t += kBalFinWays) {
+    p += double(psum[t * E + e]);
+    c += cnt[t * E + e];
+  }
+  sh_p[way][col] = p;
+  sh_c[way][col] = c;
+  int tok = 0;
+  for (int64_t t = s0 + tid; t < s1; t += kBalFinThreads) tok += live[t];
+  if (tok) atomicAdd(&sh_tok, tok);
+  // sequences with a live token: most show one in their first slot
+  int filled = 0;
+  for (int j = tid; j < B; j += kBalFinThreads) {
+    int64_t a0, a1;
+    bal_slots(seq_off, N, T, j, a0, a1);
+    bool any = false;
+    for (int64_t t = a0; t < a1 && !any; ++t) any = live[t] != 0;
+    filled += any ? 1 : 0;
+  }
+  if (filled) atomicAdd(&sh_filled, filled);
+  __syncthreads();
+  if (tid < 64) {
+    double share = 0.0;
+    if (tid < 16) {
+#pragma unroll
+      for (int w = 1; w < kBalFinWays; ++w) {
+        p += sh_p[w][col];
+        c += sh_c[w][col];
+      }
+      const double toks = double(sh_tok);
+      const double per = sh_tok > 0 ? 1.0 / toks : 0.0;
+      const double scale = double(coef) / double(sh_filled > 0 ? sh_filled : 1);
+      const double f = double(c) * per * (double(E) / double(K));
+      if (count) count[int64_t(q) * E + e] = c;
+      if (weight) weight[int64_t(q) * E + e] = float(scale * (f - 1.0) * per);
+      share = scale * f * p * per;
+    }
+    if (loss) {
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) share += __shfl_xor(share, d);
+      if (tid == 0) {
+        __hip_atomic_store(reinterpret_cast<unsigned long long*>(part + blockIdx.x),
+                           __builtin_bit_cast(unsigned long long, share), __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT);
+        sh_last = __hip_atomic_fetch_add(arrivals, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+      }
+    }
+  }
+  if (!loss) return;
+  __syncthreads();
+  if (!sh_last) return;
+  double sum = 0.0;
+  for (int i = tid; i < int(gridDim.x); i += kBalFinThreads)
+    sum += __builtin_bit_cast(double, __hip_atomic_load(reinterpret_cast<unsigned long long*>(part + i),
+                                                        __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_AGENT));
+  sh_p[way][col] = sum;
+  __syncthreads();
+  if (tid == 0) {
+    double all = 0.0;
+    for (int i = 0; i < kBalFinThreads; ++i) all += sh_p[i >> 4][i & 15];
+    *loss = float(all);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward: one read of the scores, one write of the gradient.  The K gate
+// terms of a row go through a small LDS table (E floats a row, zero between
+// rows) that the row's lanes read in their own layout.
+template <int E>
+__global__ __launch_bounds__(kBalThreads) void k_balance_bwd(
+    const float* __restrict__ s, const int32_t* __restrict__ topk, int N, int K, const int32_t* __restrict__ seq_off,
+    int B, const uint8_t* __restrict__ valid, const float* __restrict__ weight, const float* __restrict__ dloss,
+    const float* __restrict__ dgate, float* __restrict__ dlogits) {
+  using S = BalShape<E>;
+  constexpr int LPR = S::LPR, F4 = S::F4, RPW = S::RPW, R = S::R, KU = 16 / LPR;
+  __shared__ __align__(16) float add[kBalWaves][RPW][E];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int rho = lane / LPR, ql = lane % LPR;
+  float* mine = add[wave][rho];
+#pragma unroll
+  for (int t = 0; t < F4; ++t)
+    *reinterpret_cast<float4*>(mine + 4 * (LPR * t + ql)) = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float dl = weight ? (dloss ? *dloss : 1.0f) : 0.f;
+  for (int64_t rb = int64_t(blockIdx.x) * R; rb < N; rb += int64_t(gridDim.x) * R) {
+    if (rb + wave * RPW >= N) break;
+    const int64_t row = rb + wave * RPW + rho;
+    const bool here = row < N;
+    const int64_t lr = here ? row : N - 1;
+    const float* src = s + lr * E;
+    float4 x[F4];
+#pragma unroll
+    for (int t = 0; t < F4; ++t) x[t] = ld4(src + 4 * (LPR * t + ql));
+    bool lv = !valid || valid[lr] != 0;
+    int q = 0;
+    if (seq_off) {
+      q = bal_find(seq_off, B, int(lr));
+      lv = lv && q < B && lr >= seq_off[0];
+      q = q < B ? q : B - 1;
+    }
+    int id[KU];
+    if (dgate) {
+      float sv[KU], dg[KU], total = 0.f, inner = 0.f;
+#pragma unroll
+      for (int u = 0; u < KU; ++u) {
+        const int k = ql + u * LPR;
+        id[u] = k < K ? topk[lr * K + k] : -1;
+        const bool on = lv && unsigned(id[u]) < unsigned(E);
+        id[u] = on ? id[u] : -1;
+        sv[u] = on ? src[id[u]] : 0.f;
+        dg[u] = on ? dgate[lr * K + k] : 0.f;
+        total += sv[u];
+        inner = fmaf(dg[u], sv[u], inner);
+      }
+      total = bal_row_sum<LPR>(total);
+      inner = bal_row_sum<LPR>(inner);
+      const float per = total > 0.f ? 1.0f / total : 0.f;
+      inner *= per;
+#pragma unroll
+      for (int u = 0; u < KU; ++u)
+        if (id[u] >= 0) mine[id[u]] = (dg[u] - inner) * per;
+    }
+    __builtin_amdgcn_wave_barrier();
+    asm volatile("" ::: "memory");
+    float z = 0.f, dot = 0.f;
+    float4 w[F4];
+    if (weight) {
+      const float* wr = weight + int64_t(q) * E;
+#pragma unroll
+      for (int t = 0; t < F4; ++t) {
+        w[t] = ld4(wr + 4 * (LPR * t + ql));
+        z += (x[t].x + x[t].y) + (x[t].z + x[t].w);
+        dot = fmaf(w[t].x, x[t].x, dot);
+        dot = fmaf(w[t].y, x[t].y, dot);
+        dot = fmaf(w[t].z, x[t].z, dot);
+        dot = fmaf(w[t].w, x[t].w, dot);
+      }
+      z = bal_row_sum<LPR>(z);
+      dot = bal_row_sum<LPR>(dot);
+    } else {
+#pragma unroll
+      for (int t = 0; t < F4; ++t) w[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const float inv = lv && z > 0.f ? 1.0f / z : 0.f;
+    const float mean = dot * inv, scale = dl * inv;
+#pragma unroll
+    for (int t = 0; t < F4; ++t) {
+      float4 g = dgate ? *reinterpret_cast<const float4*>(mine + 4 * (LPR * t + ql)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 o;
+      o.x = fmaf(w[t].x - mean, scale, g.x) * (x[t].x * (1.0f - x[t].x));
+      o.y = fmaf(w[t].y - mean, scale, g.y) * (x[t].y * (1.0f - x[t].y));
+      o.z = fmaf(w[t].z - mean, scale, g.z) * (x[t].z * (1.0f - x[t].z));
+      o.w = fmaf(w[t].w - mean, scale, g.w) * (x[t].w * (1.0f - x[t].w));
+      if (!lv) o = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (here) *reinterpret_cast<float4*>(dlogits + row * E + 4 * (LPR * t + ql)) = o;
+    }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+    if (dgate) {
+#pragma unroll
+      for (int u = 0; u < KU; ++u)
+        if (id[u] >= 0) mine[id[u]] = 0.f;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+
+template <int E, int P>
+static int fwd_ep(const BalFwd& a, const BalWs& w, hipStream_t st) {
+  const dim3 grid{unsigned(w.chunks), 1u, 1u}, block{unsigned(kBalThreads), 1u, 1u};
+  uint8_t* ws = a.ws;
+  if (ws)
+    hipLaunchKernelGGL((k_balance_fwd<E, P, true>), grid, block, 0, st, a.s, a.b, int(a.N), a.K, a.seq_off, a.B,
+                       a.valid, w.T, a.topk, a.gate, reinterpret_cast<float*>(ws + w.psum),
+                       reinterpret_cast<int32_t*>(ws + w.cnt), reinterpret_cast<int32_t*>(ws + w.live),
+                       reinterpret_cast<uint32_t*>(ws));
+  else
+    hipLaunchKernelGGL((k_balance_fwd<E, P, false>), grid, block, 0, st, a.s, a.b, int(a.N), a.K, a.seq_off, a.B,
+                       a.valid, w.T, a.topk, a.gate, nullptr, nullptr, nullptr, nullptr);
+  return int(hipGetLastError());
+}
+
+template <int E>
+static int fwd_e(const BalFwd& a, const BalWs& w, hipStream_t st) {
+  // lists of the next of 4, 8 and 16 slots at or above K
+  if (a.K <= 4) return fwd_ep<E, 4>(a, w, st);
+  if (a.K <= 8) return fwd_ep<E, 8>(a, w, st);
+  return fwd_ep<E, 16>(a, w, st);
+}
+
+int launch_balance_fwd(const BalFwd& a, hipStream_t st) {
+  const BalWs w = balance_ws_layout(a.N, a.E, a.B);
+  int rc = int(hipErrorInvalidValue);
+  switch (a.E) {
+    case 16: rc = fwd_e<16>(a, w, st); break;
+    case 32: rc = fwd_e<32>(a, w, st); break;
+    case 64: rc = fwd_e<64>(a, w, st); break;
+    case 128: rc = fwd_e<128>(a, w, st); break;
+    case 256: rc = fwd_e<256>(a, w, st); break;
+  }
+  if (rc != int(hipSuccess) || !a.ws) return rc;
+  uint8_t* ws = a.ws;
+  hipLaunchKernelGGL(k_balance_fin, dim3(unsigned(w.groups)), dim3(kBalFinThreads), 0, st, a.seq_off, a.B, int(a.N),
+                     a.E, a.K, w.T, a.coef, reinterpret_cast<const float*>(ws + w.psum),
+                     reinterpret_cast<const int32_t*>(ws + w.cnt), reinterpret_cast<const int32_t*>(ws + w.live),
+                     reinterpret_cast<double*>(ws + w.part), reinterpret_cast<uint32_t*>(ws), a.count, a.weight,
+                     a.loss);
+  return int(hipGetLastError());
+}
+
+template <int E>
+static int bwd_e(const BalBwd& a, hipStream_t st) {
+  constexpr int R = BalShape<E>::R;
+  const int64_t steps = (a.N + R - 1) / R;
+  const int64_t most = int64_t(device_cu_count()) * 4;  // workgroups that run at once; more rows are further trips
+  const dim3 grid{unsigned(std::min(steps, most)), 1u, 1u}, block{unsigned(kBalThreads), 1u, 1u};
+  hipLaunchKernelGGL((k_balance_bwd<E>), grid, block, 0, st, a.s, a.topk, int(a.N), a.K, a.seq_off, a.B, a.valid,
+                     a.weight, a.dloss, a.dgate, a.dlogits);
+  return int(hipGetLastError());
+}
+
+int launch_balance_bwd(const BalBwd& a, hipStream_t st) {
+  switch (a.E) {
+    case 16: return bwd_e<16>(a, st);
+    case 32: return bwd_e<32>(a, st);
+    case 64: return bwd_e<64>(a, st);
+    case 128: return bwd_e<128>(a, st);
+    case 256: return bwd_e<256>(a, st);
+  }
+  return int(hipErrorInvalidValue);
+}
+
+}  // namespace qbk

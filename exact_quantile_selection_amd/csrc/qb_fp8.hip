@@ -1,0 +1,855 @@
+// qb_fp8.hip -- matrix products in 8-bit floating point (e4m3) with a
+// power-of-two scale for each block of 128, for one weight matrix and for one
+// matrix per expert.
+//
+// Quantising a row: for each 128 consecutive values the least whole e >= -126
+// with max|x| <= 448 * 2^e, stored as e + 127 in 8 bits; the values are
+// x 2^-e (exact) rounded to nearest even.  2^e is the matrix instruction's
+// own scale operand (v_mfma_scale_f32_16x16x128_f8f6f4 multiplies 32 values
+// of each operand's row by one such byte), so a scale costs no arithmetic:
+// one instruction's 128 values of K are one block, and all four lanes of a
+// row hold its byte.  Sums are held in 32 bits and rounded once on the way
+// out.
+//
+//   product:      y[m][n]  = sum_c x[m][c] w_e[n][c]          (e: m's expert)
+//   weight grad:  dw_e[n][c] = sum_{m of e} dy[m][n] x[m][c]
+// both as out[a][b] = sum_k A[a][k] B[b][k] of two K-contiguous operands (the
+// gradient's operands are quantised along the rows, so that their blocks lie
+// along its sum).
+//
+// Operand layout of the instruction (checked on the GPU): lane l supplies 32
+// of the 128 values of row l % 16 of either operand, the same ones of both;
+// which 32 is free as long as A and B agree.  Result element i of lane l is
+// C[row 4 (l / 16) + i of the first operand][row l % 16 of the second].
+//
+// How exactly it adds (measured with single values, on the GPU): the eight
+// products of a group are aligned to the largest of them and what lies more
+// than 2^-13 below it is dropped; groups, and the running sum, are added in 32
+// bits.  All 8-bit matrix instructions of this GPU do so, the 16-bit ones do
+// not.  So there are two ways to multiply, with the same tiles:
+//   * the 8-bit instruction: up to 2^-10 of sum |a b|, unseen beside a bf16
+//     result's own 2^-8 unless the sum cancels.  The product's default.
+//   * EXACT: both operands widened in registers to bf16 (e4m3 times its
+//     scale is exact there), whose instruction adds products in full: every
+//     sum in 32 bits, half the peak rate.  The weight gradient, whose result
+//     keeps 32 bits, and the products of few rows, where the weight's bytes
+//     cost more than either instruction, always use it.
+#include <algorithm>
+
+#include "qb_device.hpp"
+#include "qb_internal.hpp"
+
+namespace qbk {
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void* lds_vptr;
+typedef __attribute__((address_space(1))) void* glb_vptr;
+
+struct __attribute__((packed, aligned(2))) Half8 {
+  uint32_t v[4];
+};
+struct __attribute__((packed, aligned(2))) Half4 {
+  uint32_t v[2];
+};
+struct __attribute__((packed, aligned(4))) Float4 {
+  float v[4];
+};
+
+// ---------------------------------------------------------------------------
+// quantising
+
+// 8 bf16 of a row from p, of which n lie inside it; the others are zero.
+__device__ __forceinline__ void ld_half8(const uint16_t* p, int n, uint32_t (&v)[4]) {
+  if (n >= 8) {
+    const Half8 t = *reinterpret_cast<const Half8*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = t.v[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = 2 * i < n ? p[2 * i] : 0, hi = 2 * i + 1 < n ? p[2 * i + 1] : 0;
+      v[i] = lo | (hi << 16);
+    }
+  }
+}
+
+// The exponent byte of a block whose largest |x| has the bf16 pattern `top`
+// (sign cleared; patterns order as values do, NaN above infinity).
+__device__ __forceinline__ int scale_byte(uint32_t top) {
+  // 448 = 1.75 * 2^8: one more power when the fraction is above 0.75
+  const int e = int(top >> 7) - 127 - 8 + ((top & 0x7Fu) > 0x60u ? 1 : 0);
+  return (e < -126 ? -126 : e) + 127;
+}
+// 2^-e of such a byte; e <= 120 for finite blocks, so it is a normal float.
+__device__ __forceinline__ float scale_down(int byte) {
+  return __builtin_bit_cast(float, uint32_t(254 - byte) << 23);
+}
+__device__ __forceinline__ float half_lo(uint32_t p) { return __builtin_bit_cast(float, p << 16); }
+__device__ __forceinline__ float half_hi(uint32_t p) { return __builtin_bit_cast(float, p & 0xFFFF0000u); }
+
+// Four values to e4m3 bytes (nearest even).  bad: the block holds a NaN or an
+// infinity; those values become NaN, as a cast of them does.
+__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d, bool bad) {
+  int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+  if (bad) {
+    uint32_t u = uint32_t(r);
+    const float inf = __builtin_inff();
+    if (!(fabsf(a) < inf)) u = (u & ~0xFFu) | 0x7Fu;
+    if (!(fabsf(b) < inf)) u = (u & ~0xFF00u) | 0x7F00u;
+    if (!(fabsf(c) < inf)) u = (u & ~0xFF0000u) | 0x7F0000u;
+    if (!(fabsf(d) < inf)) u = (u & ~0xFF000000u) | 0x7F000000u;
+    return u;
+  }
+  return uint32_t(r);
+}
+
+__device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t p) {
+  const uint32_t lo = p & 0x7FFFu, hi = (p >> 16) & 0x7FFFu;
+  m = m > lo ? m : lo;
+  return m > hi ? m : hi;
+}
+
+// Along the rows: a wave takes 512 columns (one word of four scales) of U
+// rows, 16 lanes a block.  Bound by its 2 bytes in, 1 byte out a value.
+template <int U>
+__global__ __launch_bounds__(256) void k_fp8_quantize(const uint16_t* __restrict__ x, int64_t Mx,
+                                                      const int32_t* __restrict__ row_src, int64_t M, int C,
+                                                      uint8_t* __restrict__ xq, uint8_t* __restrict__ xs) {
+  const int lane = threadIdx.x & 63;
+  const int chunks = int(gridDim.y);
+  const int64_t r0 = (int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6)) * U;
+  const int c0 = int(blockIdx.y) * 512 + lane * 8;
+  const int64_t ld = (int64_t(C) + kQBlock - 1) / kQBlock * kQBlock;
+  uint32_t v[U][4];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t r = r0 + u;
+    int64_t src = r < M ? r : -1;
+    if (row_src && src >= 0) {
+      src = row_src[r];
+      if (src >= Mx) src = -1;
+    }
+    if (src >= 0 && c0 < C) {
+      ld_half8(x + src * C + c0, C - c0, v[u]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[u][i] = 0;
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t r = r0 + u;
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = abs_max2(top, v[u][i]);
+    auto join = [&](int o) { top = top > uint32_t(o) ? top : uint32_t(o); };
+    join(__builtin_amdgcn_mov_dpp(int(top), kQuadXor1, 0xF, 0xF, true));
+    join(__builtin_amdgcn_mov_dpp(int(top), kQuadXor2, 0xF, 0xF, true));
+    join(__builtin_amdgcn_mov_dpp(int(top), kHalfMirror, 0xF, 0xF, true));
+    join(__builtin_amdgcn_mov_dpp(int(top), 0x140, 0xF, 0xF, true));  // row_mirror: lane i of 16 reads lane 15 - i
+    const int byte = scale_byte(top);
+    const float f = scale_down(byte);
+    const bool bad = top >= 0x7F80u;
+    if (r < M) {
+      if (c0 < ld) {
+        uint2 o;
+        o.x = to_e4m3x4(half_lo(v[u][0]) * f, half_hi(v[u][0]) * f, half_lo(v[u][1]) * f, half_hi(v[u][1]) * f, bad);
+        o.y = to_e4m3x4(half_lo(v[u][2]) * f, half_hi(v[u][2]) * f, half_lo(v[u][3]) * f, half_hi(v[u][3]) * f, bad);
+        *reinterpret_cast<uint2*>(xq + r * ld + c0) = o;
+      }
+      if ((lane & 15) == 0) xs[r * (int64_t(chunks) * 4) + int(blockIdx.y) * 4 + (lane >> 4)] = uint8_t(byte);
+    }
+  }
+}
+
+// Along the columns: a workgroup takes 128 rows (one block) of 64 columns and
+// writes them transposed, 128 contiguous bytes a column.  A thread holds 8
+// columns of 4 consecutive rows, so that a column's 4 bytes are one word; the
+// words cross to the columns' order through LDS (33 words a column: the 64
+// lanes of a store lie in 64 banks).
+__global__ __launch_bounds__(256) void k_fp8_quantize_cols(const uint16_t* __restrict__ x, int64_t Mx,
+                                                           const int32_t* __restrict__ row_src, int64_t M, int C,
+                                                           int64_t ld, int64_t sld, uint8_t* __restrict__ xt,
+                                                           uint8_t* __restrict__ xts) {
+  __shared__ uint32_t tops[4][64];
+  __shared__ uint32_t words[64 * 33];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int cg = tid & 7, rg = tid >> 3;
+  const int64_t blk = int64_t(blockIdx.y);
+  const int64_t r0 = blk * kQBlock + rg * 4;
+  const int cbase = int(blockIdx.x) * 64, c0 = cbase + cg * 8;
+  uint32_t v[4][4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int64_t r = r0 + u;
+    int64_t src = r < M ? r : -1;
+    if (row_src && src >= 0) {
+      src = row_src[r];
+      if (src >= Mx) src = -1;
+    }
+    if (src >= 0 && c0 < C) {
+      ld_half8(x + src * C + c0, C - c0, v[u]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[u][i] = 0;
+    }
+  }
+  uint32_t top[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    top[2 * i] = top[2 * i + 1] = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t lo = v[u][i] & 0x7FFFu, hi = (v[u][i] >> 16) & 0x7FFFu;
+      top[2 * i] = top[2 * i] > lo ? top[2 * i] : lo;
+      top[2 * i + 1] = top[2 * i + 1] > hi ? top[2 * i + 1] : hi;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+#pragma unroll
+    for (int d = 8; d < kWave; d <<= 1) {
+      const uint32_t o = __shfl_xor(top[j], d);
+      top[j] = top[j] > o ? top[j] : o;
+    }
+    if (lane < 8) tops[wave][cg * 8 + j] = top[j];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    uint32_t t = tops[0][cg * 8 + j];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) t = t > tops[w][cg * 8 + j] ? t : tops[w][cg * 8 + j];
+    const int byte = scale_byte(t);
+    const float f = scale_down(byte);
+    float a[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) a[u] = ((j & 1) ? half_hi(v[u][j >> 1]) : half_lo(v[u][j >> 1])) * f;
+    words[(cg * 8 + j) * 33 + rg] = to_e4m3x4(a[0], a[1], a[2], a[3], t >= 0x7F80u);
+    if (rg == 0 && c0 + j < C) xts[(c0 + j) * sld + blk] = uint8_t(byte);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = h * 256 + tid, col = i >> 3, part = i & 7;
+    if (cbase + col < C) {
+      uint4 o;
+      const uint32_t* src = words + col * 33 + part * 4;
+      o.x = src[0], o.y = src[1], o.z = src[2], o.w = src[3];
+      *reinterpret_cast<uint4*>(xt + int64_t(cbase + col) * ld + blk * kQBlock + part * 16) = o;
+    }
+  }
+}
+
+int launch_fp8_quantize(const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M, int C, uint8_t* xq,
+                        uint8_t* xs, hipStream_t st) {
+  const unsigned chunks = unsigned(fp8_sld(C) / 4);
+  // four rows a wave once that still gives every CU its waves
+  if (M * chunks >= 16 * 1024)
+    hipLaunchKernelGGL((k_fp8_quantize<4>), dim3(unsigned((M + 15) / 16), chunks), dim3(256), 0, st, x, Mx, row_src,
+                       M, C, xq, xs);
+  else
+    hipLaunchKernelGGL((k_fp8_quantize<1>), dim3(unsigned((M + 3) / 4), chunks), dim3(256), 0, st, x, Mx, row_src, M,
+                       C, xq, xs);
+  return int(hipGetLastError());
+}
+
+int launch_fp8_quantize_cols(const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M, int C, uint8_t* xt,
+                             uint8_t* xts, hipStream_t st) {
+  const int64_t ld = fp8_ld(M);
+  hipLaunchKernelGGL(k_fp8_quantize_cols, dim3(unsigned((C + 63) / 64), unsigned(ld / kQBlock)), dim3(256), 0, st, x,
+                     Mx, row_src, M, C, ld, fp8_sld(M), xt, xts);
+  return int(hipGetLastError());
+}
+
+// A weight stack: a workgroup takes one 128 x 128 block of one matrix, in both
+// orders.  A thread holds 4 rows of 16 columns; both layouts leave through the
+// same LDS bytes (rows of 132, so that the reads of a column spread over the
+// banks).
+__global__ __launch_bounds__(256) void k_fp8_quantize_weight(const float* __restrict__ w, int N, int C,
+                                                             uint8_t* __restrict__ wq, uint8_t* __restrict__ ws,
+                                                             uint8_t* __restrict__ wt, uint8_t* __restrict__ wts) {
+  __shared__ uint32_t tops[4];
+  __shared__ uint32_t words[kQBlock * 33];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int cb = int(blockIdx.x), nb = int(blockIdx.y);
+  const int64_t g = blockIdx.z;
+  const int64_t ldc = (int64_t(C) + kQBlock - 1) / kQBlock * kQBlock, ldn = (int64_t(N) + kQBlock - 1) / kQBlock * kQBlock;
+  const int64_t sldc = (ldc / kQBlock + 3) / 4 * 4, sldn = (ldn / kQBlock + 3) / 4 * 4;
+  const int cg = tid & 31, rg = tid >> 5;  // 4 columns from 4 cg, rows rg + 8 u
+  const int c0 = cb * kQBlock + cg * 4;
+  float v[16][4];
+  uint32_t top = 0;
+#pragma unroll
+  for (int u = 0; u < 16; ++u) {
+    const int n = nb * kQBlock + rg + 8 * u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[u][i] = n < N && c0 + i < C ? w[(g * N + n) * C + c0 + i] : 0.f;
+      const uint32_t a = __builtin_bit_cast(uint32_t, v[u][i]) & 0x7FFFFFFFu;
+      top = top > a ? top : a;
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const uint32_t o = __shfl_xor(top, d);
+    top = top > o ? top : o;
+  }
+  if (lane == 0) tops[wave] = top;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) top = top > tops[k] ? top : tops[k];
+  // 448 = 1.75 * 2^8: one more power when the fraction is above 0.75
+  int e = int(top >> 23) - 127 - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  e = e < -126 ? -126 : e;
+  const float f = scale_down(e + 127);
+  const bool bad = top >= 0x7F800000u;
+#pragma unroll
+  for (int u = 0; u < 16; ++u) {
+    const int row = rg + 8 * u;
+    words[row * 33 + cg] = to_e4m3x4(v[u][0] * f, v[u][1] * f, v[u][2] * f, v[u][3] * f, bad);
+  }
+  __syncthreads();
+  // 128 rows of eight 16-byte parts
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    const int i = h * 256 + tid, row = i >> 3, part = i & 7, n = nb * kQBlock + row;
+    if (n < N) {
+      const uint32_t* src = words + row * 33 + part * 4;
+      uint4 o;
+      o.x = src[0], o.y = src[1], o.z = src[2], o.w = src[3];
+      *reinterpret_cast<uint4*>(wq + (g * N + n) * ldc + cb * kQBlock + part * 16) = o;
+    }
+  }
+  if (tid == 0) ws[(g * (ldn / kQBlock) + nb) * sldc + cb] = uint8_t(e + 127);
+  if (wt) {
+    const uint8_t* bytes = reinterpret_cast<const uint8_t*>(words);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const int i = h * 256 + tid, col = i & 127, part = i >> 7, c = cb * kQBlock + col;
+      if (c < C) {
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          o[k] = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[k] |= uint32_t(bytes[(part * 16 + k * 4 + j) * 132 + col]) << (8 * j);
+        }
+        *reinterpret_cast<uint4*>(wt + (g * C + c) * ldn + nb * kQBlock + part * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+    if (tid == 0) wts[(g * (ldc / kQBlock) + cb) * sldn + nb] = uint8_t(e + 127);
+  }
+}
+
+int launch_fp8_quantize_weight(const float* w, int G, int N, int C, uint8_t* wq, uint8_t* ws, uint8_t* wt,
+                               uint8_t* wts, hipStream_t st) {
+  const dim3 grid{unsigned(fp8_ld(C) / kQBlock), unsigned(fp8_ld(N) / kQBlock), unsigned(G)};
+  hipLaunchKernelGGL(k_fp8_quantize_weight, grid, dim3(256), 0, st, w, N, C, wq, ws, wt, wts);
+  return int(hipGetLastError());
+}
+
+// Eight e4m3 bytes times a scale as bf16, exactly.
+__device__ __forceinline__ bf16x8 widen(int lo, int hi, float scale) {
+  const auto a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+  const auto b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+  const auto c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+  const auto d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+  return (bf16x8){a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+// 2^(byte - 127) of a scale byte.
+__device__ __forceinline__ float scale_value(int byte) { return __builtin_bit_cast(float, uint32_t(byte) << 23); }
+
+// ---------------------------------------------------------------------------
+// which expert a tile of rows belongs to
+
+struct Tile {
+  int e;            // expert, -1: none
+  int64_t lo, hi;   // its rows
+  int at;           // the tile's number inside it
+};
+
+// The wave finds tile t of the list of all experts' tiles of BM rows (four
+// experts a lane); total: the list's length.  Offsets outside [0, M] or out
+// of order are clamped, so any `off` stays inside the arrays.
+__device__ __forceinline__ int group_tiles(const int32_t* off, int G, int64_t M, int BM, int lane, int (&lo)[4],
+                                           int (&hi)[4], int (&n)[4], int& before) {
+  int sum = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int e = 4 * lane + j;
+    int a = e < G ? off[e] : 0, b = e < G ? off[e + 1] : 0;
+    a = a < 0 ? 0 : (a > M ? int(M) : a);
+    b = b < a ? a : (b > M ? int(M) : b);
+    lo[j] = a;
+    hi[j] = b;
+    n[j] = (b - a + BM - 1) / BM;
+    sum += n[j];
+  }
+  int run = sum;
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const int o = __shfl_up(run, d);
+    run += lane >= d ? o : 0;
+  }
+  before = run - sum;
+  return __shfl(run, kWave - 1);
+}
+__device__ __forceinline__ Tile group_find(int t, int lane, const int (&lo)[4], const int (&hi)[4], const int (&n)[4],
+                                           int before) {
+  int e = -1, at = 0, a = 0, b = 0, run = before;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (t >= run && t < run + n[j]) {
+      e = 4 * lane + j;
+      at = t - run;
+      a = lo[j];
+      b = hi[j];
+    }
+    run += n[j];
+  }
+  const uint64_t m = __ballot(e >= 0);
+  Tile r;
+  if (m == 0) {
+    r.e = -1;
+    r.lo = r.hi = 0;
+    r.at = 0;
+    return r;
+  }
+  const int from = __builtin_ctzll(m);
+  r.e = __builtin_amdgcn_readlane(e, from);
+  r.at = __builtin_amdgcn_readlane(at, from);
+  r.lo = __builtin_amdgcn_readlane(a, from);
+  r.hi = __builtin_amdgcn_readlane(b, from);
+  return r;
+}
+
+// Workgroups are dealt out to the 8 XCDs in turn; each XCD takes a
+// consecutive stretch of the tiles, so the tiles in flight on one L2 share
+// rows.  A permutation of [0, n).
+__device__ __forceinline__ int xcd_tile(int b, int n) {
+  const int per = n / 8, more = n % 8, x = b % 8, i = b / 8;
+  return x * per + (x < more ? x : more) + i;
+}
+
+// Tiles in groups of GM rows of tiles, column by column inside a group.
+__device__ __forceinline__ void tile_order(int t, int tm_all, int tn_all, int GM, int& tm, int& tn) {
+  const int g = t / (GM * tn_all), r = t % (GM * tn_all);
+  const int rows = tm_all - g * GM < GM ? tm_all - g * GM : GM;
+  tm = g * GM + r % rows;
+  tn = r / rows;
+}
+
+// ---------------------------------------------------------------------------
+// the tiled product
+
+// A workgroup computes BM x BN of the result from an LDS ring of two stages
+// of 128 bytes of K, filled by loads that go to LDS directly; the waves tile
+// it WM x WN.  A row's 128 bytes are 8 slots of 16, XORed with (row / 2) mod
+// 8, so 16 lanes reading one slot number of 16 rows touch all banks once.
+// The scales of four blocks of K are one word a row, staged beside the tiles.
+// GRAD: the weight gradient (float out, K = an expert's rows, every expert's
+// output is written); else the product (bf16 out, an expert's rows tiled).
+template <int BM, int BN, int WM, int WN, bool GRAD, bool EXACT>
+__global__ __launch_bounds__(WM* WN* kWave) void k_fp8_gemm(const uint8_t* __restrict__ A,
+                                                            const uint8_t* __restrict__ As,
+                                                            const uint8_t* __restrict__ Bm,
+                                                            const uint8_t* __restrict__ Bs, int64_t M, int N,
+                                                            int64_t ldk, int64_t sld, const int32_t* __restrict__ off,
+                                                            int G, void* __restrict__ outp) {
+  constexpr int W = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
+  constexpr int A_BYTES = BM * kQBlock, B_BYTES = BN * kQBlock;
+  constexpr int A_PW = A_BYTES / 1024 / W, B_PW = B_BYTES / 1024 / W;  // 1 KiB loads per wave and stage
+  constexpr int ROWS = BM + BN;
+  static_assert(A_PW * W * 1024 == A_BYTES && B_PW * W * 1024 == B_BYTES, "tile split");
+  __shared__ __align__(1024) uint8_t lds[2 * (A_BYTES + B_BYTES) + 2 * ROWS * 4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int tn_all = (N + BN - 1) / BN;
+
+  // this workgroup's tile: rows [m0, m_end) of A and of the result, rows
+  // n0... of B, blocks [k0, k1) of K
+  int64_t m0, m_end;
+  int n0, k0 = 0, k1 = int(ldk / kQBlock);
+  int64_t out_row = 0;  // what the result's row number is counted from
+  if constexpr (GRAD) {
+    const int tm_all = int((M + BM - 1) / BM), per = tm_all * tn_all;
+    const int t = xcd_tile(int(blockIdx.x), int(gridDim.x));
+    const int e = t / per;
+    int tm, tn;
+    tile_order(t % per, tm_all, tn_all, 8, tm, tn);
+    if (off) {
+      int a = off[e] / kQBlock, b = off[e + 1] / kQBlock;
+      a = a < 0 ? 0 : (a > k1 ? k1 : a);
+      b = b < a ? a : (b > k1 ? k1 : b);
+      k0 = a;
+      k1 = b;
+    }
+    m0 = int64_t(tm) * BM;
+    m_end = M;
+    n0 = tn * BN;
+    out_row = int64_t(e) * M;
+  } else if (off) {
+    int lo[4], hi[4], n[4], before;
+    const int total = group_tiles(off, G, M, BM, lane, lo, hi, n, before);
+    if (int(blockIdx.x) >= total * tn_all) return;
+    const int t = xcd_tile(int(blockIdx.x), total * tn_all);
+    int tm, tn;
+    tile_order(t, total, tn_all, 8, tm, tn);
+    const Tile g = group_find(tm, lane, lo, hi, n, before);
+    if (g.e < 0) return;
+    m0 = g.lo + int64_t(g.at) * BM;
+    m_end = g.hi;
+    n0 = tn * BN;
+    Bm += int64_t(g.e) * N * ldk;
+    Bs += int64_t(g.e) * ((N + kQBlock - 1) / kQBlock) * sld;
+  } else {
+    const int tm_all = int((M + BM - 1) / BM);
+    const int t = xcd_tile(int(blockIdx.x), int(gridDim.x));
+    int tm, tn;
+    tile_order(t, tm_all, tn_all, 8, tm, tn);
+    m0 = int64_t(tm) * BM;
+    m_end = M;
+    n0 = tn * BN;
+  }
+
+  // per-lane sources: rows past the end re-read the last one
+  const uint8_t* a_base = A + m0 * ldk;
+  const uint8_t* b_base = Bm + int64_t(n0) * ldk;
+  uint32_t a_off[A_PW], b_off[B_PW];
+#pragma unroll
+  for (int j = 0; j < A_PW; ++j) {
+    const int p = (wave * A_PW + j) * kWave + lane, q = p ^ ((p >> 4) & 7);
+    int row = q >> 3;
+    row = m0 + row < m_end ? row : int(m_end - 1 - m0);
+    a_off[j] = uint32_t(row) * uint32_t(ldk) + (q & 7) * 16;
+  }
+#pragma unroll
+  for (int j = 0; j < B_PW; ++j) {
+    const int p = (wave * B_PW + j) * kWave + lane, q = p ^ ((p >> 4) & 7);
+    int row = q >> 3;
+    row = n0 + row < N ? row : N - 1 - n0;
+    b_off[j] = uint32_t(row) * uint32_t(ldk) + (q & 7) * 16;
+  }
+  // scales: ROWS words, 64 a load
+  constexpr int S_PW = (ROWS / kWave + W - 1) / W;
+  const uint8_t* s_src[S_PW];
+#pragma unroll
+  for (int j = 0; j < S_PW; ++j) {
+    const int i = (wave * S_PW + j) * kWave + lane;
+    if (i < BM) {
+      int64_t row = m0 + i;
+      row = row < m_end ? row : m_end - 1;
+      s_src[j] = As + row * sld;
+    } else {
+      int row = n0 + (i - BM);
+      row = row < N ? row : N - 1;
+      s_src[j] = Bs + int64_t(GRAD ? row : row / kQBlock) * sld;
+    }
+  }
+  uint8_t* lds_s = lds + 2 * (A_BYTES + B_BYTES);
+  auto issue = [&](int kb, bool first) {
+    const int st = kb & 1;
+    const int64_t ko = int64_t(kb) * kQBlock;
+    uint8_t* sa = lds + st * A_BYTES;
+    uint8_t* sb = lds + 2 * A_BYTES + st * B_BYTES;
+    const uint8_t* ak = a_base + ko;
+    const uint8_t* bk = b_base + ko;
+#pragma unroll
+    for (int j = 0; j < A_PW; ++j)
+      __builtin_amdgcn_global_load_lds((glb_vptr)(ak + a_off[j]), (lds_vptr)(sa + (wave * A_PW + j) * 1024), 16, 0, 0);
+#pragma unroll
+    for (int j = 0; j < B_PW; ++j)
+      __builtin_amdgcn_global_load_lds((glb_vptr)(bk + b_off[j]), (lds_vptr)(sb + (wave * B_PW + j) * 1024), 16, 0, 0);
+    if (first || (kb & 3) == 0) {
+      uint8_t* ss = lds_s + ((kb >> 2) & 1) * (ROWS * 4);
+#pragma unroll
+      for (int j = 0; j < S_PW; ++j)
+        if ((wave * S_PW + j) * kWave < ROWS)
+          __builtin_amdgcn_global_load_lds((glb_vptr)(s_src[j] + (kb & ~3)), (lds_vptr)(ss + (wave * S_PW + j) * 256),
+                                           4, 0, 0);
+    }
+  };
+
+  v4f acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+
+  const int r = lane & 15, g4 = lane >> 4;
+  const int frag = r * kQBlock + ((g4 ^ ((r >> 1) & 7)) * 16), frag4 = frag ^ 64;  // slots g4 and g4 + 4
+  if (k0 < k1) issue(k0, true);
+  for (int kb = k0; kb < k1; ++kb) {
+    // the tile's loads are the only ones in flight; the barrier publishes
+    // every wave's and retires all reads of the stage that is filled next
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (kb + 1 < k1) issue(kb + 1, false);
+    const uint8_t* sa = lds + (kb & 1) * A_BYTES + wm * (TM * 16) * kQBlock;
+    const uint8_t* sb = lds + 2 * A_BYTES + (kb & 1) * B_BYTES + wn * (TN * 16) * kQBlock;
+    const uint8_t* ss = lds_s + ((kb >> 2) & 1) * (ROWS * 4) + (kb & 3);
+    if constexpr (!EXACT) {
+      v8i b[TN];
+      int bs[TN];
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const v4i lo = *reinterpret_cast<const v4i*>(sb + j * 16 * kQBlock + frag);
+        const v4i hi = *reinterpret_cast<const v4i*>(sb + j * 16 * kQBlock + frag4);
+        b[j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        bs[j] = ss[(BM + (wn * TN + j) * 16 + r) * 4];
+      }
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const v4i lo = *reinterpret_cast<const v4i*>(sa + i * 16 * kQBlock + frag);
+        const v4i hi = *reinterpret_cast<const v4i*>(sa + i * 16 * kQBlock + frag4);
+        const v8i a = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        const int as = ss[((wm * TM + i) * 16 + r) * 4];
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j], a, acc[i][j], 0, 0, 0, bs[j], 0, as);
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at = h ? frag4 : frag;
+        bf16x8 b[TN][2];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          const v4i t = *reinterpret_cast<const v4i*>(sb + j * 16 * kQBlock + at);
+          const float f = scale_value(ss[(BM + (wn * TN + j) * 16 + r) * 4]);
+          b[j][0] = widen(t[0], t[1], f);
+          b[j][1] = widen(t[2], t[3], f);
+        }
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          const v4i t = *reinterpret_cast<const v4i*>(sa + i * 16 * kQBlock + at);
+          const float f = scale_value(ss[((wm * TM + i) * 16 + r) * 4]);
+          const bf16x8 a0 = widen(t[0], t[1], f), a1 = widen(t[2], t[3], f);
+#pragma unroll
+          for (int j = 0; j < TN; ++j) {
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j][0], a0, acc[i][j], 0, 0, 0);
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j][1], a1, acc[i][j], 0, 0, 0);
+          }
+        }
+      }
+    }
+  }
+
+  // element c of acc[i][j]: row 16 i + l % 16, column 16 j + 4 (l / 16) + c
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int64_t row = m0 + (wm * TM + i) * 16 + r;
+    if (row >= m_end) continue;
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const int col = n0 + (wn * TN + j) * 16 + g4 * 4;
+      const v4f v = acc[i][j];
+      if constexpr (GRAD) {
+        float* o = static_cast<float*>(outp) + (out_row + row) * N + col;
+        if (col + 3 < N) {
+          Float4 t;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) t.v[c] = v[c];
+          *reinterpret_cast<Float4*>(o) = t;
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (col + c < N) o[c] = v[c];
+        }
+      } else {
+        uint16_t* o = static_cast<uint16_t*>(outp) + row * N + col;
+        Half4 t;
+        t.v[0] = bf16x2_rne(v[0], v[1]);
+        t.v[1] = bf16x2_rne(v[2], v[3]);
+        if (col + 3 < N) {
+          *reinterpret_cast<Half4*>(o) = t;
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (col + c < N) o[c] = uint16_t(t.v[c >> 1] >> (16 * (c & 1)));
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the product of few rows
+
+// Bound by the weight's bytes: a workgroup of 8 waves takes 16 MT rows and
+// 16 * 8 / KW columns; KW waves share a column tile's K, block by block, so
+// that the whole weight is in flight at once, and join their sums through
+// LDS in order.  Both operands go from memory to registers: lane l takes 32
+// contiguous bytes of row l % 16, four lanes a line.
+template <int MT, int KW>
+__global__ __launch_bounds__(512) void k_fp8_thin(const uint8_t* __restrict__ A, const uint8_t* __restrict__ As,
+                                                  const uint8_t* __restrict__ Bm, const uint8_t* __restrict__ Bs,
+                                                  int64_t M, int N, int64_t ldk, int64_t sld,
+                                                  const int32_t* __restrict__ off, int G,
+                                                  uint16_t* __restrict__ out) {
+  constexpr int NW = 8 / KW, BM = 16 * MT, BN = 16 * NW, U = MT >= 4 ? 2 : 4;
+  __shared__ __align__(16) float red[KW > 1 ? 8 : 1][MT][kWave][4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wave / KW, wk = wave % KW;
+  const int tn_all = (N + BN - 1) / BN;
+  int64_t m0, m_end;
+  int n0;
+  if (off) {
+    const int tm = int(blockIdx.x) / tn_all;
+    n0 = (int(blockIdx.x) % tn_all) * BN;
+    int lo[4], hi[4], n[4], before;
+    group_tiles(off, G, M, BM, lane, lo, hi, n, before);
+    const Tile g = group_find(tm, lane, lo, hi, n, before);
+    if (g.e < 0) return;
+    m0 = g.lo + int64_t(g.at) * BM;
+    m_end = g.hi;
+    Bm += int64_t(g.e) * N * ldk;
+    Bs += int64_t(g.e) * ((N + kQBlock - 1) / kQBlock) * sld;
+  } else {
+    m0 = int64_t(int(blockIdx.x) / tn_all) * BM;
+    n0 = (int(blockIdx.x) % tn_all) * BN;
+    m_end = M;
+  }
+  const int r = lane & 15, g4 = lane >> 4;
+  const int KB = int(ldk / kQBlock);
+  const int ncol = n0 + wn * 16;
+  const int brow = ncol + r < N ? ncol + r : N - 1;
+  const uint8_t* bp = Bm + int64_t(brow) * ldk + g4 * 32;
+  const uint8_t* bsp = Bs + int64_t(brow / kQBlock) * sld;
+  const uint8_t* ap[MT];
+  const uint8_t* asp[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    int64_t row = m0 + 16 * i + r;
+    row = row < m_end ? row : m_end - 1;
+    ap[i] = A + row * ldk + g4 * 32;
+    asp[i] = As + row * sld;
+  }
+  v4f acc[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) acc[i] = (v4f){0.f, 0.f, 0.f, 0.f};
+  for (int kb = wk; kb < KB; kb += KW * U) {
+    v8i b[U], a[U][MT];
+    int bs[U], as[U][MT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = kb + u * KW;
+      const int kc = k < KB ? k : kb;  // past the end: re-read, and not used
+      b[u] = *reinterpret_cast<const v8i*>(bp + int64_t(kc) * kQBlock);
+      bs[u] = bsp[kc];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        a[u][i] = *reinterpret_cast<const v8i*>(ap[i] + int64_t(kc) * kQBlock);
+        as[u][i] = asp[i][kc];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (kb + u * KW < KB) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const bf16x8 bw = widen(b[u][2 * h], b[u][2 * h + 1], scale_value(bs[u]));
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                bw, widen(a[u][i][2 * h], a[u][i][2 * h + 1], scale_value(as[u][i])), acc[i], 0, 0, 0);
+        }
+      }
+    }
+  }
+  if constexpr (KW > 1) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i) *reinterpret_cast<v4f*>(&red[wave][i][lane][0]) = acc[i];
+    __syncthreads();
+    if (wk != 0) return;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int k = 1; k < KW; ++k) acc[i] += *reinterpret_cast<const v4f*>(&red[wave + k][i][lane][0]);
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int64_t row = m0 + 16 * i + r;
+    const int col = ncol + g4 * 4;
+    if (row >= m_end) continue;
+    uint16_t* o = out + row * N + col;
+    Half4 t;
+    t.v[0] = bf16x2_rne(acc[i][0], acc[i][1]);
+    t.v[1] = bf16x2_rne(acc[i][2], acc[i][3]);
+    if (col + 3 < N) {
+      *reinterpret_cast<Half4*>(o) = t;
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (col + c < N) o[c] = uint16_t(t.v[c >> 1] >> (16 * (c & 1)));
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+
+struct Gemm {
+  const uint8_t *A, *As, *B, *Bs;
+  int64_t M;
+  int N;
+  int64_t ldk, sld;
+  const int32_t* off;
+  int G;
+  void* out;
+};
+
+// Tiles of BM rows that G experts' M rows make at most.
+static int64_t row_tiles(const Gemm& g, int BM) {
+  if (!g.off) return (g.M + BM - 1) / BM;
+  return g.M / BM + std::min<int64_t>(g.G, g.M);
+}
+
+template <int BM, int BN, int WM, int WN, bool GRAD, bool EXACT>
+static int gemm_tiled(const Gemm& g, hipStream_t st) {
+  const int64_t tn = (g.N + BN - 1) / BN;
+  const int64_t blocks = GRAD ? int64_t(g.G) * ((g.M + BM - 1) / BM) * tn : row_tiles(g, BM) * tn;
+  if (blocks > INT32_MAX) return int(hipErrorInvalidValue);
+  hipLaunchKernelGGL((k_fp8_gemm<BM, BN, WM, WN, GRAD, EXACT>), dim3(unsigned(blocks)), dim3(WM * WN * kWave), 0, st, g.A,
+                     g.As, g.B, g.Bs, g.M, g.N, g.ldk, g.sld, g.off, g.G, g.out);
+  return int(hipGetLastError());
+}
+
+template <int MT, int KW>
+static int gemm_thin(const Gemm& g, hipStream_t st) {
+  constexpr int BN = 16 * (8 / KW);
+  const int64_t blocks = row_tiles(g, 16 * MT) * ((g.N + BN - 1) / BN);
+  if (blocks > INT32_MAX) return int(hipErrorInvalidValue);
+  hipLaunchKernelGGL((k_fp8_thin<MT, KW>), dim3(unsigned(blocks)), dim3(512), 0, st, g.A, g.As, g.B, g.Bs, g.M, g.N,
+                     g.ldk, g.sld, g.off, g.G, static_cast<uint16_t*>(g.out));
+  return int(hipGetLastError());
+}
+
+int launch_fp8_product(const uint8_t* xq, const uint8_t* xs, const uint8_t* w, const uint8_t* ws, int64_t M, int N,
+                       int64_t ldk, const int32_t* off, int G, bool exact, uint16_t* y, hipStream_t st) {
+  const Gemm g{xq, xs, w, ws, M, N, ldk, fp8_sld(ldk), off, G, y};
+  const int64_t rows = off ? (M + G - 1) / G : M;  // rows of an expert, on average
+  if (rows <= 64) {
+    if (rows <= 16) return gemm_thin<1, 8>(g, st);
+    if (rows <= 32) return gemm_thin<2, 8>(g, st);
+    return gemm_thin<4, 8>(g, st);
+  }
+  if (row_tiles(g, 256) * ((N + 255) / 256) >= 192)
+    return exact ? gemm_tiled<256, 256, 2, 4, false, true>(g, st) : gemm_tiled<256, 256, 2, 4, false, false>(g, st);
+  return exact ? gemm_tiled<128, 128, 2, 2, false, true>(g, st) : gemm_tiled<128, 128, 2, 2, false, false>(g, st);
+}
+
+int launch_fp8_weight_grad(const uint8_t* dyt, const uint8_t* dyts, const uint8_t* xt, const uint8_t* xts, int N,
+                           int C, int64_t ldm, const int32_t* off, int G, float* dw, hipStream_t st) {
+  const Gemm g{dyt, dyts, xt, xts, N, C, ldm, fp8_sld(ldm), off, G, dw};
+  if (int64_t(G) * ((N + 255) / 256) * ((C + 255) / 256) >= 192) return gemm_tiled<256, 256, 2, 4, true, true>(g, st);
+  return gemm_tiled<128, 128, 2, 2, true, true>(g, st);
+}
+
+}  // namespace qbk

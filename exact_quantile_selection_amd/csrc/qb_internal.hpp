@@ -125,4 +125,74 @@ int launch_lei(float* g, const int32_t* load, int64_t N, int E, int K, float eta
 
 bool supported_E(int E);
 
+// Routing with a balance loss.  Workspace: an arrival counter, one float64
+// share of the loss for every 16 experts of every sequence, then for each
+// slot (chunk of T rows + sequence) E sums, E counts and the live tokens.
+// Every word that is read was written by the same call.
+struct BalWs {
+  int T;                                        // rows per chunk
+  int64_t chunks, slots, groups;
+  int64_t part, psum, cnt, live, bytes;         // byte offsets (16-byte aligned), total
+};
+BalWs balance_ws_layout(int64_t N, int E, int B);
+struct BalFwd {
+  const float *s, *b;
+  int64_t N;
+  int E, K;
+  const int32_t* seq_off;  // nullable: one sequence of all rows
+  int B;
+  const uint8_t* valid;    // nullable
+  float coef;
+  int32_t* topk;
+  float* gate;             // nullable
+  int32_t* count;          // nullable
+  float *weight, *loss;    // nullable
+  uint8_t* ws;             // null: experts and gates alone
+};
+struct BalBwd {
+  const float* s;
+  const int32_t* topk;
+  int64_t N;
+  int E, K;
+  const int32_t* seq_off;
+  int B;
+  const uint8_t* valid;
+  const float *weight, *dloss, *dgate;  // each nullable
+  float* dlogits;
+};
+int launch_balance_fwd(const BalFwd& a, hipStream_t st);
+int launch_balance_bwd(const BalBwd& a, hipStream_t st);
+
+// The exchange between tokens and experts.
+struct Dispatch {
+  const int32_t* topk;
+  int64_t pairs;  // N * K
+  int K, E, align;
+  int32_t* off;
+  int64_t R;
+  int32_t *row_src, *pos, *ws;
+};
+int64_t dispatch_ws_bytes(int64_t pairs, int E);
+int launch_dispatch(const Dispatch& a, hipStream_t st);
+int launch_combine(const uint16_t* rows, int64_t R, const int32_t* pos, const float* gate, int64_t N, int K, int H,
+                   uint16_t* out, hipStream_t st);
+int launch_combine_bwd(const uint16_t* dout, const uint16_t* rows, int64_t R, const int32_t* pos,
+                       const int32_t* row_src, const float* gate, int64_t N, int K, int H, uint16_t* drows,
+                       float* dgate, hipStream_t st);
+
+// 8-bit products with a power-of-two scale for each block of 128.
+constexpr int kQBlock = 128;
+inline int64_t fp8_ld(int64_t n) { return (n + kQBlock - 1) / kQBlock * kQBlock; }
+inline int64_t fp8_sld(int64_t n) { return (n + 4 * kQBlock - 1) / (4 * kQBlock) * 4; }
+int launch_fp8_quantize(const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M, int C, uint8_t* xq,
+                        uint8_t* xs, hipStream_t st);
+int launch_fp8_quantize_cols(const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M, int C, uint8_t* xt,
+                             uint8_t* xts, hipStream_t st);
+int launch_fp8_quantize_weight(const float* w, int G, int N, int C, uint8_t* wq, uint8_t* ws, uint8_t* wt,
+                               uint8_t* wts, hipStream_t st);
+int launch_fp8_product(const uint8_t* xq, const uint8_t* xs, const uint8_t* w, const uint8_t* ws, int64_t M, int N,
+                       int64_t ldk, const int32_t* off, int G, bool exact, uint16_t* y, hipStream_t st);
+int launch_fp8_weight_grad(const uint8_t* dyt, const uint8_t* dyts, const uint8_t* xt, const uint8_t* xts, int N,
+                           int C, int64_t ldm, const int32_t* off, int G, float* dw, hipStream_t st);
+
 }  // namespace qbk

@@ -73,6 +73,18 @@ def lib() -> C.CDLL:
             "qb_radix_lo_trip_rows": [i32],
             "qb_radix_lo_select_noalloc": [vp, vp, i32, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp],
         }
+        sig |= {
+            "qb_balance_forward": [vp, vp, i64, i32, i32, vp, i32, vp, f32, vp, vp, vp, vp, vp, vp, i64, vp],
+            "qb_balance_backward": [vp, vp, i64, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp],
+            "qb_dispatch": [vp, i64, i32, i32, i32, vp, i64, vp, vp, vp, i64, vp],
+            "qb_combine": [vp, i64, vp, vp, i64, i32, i32, vp, vp],
+            "qb_combine_backward": [vp, vp, i64, vp, vp, vp, i64, i32, i32, vp, vp, vp],
+            "qb_fp8_quantize": [vp, i64, vp, i64, i32, vp, vp, vp],
+            "qb_fp8_quantize_cols": [vp, i64, vp, i64, i32, vp, vp, vp],
+            "qb_fp8_quantize_weight": [vp, i32, i32, i32, vp, vp, vp, vp, vp],
+            "qb_fp8_product": [vp, vp, vp, vp, i64, i32, i32, vp, i32, i32, vp, vp],
+            "qb_fp8_weight_grad": [vp, vp, vp, vp, i64, i32, i32, vp, i32, vp, vp],
+        }
         for name, args in sig.items():
             fn = getattr(L, name)
             fn.argtypes = args
@@ -81,6 +93,11 @@ def lib() -> C.CDLL:
         L.qb_hist_lo_workspace_bytes.restype = C.c_int64
         L.qb_uniform_hist_workspace_bytes.argtypes = [i32, i64, i32, i32]
         L.qb_uniform_hist_workspace_bytes.restype = C.c_int64
+        L.qb_balance_workspace_bytes.argtypes = [i64, i32, i32]
+        L.qb_dispatch_rows.argtypes = [i64, i32, i32, i32]
+        L.qb_dispatch_workspace_bytes.argtypes = [i64, i32, i32]
+        for name in ("qb_balance_workspace_bytes", "qb_dispatch_rows", "qb_dispatch_workspace_bytes"):
+            getattr(L, name).restype = C.c_int64
         L.qb_status_string.argtypes = [C.c_int]
         L.qb_status_string.restype = C.c_char_p
         L.qb_last_error.argtypes = []
@@ -424,6 +441,173 @@ def qb_rank_average(q, b, bounds=None, stream=None):
     R, E = q.shape
     _check(lib().qb_rank_average(_ptr(q, torch.float32, "q"), R, E, _ptr(b, torch.float32, "b", (E,)),
                                  _ptr(bounds, torch.float32, "bounds", (2,), opt=True), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# The expert layer: routing with a balance loss, the exchange of rows between
+# tokens and experts, products in 8-bit floating point.
+
+F8 = torch.float8_e4m3fn
+FP8_BLOCK = 128
+
+
+def fp8_ld(n):
+    """Bytes of a row of a quantised matrix of n columns."""
+    return -(-n // FP8_BLOCK) * FP8_BLOCK
+
+
+def fp8_sld(n):
+    """Scale bytes of such a row."""
+    return -(-n // (4 * FP8_BLOCK)) * 4
+
+
+def _bytes(n):
+    if n < 0:
+        _check(int(n))
+    return int(n)
+
+
+def _wsopt(ws):
+    return (None, 0) if ws is None else _ws(ws)
+
+
+def _seqs(seq_off, valid, N):
+    B = 1 if seq_off is None else seq_off.numel() - 1
+    return _ptr(seq_off, torch.int32, "seq_off", (B + 1,), opt=True), B, _ptr(valid, torch.uint8, "valid", (N,), opt=True)
+
+
+def qb_balance_workspace_bytes(N, E, B=1):
+    return _bytes(lib().qb_balance_workspace_bytes(N, E, B))
+
+
+def qb_balance_forward(s, b, K, topk, gate=None, count=None, weight=None, loss=None, ws=None, coef=0.0, seq_off=None,
+                       valid=None, stream=None):
+    """The K experts of every token of s [N, E] by s + b into topk [N, K] and
+    their normalised gates; with count [B, E], weight [B, E] or loss [1] (and
+    ws, uint8 of qb_balance_workspace_bytes) the sequence-wise balance loss
+    and what its gradient needs.  seq_off int32 [B + 1]: the packed
+    sequences; valid uint8 [N]: 0 for padding."""
+    N, E = s.shape
+    so, B, va = _seqs(seq_off, valid, N)
+    wp, wn = _wsopt(ws)
+    _check(lib().qb_balance_forward(
+        _ptr(s, torch.float32, "s"), _ptr(b, torch.float32, "b", (E,)), N, E, K, so, B, va, coef,
+        _ptr(topk, torch.int32, "topk", (N, K)), _ptr(gate, torch.float32, "gate", (N, K), opt=True),
+        _ptr(count, torch.int32, "count", (B, E), opt=True), _ptr(weight, torch.float32, "weight", (B, E), opt=True),
+        _ptr(loss, torch.float32, "loss", (1,), opt=True), wp, wn, _stream(stream)))
+
+
+def qb_balance_backward(s, topk, weight=None, dloss=None, dgate=None, dlogits=None, seq_off=None, valid=None,
+                        stream=None):
+    """dlogits [N, E]: the gradient of dloss * loss + sum dgate * gate through
+    the sigmoid, from the forward's topk and weight."""
+    N, E = s.shape
+    so, B, va = _seqs(seq_off, valid, N)
+    K = topk.shape[-1]
+    _check(lib().qb_balance_backward(
+        _ptr(s, torch.float32, "s"), _ptr(topk, torch.int32, "topk", (N, K)), N, E, K, so, B, va,
+        _ptr(weight, torch.float32, "weight", (B, E), opt=True), _ptr(dloss, torch.float32, "dloss", (1,), opt=True),
+        _ptr(dgate, torch.float32, "dgate", (N, K), opt=True), _ptr(dlogits, torch.float32, "dlogits", (N, E)),
+        _stream(stream)))
+
+
+def qb_dispatch_rows(N, K, E, align=1):
+    return _bytes(lib().qb_dispatch_rows(N, K, E, align))
+
+
+def qb_dispatch_workspace_bytes(N, K, E):
+    return _bytes(lib().qb_dispatch_workspace_bytes(N, K, E))
+
+
+def qb_dispatch(topk, E, align, off, row_src, pos, ws=None, stream=None):
+    """off [E + 1], row_src [R] and pos [N, K] of the order that puts each
+    expert's pairs of topk [N, K] side by side, every expert rounded up to a
+    multiple of align rows."""
+    N, K = topk.shape
+    wp, wn = _wsopt(ws)
+    _check(lib().qb_dispatch(
+        _ptr(topk, torch.int32, "topk"), N, K, E, align, _ptr(off, torch.int32, "off", (E + 1,)), row_src.numel(),
+        _ptr(row_src, torch.int32, "row_src"), _ptr(pos, torch.int32, "pos", (N, K)), wp, wn, _stream(stream)))
+
+
+def qb_combine(rows, pos, out, gate=None, stream=None):
+    """out [N, H] = sum_k gate[:, k] * rows[pos[:, k]] (bf16; gate 1 if not
+    given, rows with pos < 0 left out)."""
+    (R, H), (N, K) = rows.shape, pos.shape
+    _check(lib().qb_combine(
+        _ptr(rows, torch.bfloat16, "rows"), R, _ptr(pos, torch.int32, "pos"),
+        _ptr(gate, torch.float32, "gate", (N, K), opt=True), N, K, H, _ptr(out, torch.bfloat16, "out", (N, H)),
+        _stream(stream)))
+
+
+def qb_combine_backward(dout, rows, pos, row_src, drows, gate=None, dgate=None, stream=None):
+    """drows [R, H] and (with rows and dgate) dgate [N, K] of qb_combine."""
+    (R, H), (N, K) = drows.shape, pos.shape
+    _check(lib().qb_combine_backward(
+        _ptr(dout, torch.bfloat16, "dout", (N, H)), _ptr(rows, torch.bfloat16, "rows", (R, H), opt=True), R,
+        _ptr(pos, torch.int32, "pos"), _ptr(row_src, torch.int32, "row_src", (R,)),
+        _ptr(gate, torch.float32, "gate", (N, K), opt=True), N, K, H, _ptr(drows, torch.bfloat16, "drows"),
+        _ptr(dgate, torch.float32, "dgate", (N, K), opt=True), _stream(stream)))
+
+
+def qb_fp8_quantize(x, xq, xs, row_src=None, stream=None):
+    """x bf16 [Mx, C] -> xq e4m3 [M, fp8_ld(C)] and xs uint8 [M, fp8_sld(C)],
+    a scale for each 128 columns; row_src int32 [M]: row i is x[row_src[i]]
+    (zeros where negative)."""
+    Mx, C_ = x.shape
+    M = Mx if row_src is None else row_src.numel()
+    _check(lib().qb_fp8_quantize(
+        _ptr(x, torch.bfloat16, "x"), Mx, _ptr(row_src, torch.int32, "row_src", (M,), opt=True), M, C_,
+        _ptr(xq, F8, "xq", (M, fp8_ld(C_))), _ptr(xs, torch.uint8, "xs", (M, fp8_sld(C_))), _stream(stream)))
+
+
+def qb_fp8_quantize_cols(x, xt, xts, row_src=None, stream=None):
+    """The transpose, a scale for each 128 rows: xt e4m3 [C, fp8_ld(M)], xts
+    uint8 [C, fp8_sld(M)]."""
+    Mx, C_ = x.shape
+    M = Mx if row_src is None else row_src.numel()
+    _check(lib().qb_fp8_quantize_cols(
+        _ptr(x, torch.bfloat16, "x"), Mx, _ptr(row_src, torch.int32, "row_src", (M,), opt=True), M, C_,
+        _ptr(xt, F8, "xt", (C_, fp8_ld(M))), _ptr(xts, torch.uint8, "xts", (C_, fp8_sld(M))), _stream(stream)))
+
+
+def qb_fp8_quantize_weight(w, wq, ws, wt=None, wts=None, stream=None):
+    """w float [N, C] or [G, N, C] -> wq, ws (a scale for each 128 x 128
+    block) and, on request, the same values transposed, wt and wts."""
+    lead = tuple(w.shape[:-2])
+    N, C_ = w.shape[-2:]
+    nb, cb = -(-N // FP8_BLOCK), -(-C_ // FP8_BLOCK)
+    _check(lib().qb_fp8_quantize_weight(
+        _ptr(w, torch.float32, "w"), w.shape[0] if lead else 1, N, C_, _ptr(wq, F8, "wq", lead + (N, fp8_ld(C_))),
+        _ptr(ws, torch.uint8, "ws", lead + (nb, fp8_sld(C_))), _ptr(wt, F8, "wt", lead + (C_, fp8_ld(N)), opt=True),
+        _ptr(wts, torch.uint8, "wts", lead + (cb, fp8_sld(N)), opt=True), _stream(stream)))
+
+
+def qb_fp8_product(xq, xs, w, w_scale, y, off=None, exact=False, stream=None):
+    """y bf16 [M, N] = xq times w [N, ld] transposed; with off int32 [G + 1]
+    rows off[e] .. off[e + 1] - 1 take w[e] of w [G, N, ld].  exact: sums in
+    32 bits throughout, at half the matrix rate (else the 8-bit instruction's,
+    which drops the parts of products 2^13 below the largest of eight)."""
+    M, ld = xq.shape
+    N = w.shape[-2]
+    lead = () if off is None else (off.numel() - 1,)
+    _check(lib().qb_fp8_product(
+        _ptr(xq, F8, "xq"), _ptr(xs, torch.uint8, "xs", (M, fp8_sld(ld))), _ptr(w, F8, "w", lead + (N, ld)),
+        _ptr(w_scale, torch.uint8, "w_scale", lead + (-(-N // FP8_BLOCK), fp8_sld(ld))), M, N, ld,
+        _ptr(off, torch.int32, "off", opt=True), lead[0] if lead else 1, int(bool(exact)),
+        _ptr(y, torch.bfloat16, "y", (M, N)),
+        _stream(stream)))
+
+
+def qb_fp8_weight_grad(dyt, dyts, xt, xts, dw, off=None, stream=None):
+    """dw float [N, C] (or [G, N, C] with off, multiples of 128) = sum over
+    the rows of dy times x, both quantised by qb_fp8_quantize_cols."""
+    (N, ld), C_ = dyt.shape, xt.shape[0]
+    lead = () if off is None else (off.numel() - 1,)
+    _check(lib().qb_fp8_weight_grad(
+        _ptr(dyt, F8, "dyt"), _ptr(dyts, torch.uint8, "dyts", (N, fp8_sld(ld))), _ptr(xt, F8, "xt", (C_, ld)),
+        _ptr(xts, torch.uint8, "xts", (C_, fp8_sld(ld))), ld, N, C_, _ptr(off, torch.int32, "off", opt=True),
+        lead[0] if lead else 1, _ptr(dw, torch.float32, "dw", lead + (N, C_)), _stream(stream)))
 
 
 # ---------------------------------------------------------------------------

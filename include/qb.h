@@ -447,6 +447,145 @@ QB_API int qb_rank_average(const float* q, int R, int E, float* b, float* bounds
 QB_API int qb_lei_grad(float* g, const int32_t* load, int64_t N, int E, int K, float eta,
                        qb_stream_t stream);
 
+/*
+ * An expert layer around the balanced router: routing with a sequence-wise
+ * balance loss, the exchange of rows between tokens and experts, and the
+ * experts' products in 8-bit floating point.
+ *
+ * qb_balance_forward: experts, gates and, on request, the balance loss.  Row
+ * i of the scores is a token; sequence q holds rows seq_off[q] ..
+ * seq_off[q + 1] - 1.  A token is live if it lies in a sequence and valid[i]
+ * is not 0 (each of the two only if given).  For live tokens
+ *   topk[i]   = the K largest of fl32(s[i] + b), larger first, equal values
+ *               by lower index;  gate[i][k] = s[i][topk[i][k]] / their sum
+ *               (0 where that sum is 0);  -1 and 0 for tokens not live
+ *   count[q][e] = live tokens of q that chose e;  T = live tokens of q
+ *   p[i] = s[i] / sum_e s[i][e] (0 where that sum is 0);  f[q][e] = count E / (K T)
+ *   loss      = coef / n sum_q sum_e f[q][e] (1 / T) sum_{i live in q} p[i][e],
+ *               n = sequences with a live token (0 if there is none)
+ *   weight[q][e] = coef (f[q][e] - 1) / (n T), what qb_balance_backward needs
+ * Sums over tokens are added in a fixed order in 64 bits: the same result on
+ * every run.
+ *   s float [N][E] (16-byte aligned), b float [E]; E in {16, 32, 64, 128,
+ *   256}, 1 <= K <= 15, K < E, 1 <= N <= 2^30, 1 <= B <= 2^20.
+ *   seq_off nullable int32 [B + 1], not decreasing, within [0, N]; without it
+ *   B is 1 and every row belongs to the one sequence.  valid nullable uint8
+ *   [N].  topk int32 [N][K]; gate nullable float [N][K].
+ *   count (int32 [B][E]), weight (float [B][E]; 16-byte aligned), loss (float
+ *   [1]): each nullable; with any of them ws (16-byte aligned, at least
+ *   qb_balance_workspace_bytes; its contents do not matter) is required.
+ *   Scores of tokens that are not live may be anything; other NaN or Inf
+ *   inputs and offsets out of order give unspecified, memory-safe results.
+ */
+QB_API int64_t qb_balance_workspace_bytes(int64_t N, int E, int B);
+QB_API int qb_balance_forward(const float* s, const float* b, int64_t N, int E, int K, const int32_t* seq_off, int B,
+                              const uint8_t* valid, float coef, int32_t* topk, float* gate, int32_t* count,
+                              float* weight, float* loss, void* ws, int64_t ws_bytes, qb_stream_t stream);
+
+/*
+ * The gradient with respect to the logits (s = sigmoid(logits)) of
+ * dloss * loss + sum dgate * gate, the counts held constant:
+ *   ds = dloss (weight[q] - sum_e weight[q][e] p[e]) / sum_e s[e]
+ *        + (dgate[k] - sum_k' dgate[k'] gate[k']) / sum_k s[topk[k]] at topk[k]
+ *   dlogits = ds s (1 - s);  0 for tokens not live.
+ *   weight nullable float [B][E] (no loss term without it), 16-byte aligned;
+ *   dloss nullable float [1] on the device (1 without it); dgate nullable
+ *   float [N][K]; one of weight and dgate is required.  topk, seq_off and
+ *   valid as given to or returned by qb_balance_forward; a topk entry outside
+ *   [0, E) has no gate.  dlogits float [N][E], 16-byte aligned, overwritten.
+ */
+QB_API int qb_balance_backward(const float* s, const int32_t* topk, int64_t N, int E, int K, const int32_t* seq_off,
+                               int B, const uint8_t* valid, const float* weight, const float* dloss,
+                               const float* dgate, float* dlogits, qb_stream_t stream);
+
+/*
+ * qb_dispatch: the order that puts each expert's rows side by side.  Pair i =
+ * t K + k goes to expert e = topk[i] (outside [0, E): nowhere).
+ *   off[e]  int32 [E + 1]: expert e's first row; off[0] = 0 and each expert
+ *           takes its pairs rounded up to a multiple of align
+ *   pos[i]  int32 [N][K]: the pair's row, in the pairs' order inside an
+ *           expert (-1: nowhere)
+ *   row_src int32 [R]: the token of each row, -1 for rows without a pair
+ * R is at least qb_dispatch_rows(N, K, E, align), the rows that any topk of
+ * this shape fits in.  ws: at least qb_dispatch_workspace_bytes (0 up to 8192
+ * pairs; ws may then be NULL), 16-byte aligned.  1 <= E <= 256, K >= 1, N >=
+ * 0, align >= 1; N K and R below 2^31.
+ */
+QB_API int64_t qb_dispatch_rows(int64_t N, int K, int E, int align);
+QB_API int64_t qb_dispatch_workspace_bytes(int64_t N, int K, int E);
+QB_API int qb_dispatch(const int32_t* topk, int64_t N, int K, int E, int align, int32_t* off, int64_t R,
+                       int32_t* row_src, int32_t* pos, void* ws, int64_t ws_bytes, qb_stream_t stream);
+
+/*
+ * qb_combine: out[t] = sum_k gate[t][k] rows[pos[t][k]], summed in 32 bits in
+ * the order of k and rounded once.  rows and out bf16 bit patterns [R][H] and
+ * [N][H]; pos int32 [N][K], a row outside [0, R) adds nothing; gate nullable
+ * float [N][K] (1 without it: then this is also the backward of handing each
+ * expert its copy of a token).  H >= 1, K >= 1, 0 <= N <= 2^24, R < 2^31.
+ * qb_combine_backward: dgate[t][k] = sum_h dout[t][h] rows[pos[t][k]][h] (0
+ * where pos is outside [0, R)), drows[pos[t][k]] = gate[t][k] dout[t], and 0
+ * in the rows with row_src < 0.  dgate nullable (rows is then not read and
+ * may be NULL; without gate too, drows is the copy each expert gets).  Each
+ * row belongs to one pair, as qb_dispatch leaves it.
+ */
+QB_API int qb_combine(const uint16_t* rows, int64_t R, const int32_t* pos, const float* gate, int64_t N, int K, int H,
+                      uint16_t* out, qb_stream_t stream);
+QB_API int qb_combine_backward(const uint16_t* dout, const uint16_t* rows, int64_t R, const int32_t* pos,
+                               const int32_t* row_src, const float* gate, int64_t N, int K, int H, uint16_t* drows,
+                               float* dgate, qb_stream_t stream);
+
+/*
+ * Products in 8-bit floating point (e4m3) with a power-of-two scale for each
+ * block of 128 values along the sum.  A quantised matrix of n columns has
+ * rows of ld(n) = n rounded up to 128 bytes, zeros past column n, and rows of
+ * sld(n) = ceil(n / 512) * 4 scale bytes: byte j holds e + 127, e the least
+ * whole number >= -126 with max |x| <= 448 * 2^e over columns 128 j .. 128 j
+ * + 127 (bytes past the last block do not matter).  Values are x 2^-e rounded
+ * to nearest even.  A NaN or an infinity becomes NaN.
+ *
+ * qb_fp8_quantize: x bf16 [Mx][C] -> xq e4m3 [M][ld(C)], xs [M][sld(C)].
+ * qb_fp8_quantize_cols: the transpose, in blocks along the rows: xt e4m3
+ * [C][ld(M)], xts [C][sld(M)].  row_src nullable int32 [M]: row i of the
+ * matrix is x[row_src[i]], and zeros where row_src[i] is outside [0, Mx)
+ * (qb_dispatch's: the experts' rows straight from the tokens); without it M =
+ * Mx.
+ *
+ * qb_fp8_quantize_weight: w float [G][N][C] -> wq e4m3 [G][N][ld(C)] with one
+ * scale for each 128 x 128 block, ws [G][ceil(N / 128)][sld(C)], and the same
+ * values transposed, wt e4m3 [G][C][ld(N)], wts [G][ceil(C / 128)][sld(N)]
+ * (wt and wts nullable, both or neither).
+ *
+ * qb_fp8_product: y[m][n] = sum_c x[m][c] w[n][c], y bf16 [M][N], with C the
+ * summed dimension.  exact = 1: every sum in 32 bits, rounded once.  exact =
+ * 0: the 8-bit matrix instruction, nearly twice as fast on large products; of
+ * each eight products it drops what lies more than 2^13 below the largest, so
+ * up to 2^-10 sum |x w| is lost (some 2^-15 on ordinary data), and adds the
+ * rest in 32 bits.  With off (int32 [G +
+ * 1], not decreasing, within [0, M]) row m in off[e] .. off[e + 1] - 1 takes
+ * w[e]; rows outside every expert are not written.  The gradient of x is the
+ * same call on dy and the transposed weight.
+ * qb_fp8_weight_grad: dw[e][n][c] = sum over e's rows of dy[m][n] x[m][c], dw
+ * float [G][N][C], summed in 32 bits, overwritten (0 for an expert without
+ * rows), from dyt
+ * [N][ld(M)] and xt [C][ld(M)] as qb_fp8_quantize_cols writes them; off's
+ * entries are multiples of 128 (qb_dispatch with align 128).  Without off G
+ * is 1 and the sum runs over all M rows.
+ *
+ * Quantised matrices are 16-byte aligned, scale rows 4-byte, bf16 and float
+ * arrays by their element.  0 <= M, Mx <= 2^22 rows; 1 <= N, C <= 2^22; 1 <=
+ * G <= 256.
+ */
+QB_API int qb_fp8_quantize(const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M, int C, uint8_t* xq,
+                           uint8_t* xs, qb_stream_t stream);
+QB_API int qb_fp8_quantize_cols(const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M, int C, uint8_t* xt,
+                                uint8_t* xts, qb_stream_t stream);
+QB_API int qb_fp8_quantize_weight(const float* w, int G, int N, int C, uint8_t* wq, uint8_t* ws, uint8_t* wt,
+                                  uint8_t* wts, qb_stream_t stream);
+QB_API int qb_fp8_product(const uint8_t* xq, const uint8_t* xs, const uint8_t* w, const uint8_t* w_scale, int64_t M,
+                          int N, int C, const int32_t* off, int G, int exact, uint16_t* y, qb_stream_t stream);
+QB_API int qb_fp8_weight_grad(const uint8_t* dyt, const uint8_t* dyts, const uint8_t* xt, const uint8_t* xts,
+                              int64_t M, int N, int C, const int32_t* off, int G, float* dw, qb_stream_t stream);
+
 /* Short name of a status code (static storage). */
 QB_API const char* qb_status_string(int status);
 
