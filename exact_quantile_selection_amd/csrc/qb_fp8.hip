@@ -795,6 +795,10 @@ __global__ __launch_bounds__(512) void k_fp8_thin(const uint8_t* __restrict__ A,
 
 // ---------------------------------------------------------------------------
 
+#ifndef QB_F8_WIDE
+#define QB_F8_WIDE 192
+#endif
+
 struct Gemm {
   const uint8_t *A, *As, *B, *Bs;
   int64_t M;
@@ -840,7 +844,7 @@ int launch_fp8_product(const uint8_t* xq, const uint8_t* xs, const uint8_t* w, c
     if (rows <= 32) return gemm_thin<2, 8>(g, st);
     return gemm_thin<4, 8>(g, st);
   }
-  if (row_tiles(g, 256) * ((N + 255) / 256) >= 192)
+  if (row_tiles(g, 256) * ((N + 255) / 256) >= QB_F8_WIDE)
     return exact ? gemm_tiled<256, 256, 2, 4, false, true>(g, st) : gemm_tiled<256, 256, 2, 4, false, false>(g, st);
   return exact ? gemm_tiled<128, 128, 2, 2, false, true>(g, st) : gemm_tiled<128, 128, 2, 2, false, false>(g, st);
 }
@@ -848,7 +852,7 @@ int launch_fp8_product(const uint8_t* xq, const uint8_t* xs, const uint8_t* w, c
 int launch_fp8_weight_grad(const uint8_t* dyt, const uint8_t* dyts, const uint8_t* xt, const uint8_t* xts, int N,
                            int C, int64_t ldm, const int32_t* off, int G, float* dw, hipStream_t st) {
   const Gemm g{dyt, dyts, xt, xts, N, C, ldm, fp8_sld(ldm), off, G, dw};
-  if (int64_t(G) * ((N + 255) / 256) * ((C + 255) / 256) >= 192) return gemm_tiled<256, 256, 2, 4, true, true>(g, st);
+  if (int64_t(G) * ((N + 255) / 256) * ((C + 255) / 256) >= QB_F8_WIDE) return gemm_tiled<256, 256, 2, 4, true, true>(g, st);
   return gemm_tiled<128, 128, 2, 2, true, true>(g, st);
 }
 

@@ -114,7 +114,8 @@ def _check(rc: int):
 
 def _stream(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the raw handle of torch.cuda.current_stream(), without making a Stream object of it
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return int(stream.cuda_stream)
 
 
@@ -123,6 +124,10 @@ def _ptr(t, dtype, name, shape=None, opt=False):
         if opt:
             return None
         raise ValueError(f"{name} is required")
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and (shape is None or t.shape == shape) \
+            and t.is_contiguous():
+        return t.data_ptr()
+    # something is wrong: say what
     if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
         raise ValueError(f"{name} must be a GPU tensor")
     if t.dtype != dtype:
