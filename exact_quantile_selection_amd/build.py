@@ -1,4 +1,4 @@
-"""Build libqb.so (HIP, gfx950) in-tree.
+"""Build libqb.so (HIP, gfx950) and its Python binding in-tree.
 
 Each translation unit is compiled by hipcc in parallel; the pass-1 kernels are
 split into one unit per expert count.  Flags: no fast-math, no FMA
@@ -8,10 +8,12 @@ default on gfx950).
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +22,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libqb.so")
 # the diagnostic streaming kernels (the measured HBM ceiling), a separate library
 PROBE_LIB = os.path.join(PKG, "libstreamprobe.so")
+# the compiled part of qb.py (host code)
+BINDING = os.path.join(PKG, "_qb_binding.so")
 ARCH = os.environ.get("QB_OFFLOAD_ARCH", "gfx950")
 
 HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
@@ -67,7 +71,10 @@ def build(verbose: bool = False, jobs: int | None = None, defines=(), out: str |
     os.makedirs(build_dir, exist_ok=True)
     jobs = jobs or min(8, os.cpu_count() or 4)
     with ThreadPoolExecutor(jobs) as ex:
+        binding = None if out else ex.submit(build_binding, verbose)
         objs = list(ex.map(lambda u: _compile(u, verbose, build_dir, list(defines)), _units()))
+        if binding:
+            binding.result()
     tmp = lib + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     if verbose:
@@ -77,6 +84,22 @@ def build(verbose: bool = False, jobs: int | None = None, defines=(), out: str |
     if not out:
         build_probe(verbose)
     return lib
+
+
+def build_binding(verbose: bool = False) -> str:
+    """Compile _qb_binding.so: a Python module over torch's tensors that calls
+    libqb's entry points by address, so it links neither libqb nor HIP."""
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    tmp = BINDING + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(torch_dir, "include"),
+           os.path.join(CSRC, "qb_binding.cpp"), "-o", tmp,
+           "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.check_call(cmd)
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build_probe(verbose: bool = False) -> str:

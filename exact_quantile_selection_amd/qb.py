@@ -12,12 +12,14 @@ alpha [L, N], ...) or omit it for one layer.
 from __future__ import annotations
 
 import ctypes as C
+import importlib.util
 import os
 
 import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libqb.so")
+BINDING_PATH = os.path.join(PKG, "_qb_binding.so")
 
 QB_OK, QB_EINVAL, QB_EUNSUPPORTED, QB_EHIP = 0, -1, -2, -3
 QB_SELECT_HI, QB_SELECT_LO, QB_SELECT_UNIFORM, QB_SELECT_FULL = 0, 1, 2, 3
@@ -28,6 +30,7 @@ SUPPORTED_E = (16, 32, 64, 128, 256)
 MAX_K = 15
 
 _lib = None
+_native = None
 
 
 class QBError(RuntimeError):
@@ -104,6 +107,30 @@ def lib() -> C.CDLL:
         L.qb_last_error.restype = C.c_char_p
         _lib = L
     return _lib
+
+
+# the expert layer's entry points, in the order in which the compiled binding takes their addresses
+_EXPERT_LAYER = ("qb_balance_forward", "qb_balance_backward", "qb_dispatch", "qb_combine", "qb_combine_backward",
+                 "qb_fp8_quantize", "qb_fp8_quantize_cols", "qb_fp8_quantize_weight", "qb_fp8_product",
+                 "qb_fp8_weight_grad")
+
+
+def _calls():
+    """The compiled binding of the expert layer's calls (csrc/qb_binding.cpp):
+    these are made once a decoding step and take the GPU a few microseconds,
+    which marshalling by ctypes would exceed."""
+    global _native
+    if _native is None:
+        L = lib()
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"{BINDING_PATH} is not built: run __graft_entry__.build() "
+                               "(or python exact_quantile_selection_amd/build.py)")
+        spec = importlib.util.spec_from_file_location("_qb_binding", BINDING_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.connect(_stream, *(C.cast(getattr(L, name), C.c_void_p).value for name in _EXPERT_LAYER))
+        _native = module
+    return _native
 
 
 def _check(rc: int):
@@ -472,15 +499,6 @@ def _bytes(n):
     return int(n)
 
 
-def _wsopt(ws):
-    return (None, 0) if ws is None else _ws(ws)
-
-
-def _seqs(seq_off, valid, N):
-    B = 1 if seq_off is None else seq_off.numel() - 1
-    return _ptr(seq_off, torch.int32, "seq_off", (B + 1,), opt=True), B, _ptr(valid, torch.uint8, "valid", (N,), opt=True)
-
-
 def qb_balance_workspace_bytes(N, E, B=1):
     return _bytes(lib().qb_balance_workspace_bytes(N, E, B))
 
@@ -492,28 +510,14 @@ def qb_balance_forward(s, b, K, topk, gate=None, count=None, weight=None, loss=N
     ws, uint8 of qb_balance_workspace_bytes) the sequence-wise balance loss
     and what its gradient needs.  seq_off int32 [B + 1]: the packed
     sequences; valid uint8 [N]: 0 for padding."""
-    N, E = s.shape
-    so, B, va = _seqs(seq_off, valid, N)
-    wp, wn = _wsopt(ws)
-    _check(lib().qb_balance_forward(
-        _ptr(s, torch.float32, "s"), _ptr(b, torch.float32, "b", (E,)), N, E, K, so, B, va, coef,
-        _ptr(topk, torch.int32, "topk", (N, K)), _ptr(gate, torch.float32, "gate", (N, K), opt=True),
-        _ptr(count, torch.int32, "count", (B, E), opt=True), _ptr(weight, torch.float32, "weight", (B, E), opt=True),
-        _ptr(loss, torch.float32, "loss", (1,), opt=True), wp, wn, _stream(stream)))
+    _check(_calls().balance_forward(s, b, K, topk, gate, count, weight, loss, ws, coef, seq_off, valid, stream))
 
 
 def qb_balance_backward(s, topk, weight=None, dloss=None, dgate=None, dlogits=None, seq_off=None, valid=None,
                         stream=None):
     """dlogits [N, E]: the gradient of dloss * loss + sum dgate * gate through
     the sigmoid, from the forward's topk and weight."""
-    N, E = s.shape
-    so, B, va = _seqs(seq_off, valid, N)
-    K = topk.shape[-1]
-    _check(lib().qb_balance_backward(
-        _ptr(s, torch.float32, "s"), _ptr(topk, torch.int32, "topk", (N, K)), N, E, K, so, B, va,
-        _ptr(weight, torch.float32, "weight", (B, E), opt=True), _ptr(dloss, torch.float32, "dloss", (1,), opt=True),
-        _ptr(dgate, torch.float32, "dgate", (N, K), opt=True), _ptr(dlogits, torch.float32, "dlogits", (N, E)),
-        _stream(stream)))
+    _check(_calls().balance_backward(s, topk, weight, dloss, dgate, dlogits, seq_off, valid, stream))
 
 
 def qb_dispatch_rows(N, K, E, align=1):
@@ -528,64 +532,37 @@ def qb_dispatch(topk, E, align, off, row_src, pos, ws=None, stream=None):
     """off [E + 1], row_src [R] and pos [N, K] of the order that puts each
     expert's pairs of topk [N, K] side by side, every expert rounded up to a
     multiple of align rows."""
-    N, K = topk.shape
-    wp, wn = _wsopt(ws)
-    _check(lib().qb_dispatch(
-        _ptr(topk, torch.int32, "topk"), N, K, E, align, _ptr(off, torch.int32, "off", (E + 1,)), row_src.numel(),
-        _ptr(row_src, torch.int32, "row_src"), _ptr(pos, torch.int32, "pos", (N, K)), wp, wn, _stream(stream)))
+    _check(_calls().dispatch(topk, E, align, off, row_src, pos, ws, stream))
 
 
 def qb_combine(rows, pos, out, gate=None, stream=None):
     """out [N, H] = sum_k gate[:, k] * rows[pos[:, k]] (bf16; gate 1 if not
     given, rows with pos < 0 left out)."""
-    (R, H), (N, K) = rows.shape, pos.shape
-    _check(lib().qb_combine(
-        _ptr(rows, torch.bfloat16, "rows"), R, _ptr(pos, torch.int32, "pos"),
-        _ptr(gate, torch.float32, "gate", (N, K), opt=True), N, K, H, _ptr(out, torch.bfloat16, "out", (N, H)),
-        _stream(stream)))
+    _check(_calls().combine(rows, pos, out, gate, stream))
 
 
 def qb_combine_backward(dout, rows, pos, row_src, drows, gate=None, dgate=None, stream=None):
     """drows [R, H] and (with rows and dgate) dgate [N, K] of qb_combine."""
-    (R, H), (N, K) = drows.shape, pos.shape
-    _check(lib().qb_combine_backward(
-        _ptr(dout, torch.bfloat16, "dout", (N, H)), _ptr(rows, torch.bfloat16, "rows", (R, H), opt=True), R,
-        _ptr(pos, torch.int32, "pos"), _ptr(row_src, torch.int32, "row_src", (R,)),
-        _ptr(gate, torch.float32, "gate", (N, K), opt=True), N, K, H, _ptr(drows, torch.bfloat16, "drows"),
-        _ptr(dgate, torch.float32, "dgate", (N, K), opt=True), _stream(stream)))
+    _check(_calls().combine_backward(dout, rows, pos, row_src, drows, gate, dgate, stream))
 
 
 def qb_fp8_quantize(x, xq, xs, row_src=None, stream=None):
     """x bf16 [Mx, C] -> xq e4m3 [M, fp8_ld(C)] and xs uint8 [M, fp8_sld(C)],
     a scale for each 128 columns; row_src int32 [M]: row i is x[row_src[i]]
     (zeros where negative)."""
-    Mx, C_ = x.shape
-    M = Mx if row_src is None else row_src.numel()
-    _check(lib().qb_fp8_quantize(
-        _ptr(x, torch.bfloat16, "x"), Mx, _ptr(row_src, torch.int32, "row_src", (M,), opt=True), M, C_,
-        _ptr(xq, F8, "xq", (M, fp8_ld(C_))), _ptr(xs, torch.uint8, "xs", (M, fp8_sld(C_))), _stream(stream)))
+    _check(_calls().quantize(x, xq, xs, row_src, stream))
 
 
 def qb_fp8_quantize_cols(x, xt, xts, row_src=None, stream=None):
     """The transpose, a scale for each 128 rows: xt e4m3 [C, fp8_ld(M)], xts
     uint8 [C, fp8_sld(M)]."""
-    Mx, C_ = x.shape
-    M = Mx if row_src is None else row_src.numel()
-    _check(lib().qb_fp8_quantize_cols(
-        _ptr(x, torch.bfloat16, "x"), Mx, _ptr(row_src, torch.int32, "row_src", (M,), opt=True), M, C_,
-        _ptr(xt, F8, "xt", (C_, fp8_ld(M))), _ptr(xts, torch.uint8, "xts", (C_, fp8_sld(M))), _stream(stream)))
+    _check(_calls().quantize_cols(x, xt, xts, row_src, stream))
 
 
 def qb_fp8_quantize_weight(w, wq, ws, wt=None, wts=None, stream=None):
     """w float [N, C] or [G, N, C] -> wq, ws (a scale for each 128 x 128
     block) and, on request, the same values transposed, wt and wts."""
-    lead = tuple(w.shape[:-2])
-    N, C_ = w.shape[-2:]
-    nb, cb = -(-N // FP8_BLOCK), -(-C_ // FP8_BLOCK)
-    _check(lib().qb_fp8_quantize_weight(
-        _ptr(w, torch.float32, "w"), w.shape[0] if lead else 1, N, C_, _ptr(wq, F8, "wq", lead + (N, fp8_ld(C_))),
-        _ptr(ws, torch.uint8, "ws", lead + (nb, fp8_sld(C_))), _ptr(wt, F8, "wt", lead + (C_, fp8_ld(N)), opt=True),
-        _ptr(wts, torch.uint8, "wts", lead + (cb, fp8_sld(N)), opt=True), _stream(stream)))
+    _check(_calls().quantize_weight(w, wq, ws, wt, wts, stream))
 
 
 def qb_fp8_product(xq, xs, w, w_scale, y, off=None, exact=False, stream=None):
@@ -593,26 +570,13 @@ def qb_fp8_product(xq, xs, w, w_scale, y, off=None, exact=False, stream=None):
     rows off[e] .. off[e + 1] - 1 take w[e] of w [G, N, ld].  exact: sums in
     32 bits throughout, at half the matrix rate (else the 8-bit instruction's,
     which drops the parts of products 2^13 below the largest of eight)."""
-    M, ld = xq.shape
-    N = w.shape[-2]
-    lead = () if off is None else (off.numel() - 1,)
-    _check(lib().qb_fp8_product(
-        _ptr(xq, F8, "xq"), _ptr(xs, torch.uint8, "xs", (M, fp8_sld(ld))), _ptr(w, F8, "w", lead + (N, ld)),
-        _ptr(w_scale, torch.uint8, "w_scale", lead + (-(-N // FP8_BLOCK), fp8_sld(ld))), M, N, ld,
-        _ptr(off, torch.int32, "off", opt=True), lead[0] if lead else 1, int(bool(exact)),
-        _ptr(y, torch.bfloat16, "y", (M, N)),
-        _stream(stream)))
+    _check(_calls().product(xq, xs, w, w_scale, y, off, exact, stream))
 
 
 def qb_fp8_weight_grad(dyt, dyts, xt, xts, dw, off=None, stream=None):
     """dw float [N, C] (or [G, N, C] with off, multiples of 128) = sum over
     the rows of dy times x, both quantised by qb_fp8_quantize_cols."""
-    (N, ld), C_ = dyt.shape, xt.shape[0]
-    lead = () if off is None else (off.numel() - 1,)
-    _check(lib().qb_fp8_weight_grad(
-        _ptr(dyt, F8, "dyt"), _ptr(dyts, torch.uint8, "dyts", (N, fp8_sld(ld))), _ptr(xt, F8, "xt", (C_, ld)),
-        _ptr(xts, torch.uint8, "xts", (C_, fp8_sld(ld))), ld, N, C_, _ptr(off, torch.int32, "off", opt=True),
-        lead[0] if lead else 1, _ptr(dw, torch.float32, "dw", lead + (N, C_)), _stream(stream)))
+    _check(_calls().weight_grad(dyt, dyts, xt, xts, dw, off, stream))
 
 
 # ---------------------------------------------------------------------------

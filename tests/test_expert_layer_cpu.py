@@ -180,3 +180,30 @@ def test_the_binding_names_a_wrong_tensor():
         qb.qb_combine(x, torch.zeros((4, 2), dtype=torch.int32), x)
     with pytest.raises(ValueError, match="topk must be a GPU tensor"):
         qb.qb_dispatch(torch.zeros((4, 2), dtype=torch.int32), 16, 1, x, x, x)
+
+
+def test_the_binding_refuses_what_is_no_gpu_tensor(L):
+    """The compiled binding turns wrong arguments into the errors that the
+    rest of the binding raises, before any call of the library."""
+    import torch
+
+    from exact_quantile_selection_amd import qb
+
+    s, b = torch.zeros((4, 16)), torch.zeros(16)
+    ids = torch.zeros((4, 2), dtype=torch.int32)
+    for bad in (s, None, 3, "s"):
+        with pytest.raises(ValueError, match="s (must be a GPU tensor|is required)"):
+            qb.qb_balance_forward(bad, b, 2, ids, stream=Stream())
+    with pytest.raises(ValueError, match="rows must be a GPU tensor"):
+        qb.qb_combine(s.to(torch.bfloat16), ids, s.to(torch.bfloat16), stream=Stream())
+    with pytest.raises(ValueError, match="row_src must be a GPU tensor|x must be a GPU tensor"):
+        qb.qb_fp8_quantize(s.to(torch.bfloat16), None, None, row_src=ids, stream=Stream())
+    with pytest.raises(ValueError, match="w is required"):
+        qb.qb_fp8_quantize_weight(None, None, None, stream=Stream())
+    with pytest.raises(TypeError, match="13 arguments"):
+        qb._calls().balance_forward(s, b)
+
+
+class Stream:
+    """Stands for a stream where nothing is launched."""
+    cuda_stream = 0
