@@ -33,6 +33,8 @@
 
 namespace qbk {
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
 constexpr int kBalThreads = 256;
 constexpr int kBalWaves = kBalThreads / kWave;
 
@@ -61,6 +63,28 @@ __device__ __forceinline__ int bal_row_sum_i(int x) {
   return x;
 }
 
+// Lane l ^ D's value, D 16 or 32 (the instruction exchanges the D-lane halves
+// of two registers, so one of the two results is the own value and the other
+// is the partner's).
+template <int D>
+__device__ __forceinline__ float bal_swapped(float x) {
+  unsigned a = __builtin_bit_cast(unsigned, x), b = a;
+  asm volatile("" : "+v"(b));  // two registers: with one and the same operand the compiler takes the results as equal
+  const auto h = D == 16 ? __builtin_amdgcn_permlane16_swap(a, b, false, false)
+                         : __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  return __builtin_bit_cast(float, threadIdx.x & D ? h[0] : h[1]);
+}
+
+// The sum over the lanes that hold the same columns (l, l + LPR, ...), in all
+// of them: within 16 lanes by rotation, then by exchanging halves.
+template <int LPR>
+__device__ __forceinline__ float bal_col_sum(float x) {
+  if constexpr (LPR <= 4) x += quad_mov<0x124>(x);  // row_ror:4
+  x += quad_mov<0x128>(x);                          // row_ror:8
+  x += bal_swapped<16>(x);
+  return x + bal_swapped<32>(x);
+}
+
 // The sequence that row r belongs to: the number of ends off[1..B] at or
 // below r (B: past the last sequence).  off need not be sorted for this to
 // stay within [0, B].
@@ -76,17 +100,37 @@ __device__ __forceinline__ int bal_find(const int32_t* off, int B, int r) {
   return lo;
 }
 
+// The same for one row of the whole wave: 64 ends a trip, so that B <= 64
+// sequences take one load's latency (a binary search of 41 took six: 4 us of
+// the 14 that a batch of 5003 tokens spent here).
+__device__ __forceinline__ int bal_find_wave(const int32_t* off, int B, int r, int lane) {
+  int lo = 0, hi = B;
+  while (lo < hi) {
+    const int step = (hi - lo + kWave - 1) / kWave;
+    const int j = lo + (lane + 1) * step - 1;
+    const int below = __popcll(__ballot(j < hi && off[j + 1] <= r));
+    lo += below * step;
+    hi = hi < lo + step - 1 ? hi : lo + step - 1;
+  }
+  return lo;
+}
+
 // Rows per chunk: short chunks keep all CUs busy on few tokens, longer ones
 // keep the partial rows small beside the scores (128 rows of 256 experts:
 // 2 KiB of partials for 128 KiB of scores).
 int balance_chunk_rows(int64_t N) { return N <= 32768 ? 32 : 128; }
+
+// Threads of the second kernel: 16 for each of up to 64 experts.
+constexpr int kBalFinWays = 16;
+constexpr int kBalFinCols = 64;
+static int bal_fin_cols(int E) { return E < kBalFinCols ? E : kBalFinCols; }
 
 BalWs balance_ws_layout(int64_t N, int E, int B) {
   BalWs w;
   w.T = balance_chunk_rows(N);
   w.chunks = (N + w.T - 1) / w.T;
   w.slots = w.chunks + B;
-  w.groups = int64_t(B) * (E / 16);
+  w.groups = int64_t(B) * (E / bal_fin_cols(E));
   w.part = 16;  // the arrival counter comes first
   w.psum = w.part + (w.groups * 8 + 15) / 16 * 16;
   w.cnt = w.psum + w.slots * E * 4;
@@ -95,27 +139,36 @@ BalWs balance_ws_layout(int64_t N, int E, int B) {
   return w;
 }
 
-// The K first of the row's order, element by element: only for rows with
-// equal values among (or at the end of) the K largest.
+// Entries m .. K - 1 of a row's list, where the K-th and the next share their
+// upper bits (`edge`): the largest whole values among those that do, equal
+// ones by lower expert.  It reads the row again rather than hold registers in
+// every row's way; a row needs it once in some 300 (scores as of a router of
+// 256 experts), and then mostly for one entry.
 template <int E>
-__device__ __forceinline__ void bal_select_ties(const float4 (&x)[BalShape<E>::F4], const float* lds_b, int ql, int K,
-                                                uint32_t* stage_id) {
+__device__ __forceinline__ void bal_edge(const float* src, const float* lds_b, int ql, int m, int K, uint32_t edge,
+                                         uint2* stage) {
   using S = BalShape<E>;
   constexpr int LPR = S::LPR;
-  uint32_t rem = S::V >= 32 ? ~0u : (1u << (S::V & 31)) - 1u;
-  for (int k = 0; k < K; ++k) {
-    float best = -__builtin_inff();
+  float v[S::V];
+  uint32_t rem = 0;
+#pragma unroll
+  for (int t = 0; t < S::F4; ++t) {
+    const f32x4 x = *reinterpret_cast<const f32x4*>(src + 4 * (LPR * t + ql));
+    const f32x4 bb = *reinterpret_cast<const f32x4*>(lds_b + 4 * (LPR * t + ql));
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      v[4 * t + c] = x[c] + bb[c];
+      rem |= ((__builtin_bit_cast(uint32_t, v[4 * t + c]) ^ edge) < uint32_t(E) ? 1u : 0u) << (4 * t + c);
+    }
+  }
+  for (int k = m; k < K; ++k) {
+    float best = 0.f;
     int at = E;
 #pragma unroll
-    for (int t = 0; t < S::F4; ++t) {
-      const float4 bb = *reinterpret_cast<const float4*>(lds_b + 4 * (LPR * t + ql));
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float v = comp(x[t], c) + comp(bb, c);
-        const bool take = ((rem >> (4 * t + c)) & 1u) && (v > best || at == E);
-        best = take ? v : best;
-        at = take ? 4 * (LPR * t + ql) + c : at;
-      }
+    for (int n = 0; n < S::V; ++n) {
+      const bool take = ((rem >> n) & 1u) && (at == E || v[n] > best);
+      best = take ? v[n] : best;
+      at = take ? 4 * (LPR * (n >> 2) + ql) + (n & 3) : at;
     }
     auto join = [&](float ov, int oa) {
       const bool take = oa < E && (at == E || ov > best || (ov == best && oa < at));
@@ -125,25 +178,22 @@ __device__ __forceinline__ void bal_select_ties(const float4 (&x)[BalShape<E>::F
     join(quad_mov<kQuadXor1>(best), quad_mov_i<kQuadXor1>(at));
     join(quad_mov<kQuadXor2>(best), quad_mov_i<kQuadXor2>(at));
     if constexpr (LPR >= 8) join(quad_mov<kHalfMirror>(best), quad_mov_i<kHalfMirror>(at));
-    if (at < E) {
-      const int quad = at >> 2;
-      if (quad % LPR == ql) {
-        rem &= ~(1u << (4 * (quad / LPR) + (at & 3)));
-        stage_id[k] = uint32_t(at);
-      }
+    if (at < E && (at >> 2) % LPR == ql) {
+      rem &= ~(1u << (4 * ((at >> 2) / LPR) + (at & 3)));
+      stage[k] = make_uint2(__builtin_bit_cast(uint32_t, best), uint32_t(at));
     }
   }
 }
 
 template <int E, int P, bool STATS>
-__global__ __launch_bounds__(kBalThreads) void k_balance_fwd(
+__global__ __launch_bounds__(kBalThreads, P <= 9 ? 4 : 3) void k_balance_fwd(
     const float* __restrict__ s, const float* __restrict__ b, int N, int K, const int32_t* __restrict__ seq_off, int B,
     const uint8_t* __restrict__ valid, int T, int32_t* __restrict__ topk, float* __restrict__ gate,
     float* __restrict__ psum, int32_t* __restrict__ cnt, int32_t* __restrict__ live, uint32_t* __restrict__ arrivals) {
   using S = BalShape<E>;
-  constexpr int LPR = S::LPR, F4 = S::F4, RPW = S::RPW, R = S::R;
+  constexpr int LPR = S::LPR, F4 = S::F4, RPW = S::RPW, R = S::R, KU = (P - 1 + LPR - 1) / LPR;
   __shared__ __align__(16) float lds_b[E];
-  __shared__ uint32_t stage[kBalWaves][RPW][16];   // the row's chosen experts in order
+  __shared__ uint2 stage[kBalWaves][RPW][P];  // a row's chosen biased scores and experts
   __shared__ int lds_cnt[STATS ? E : 1];
   __shared__ int lds_live[kBalWaves];
   __shared__ __align__(16) float lds_p[STATS ? kBalWaves : 1][E];
@@ -160,7 +210,7 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_fwd(
     if (blockIdx.x == 0 && tid == 0) *arrivals = 0;
   __syncthreads();
 
-  int q = seq_off ? bal_find(seq_off, B, r0) : 0;
+  int q = seq_off ? bal_find_wave(seq_off, B, r0, lane) : 0;
   for (int row0 = r0; row0 < r1;) {
     // rows [row0, end) belong to sequence q, or to none
     int end = r1, begin = 0;
@@ -173,98 +223,50 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_fwd(
         begin = q == 0 ? seq_off[0] : 0;
       }
     }
-    float4 acc[STATS ? F4 : 1];
+    f32x4 acc[STATS ? F4 : 1];
     if constexpr (STATS)
 #pragma unroll
-      for (int t = 0; t < F4; ++t) acc[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int t = 0; t < F4; ++t) acc[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
     int n_live = 0;
-    for (int rb = row0; rb < end; rb += R) {
-      if (rb + wave * RPW >= end) continue;  // nothing for this wave (no barrier below)
+    for (int rb = row0; rb + wave * RPW < end; rb += R) {  // no barrier inside
       const int row = rb + wave * RPW + rho;
       const bool here = row < end;
       const int64_t ld_row = here ? row : end - 1;
       const float* src = s + ld_row * E;
-      float4 x[F4];
+      f32x4 x[F4];
 #pragma unroll
-      for (int t = 0; t < F4; ++t) x[t] = ld4(src + 4 * (LPR * t + ql));
+      for (int t = 0; t < F4; ++t) x[t] = *reinterpret_cast<const f32x4*>(src + 4 * (LPR * t + ql));
       const bool lv = here && in_seq && row >= begin && (!valid || valid[ld_row] != 0);
+      // the P largest biased scores, each with its expert in the low bits
       float top[P];
 #pragma unroll
-      for (int k = 0; k < P; ++k) top[k] = -__builtin_inff();
+      for (int k = 0; k < P; ++k) top[k] = __builtin_bit_cast(float, 0xFF7FFFFFu & ~uint32_t(E - 1));
       float z = 0.f;
 #pragma unroll
       for (int t = 0; t < F4; ++t) {
         const float4 bb = *reinterpret_cast<const float4*>(lds_b + 4 * (LPR * t + ql));
-        top_insert<P>(top, x[t].x + bb.x);
-        top_insert<P>(top, x[t].y + bb.y);
-        top_insert<P>(top, x[t].z + bb.z);
-        top_insert<P>(top, x[t].w + bb.w);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t v = __builtin_bit_cast(uint32_t, x[t][c] + comp(bb, c));
+          top_insert<P>(top, __builtin_bit_cast(float, (v & ~uint32_t(E - 1)) | uint32_t(4 * t + c)));
+        }
         if constexpr (STATS) z += (x[t].x + x[t].y) + (x[t].z + x[t].w);
       }
+#pragma unroll
+      for (int k = 0; k < P; ++k)
+        top[k] = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, top[k]) | uint32_t(ql * S::V));
       top_merge<P, kQuadXor1>(top);
       top_merge<P, kQuadXor2>(top);
       if constexpr (LPR >= 8) top_merge<P, kHalfMirror>(top);
-      float a = top[0];
+      // the set of the K is certain unless the next one differs in the bits below only
+      uint32_t edge = 0;
       bool tie = false;
 #pragma unroll
       for (int k = 1; k < P; ++k) {
-        a = k < K ? top[k] : a;
-        tie |= k < K && top[k] == top[k - 1];
+        const uint32_t above = __builtin_bit_cast(uint32_t, top[k - 1]);
+        edge = k == K ? above : edge;
+        tie = k == K ? (__builtin_bit_cast(uint32_t, top[k]) ^ above) < uint32_t(E) : tie;
       }
-      uint32_t mem = 0;  // bit 4 t + c: expert 4 (LPR t + ql) + c is among the K largest
-#pragma unroll
-      for (int t = 0; t < F4; ++t) {
-        const float4 bb = *reinterpret_cast<const float4*>(lds_b + 4 * (LPR * t + ql));
-        mem |= (x[t].x + bb.x >= a ? 1u : 0u) << (4 * t);
-        mem |= (x[t].y + bb.y >= a ? 1u : 0u) << (4 * t + 1);
-        mem |= (x[t].z + bb.z >= a ? 1u : 0u) << (4 * t + 2);
-        mem |= (x[t].w + bb.w >= a ? 1u : 0u) << (4 * t + 3);
-      }
-      tie |= bal_row_sum_i<LPR>(__popc(mem)) != K;
-      uint32_t* mine = stage[wave][rho];
-      if (!tie) {
-        while (mem) {
-          const int bit = __builtin_ctz(mem);
-          mem &= mem - 1;
-          const int e = 4 * (LPR * (bit >> 2) + ql) + (bit & 3);
-          const float v = src[e] + lds_b[e];
-          int rank = 0;
-#pragma unroll
-          for (int k = 0; k < P; ++k) rank += (k < K && top[k] > v) ? 1 : 0;
-          mine[rank] = uint32_t(e);
-        }
-      }
-      if (__ballot(tie) != 0) {
-        // every row of the wave takes the slow way; it gives the same order
-        bal_select_ties<E>(x, lds_b, ql, K, mine);
-      }
-      __builtin_amdgcn_wave_barrier();
-      asm volatile("" ::: "memory");
-      // lane ql writes ranks ql, ql + LPR, ...
-      float sv[(16 + LPR - 1) / LPR], total = 0.f;
-      int id[(16 + LPR - 1) / LPR];
-#pragma unroll
-      for (int u = 0; u < 16 / LPR; ++u) {
-        const int k = ql + u * LPR;
-        id[u] = k < K ? int(mine[k] & uint32_t(E - 1)) : 0;
-        sv[u] = k < K ? src[id[u]] : 0.f;
-        total += sv[u];
-      }
-      total = bal_row_sum<LPR>(total);
-      const float per = total > 0.f ? 1.0f / total : 0.f;
-#pragma unroll
-      for (int u = 0; u < 16 / LPR; ++u) {
-        const int k = ql + u * LPR;
-        if (here && k < K) {
-          const int64_t o = int64_t(row) * K + k;
-          topk[o] = lv ? id[u] : -1;
-          if (gate) gate[o] = lv ? sv[u] * per : 0.f;
-          if constexpr (STATS)
-            if (lv) atomicAdd(&lds_cnt[id[u]], 1);
-        }
-      }
-      asm volatile("" ::: "memory");
-      __builtin_amdgcn_wave_barrier();
       if constexpr (STATS) {
         z = bal_row_sum<LPR>(z);
         if (lv) {  // a dead row's scores may be anything
@@ -277,8 +279,73 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_fwd(
             acc[t].w = fmaf(x[t].w, inv, acc[t].w);
           }
         }
-        n_live += lv && ql == 0 ? 1 : 0;
+        n_live += __popcll(__ballot(lv)) / LPR;
       }
+      // lane ql holds the list's entries ql, ql + LPR, ...
+      uint2* mine = stage[wave][rho];
+      float sv[KU], v[KU], total = 0.f;
+      int id[KU], rank[KU];
+#pragma unroll
+      for (int u = 0; u < KU; ++u) {
+        uint32_t m = __builtin_bit_cast(uint32_t, top[u * LPR < P ? u * LPR : 0]);
+#pragma unroll
+        for (int j = 1; j < LPR; ++j)
+          if (u * LPR + j < P) m = ql == j ? __builtin_bit_cast(uint32_t, top[u * LPR + j]) : m;
+        const int k = ql + u * LPR, n = int(m & uint32_t(S::V - 1)), from = int(m & uint32_t(E - 1)) / S::V;
+        id[u] = 4 * (LPR * (n >> 2) + from) + (n & 3);
+        sv[u] = src[id[u]];
+        v[u] = sv[u] + lds_b[id[u]];
+        if (k < K) mine[k] = make_uint2(__builtin_bit_cast(uint32_t, v[u]), uint32_t(id[u]));
+      }
+      if (__ballot(tie) != 0) {
+        if (tie) {
+          int m = 0;
+#pragma unroll
+          for (int k = 0; k < P - 1; ++k) m += k < K && (__builtin_bit_cast(uint32_t, top[k]) ^ edge) >= uint32_t(E) ? 1 : 0;
+          bal_edge<E>(src, lds_b, ql, m, K, edge, mine);
+        }
+        __builtin_amdgcn_wave_barrier();
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int u = 0; u < KU; ++u) {
+          const int k = ql + u * LPR;
+          id[u] = k < K ? int(mine[k].y & uint32_t(E - 1)) : 0;
+          sv[u] = src[id[u]];
+          v[u] = sv[u] + lds_b[id[u]];
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+      asm volatile("" ::: "memory");
+      // their order is that of the whole values, equal ones by their expert
+#pragma unroll
+      for (int u = 0; u < KU; ++u) {
+        rank[u] = 0;
+        sv[u] = ql + u * LPR < K ? sv[u] : 0.f;
+        total += sv[u];
+      }
+#pragma unroll
+      for (int j = 0; j < P - 1; ++j) {
+        if (j < K) {
+          const uint2 o = mine[j];
+          const float ov = __builtin_bit_cast(float, o.x);
+#pragma unroll
+          for (int u = 0; u < KU; ++u) rank[u] += ov > v[u] || (ov == v[u] && int(o.y) < id[u]) ? 1 : 0;
+        }
+      }
+      total = bal_row_sum<LPR>(total);
+      const float per = total > 0.f ? 1.0f / total : 0.f;
+#pragma unroll
+      for (int u = 0; u < KU; ++u) {
+        if (here && ql + u * LPR < K) {
+          const int64_t o = int64_t(row) * K + (lv ? rank[u] : ql + u * LPR);  // a dead row may hold NaN
+          topk[o] = lv ? id[u] : -1;
+          if (gate) gate[o] = lv ? sv[u] * per : 0.f;
+          if constexpr (STATS)
+            if (lv) atomicAdd(&lds_cnt[id[u]], 1);
+        }
+      }
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_wave_barrier();
     }
     if constexpr (STATS) {
       if (in_seq && end > row0) {
@@ -286,16 +353,9 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_fwd(
 #pragma unroll
         for (int t = 0; t < F4; ++t) {
 #pragma unroll
-          for (int d = LPR; d < kWave; d <<= 1) {
-            acc[t].x += __shfl_xor(acc[t].x, d);
-            acc[t].y += __shfl_xor(acc[t].y, d);
-            acc[t].z += __shfl_xor(acc[t].z, d);
-            acc[t].w += __shfl_xor(acc[t].w, d);
-          }
-          if (rho == 0) *reinterpret_cast<float4*>(&lds_p[wave][4 * (LPR * t + ql)]) = acc[t];
+          for (int c = 0; c < 4; ++c) acc[t][c] = bal_col_sum<LPR>(acc[t][c]);
+          if (rho == 0) *reinterpret_cast<f32x4*>(&lds_p[wave][4 * (LPR * t + ql)]) = acc[t];
         }
-#pragma unroll
-        for (int d = 1; d < kWave; d <<= 1) n_live += __shfl_xor(n_live, d);
         if (lane == 0) lds_live[wave] = n_live;
         __syncthreads();
         const int64_t slot = int64_t(blockIdx.x) + q;
@@ -316,12 +376,13 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_fwd(
 
 // ---------------------------------------------------------------------------
 // The sums of each sequence's slots, its weights and its share of the loss:
-// one workgroup for 16 experts of one sequence.  Every workgroup counts the
-// sequences that have a live token itself (a scan of a few live words); the
-// last one to arrive adds the shares of the loss in a fixed order.
-constexpr int kBalFinThreads = 256;
-constexpr int kBalFinWays = kBalFinThreads / 16;
-
+// one workgroup for up to 64 experts of one sequence, 16 threads an expert.
+// Every workgroup counts the sequences that have a live token itself (a scan
+// of a few live words); the last one to arrive adds the shares of the loss in
+// a fixed order.  All of it is waiting (each load is of memory that another
+// XCD wrote, and arrivals at one word pass one by one), so the loads of a
+// stage are issued together and the workgroups are few: 32 sequences of
+// 131,072 x 256 take 12 us with 512 workgroups of 16 experts.
 __device__ __forceinline__ void bal_slots(const int32_t* seq_off, int N, int T, int q, int64_t& s0, int64_t& s1) {
   int lo = 0, hi = N;
   if (seq_off) {
@@ -334,85 +395,107 @@ __device__ __forceinline__ void bal_slots(const int32_t* seq_off, int N, int T, 
   s1 = hi > lo ? int64_t((hi - 1) / T) + q + 1 : s0;
 }
 
-__global__ __launch_bounds__(kBalFinThreads) void k_balance_fin(
+__global__ __launch_bounds__(kBalFinWays* kBalFinCols) void k_balance_fin(
     const int32_t* __restrict__ seq_off, int B, int N, int E, int K, int T, float coef, const float* __restrict__ psum,
     const int32_t* __restrict__ cnt, const int32_t* __restrict__ live, double* __restrict__ part,
     uint32_t* __restrict__ arrivals, int32_t* __restrict__ count, float* __restrict__ weight,
     float* __restrict__ loss) {
-  __shared__ double sh_p[kBalFinWays][16];
-  __shared__ int sh_c[kBalFinWays][16];
+  __shared__ double sh_p[kBalFinWays * kBalFinCols];
+  __shared__ int sh_c[kBalFinWays * kBalFinCols];
   __shared__ int sh_filled, sh_tok;
   __shared__ bool sh_last;
-  const int tid = threadIdx.x, col = tid & 15, way = tid >> 4;
-  const int eg = E / 16;
-  const int q = int(blockIdx.x) / eg, e = (int(blockIdx.x) % eg) * 16 + col;
+  const int threads = int(blockDim.x), cols = threads / kBalFinWays;
+  const int tid = threadIdx.x, col = tid % cols, way = tid / cols;
+  const int eg = E / cols;
+  const int q = int(blockIdx.x) / eg, e = (int(blockIdx.x) % eg) * cols + col;
   if (tid == 0) {
     sh_filled = 0;
     sh_tok = 0;
   }
-  __syncthreads();
-  int64_t s0, s1;
+  int64_t s0, s1, a0 = 0, a1 = 0;
   bal_slots(seq_off, N, T, q, s0, s1);
+  if (tid < B) bal_slots(seq_off, N, T, tid, a0, a1);
+  // eight slots a thread, the sequence's live words and another's first one are on their way at once
+  bool any = a0 < a1 && live[a0] != 0;
   double p = 0.0;
-  int c = 0;
-  for (int64_t t = s0 + way; t < s1; t += kBalFinWays) {
-    p += double(psum[t * E + e]);
-    c += cnt[t * E + e];
+  int c = 0, tok = 0;
+  for (int64_t t = s0; t < s1; t += 8 * kBalFinWays) {
+    float pv[8];
+    int cv[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int64_t at = t + u * kBalFinWays + way, from = at < s1 ? at : s1 - 1;
+      pv[u] = psum[from * E + e];
+      cv[u] = cnt[from * E + e];
+    }
+    const int64_t mine = t + tid;
+    if (tid < 8 * kBalFinWays && mine < s1) tok += live[mine];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const bool on = t + u * kBalFinWays + way < s1;
+      p += on ? double(pv[u]) : 0.0;
+      c += on ? cv[u] : 0;
+    }
   }
-  sh_p[way][col] = p;
-  sh_c[way][col] = c;
-  int tok = 0;
-  for (int64_t t = s0 + tid; t < s1; t += kBalFinThreads) tok += live[t];
+  sh_p[tid] = p;
+  sh_c[tid] = c;
+  __syncthreads();
   if (tok) atomicAdd(&sh_tok, tok);
-  // sequences with a live token: most show one in their first slot
   int filled = 0;
-  for (int j = tid; j < B; j += kBalFinThreads) {
-    int64_t a0, a1;
-    bal_slots(seq_off, N, T, j, a0, a1);
-    bool any = false;
-    for (int64_t t = a0; t < a1 && !any; ++t) any = live[t] != 0;
+  for (int j = tid; j < B;) {
+    for (++a0; a0 < a1 && !any; ++a0) any = live[a0] != 0;
     filled += any ? 1 : 0;
+    j += threads;
+    if (j < B) {
+      bal_slots(seq_off, N, T, j, a0, a1);
+      any = a0 < a1 && live[a0] != 0;
+    }
   }
   if (filled) atomicAdd(&sh_filled, filled);
   __syncthreads();
-  if (tid < 64) {
-    double share = 0.0;
-    if (tid < 16) {
+  double share = 0.0;
+  if (tid < cols) {
 #pragma unroll
-      for (int w = 1; w < kBalFinWays; ++w) {
-        p += sh_p[w][col];
-        c += sh_c[w][col];
-      }
-      const double toks = double(sh_tok);
-      const double per = sh_tok > 0 ? 1.0 / toks : 0.0;
-      const double scale = double(coef) / double(sh_filled > 0 ? sh_filled : 1);
-      const double f = double(c) * per * (double(E) / double(K));
-      if (count) count[int64_t(q) * E + e] = c;
-      if (weight) weight[int64_t(q) * E + e] = float(scale * (f - 1.0) * per);
-      share = scale * f * p * per;
+    for (int w = 1; w < kBalFinWays; ++w) {
+      p += sh_p[w * cols + col];
+      c += sh_c[w * cols + col];
     }
-    if (loss) {
-#pragma unroll
-      for (int d = 1; d < 16; d <<= 1) share += __shfl_xor(share, d);
-      if (tid == 0) {
-        __hip_atomic_store(reinterpret_cast<unsigned long long*>(part + blockIdx.x),
-                           __builtin_bit_cast(unsigned long long, share), __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT);
-        sh_last = __hip_atomic_fetch_add(arrivals, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
-      }
-    }
+    const double toks = double(sh_tok);
+    const double per = sh_tok > 0 ? 1.0 / toks : 0.0;
+    const double scale = double(coef) / double(sh_filled > 0 ? sh_filled : 1);
+    const double f = double(c) * per * (double(E) / double(K));
+    if (count) count[int64_t(q) * E + e] = c;
+    if (weight) weight[int64_t(q) * E + e] = float(scale * (f - 1.0) * per);
+    share = scale * f * p * per;
   }
   if (!loss) return;
+  if (tid < kWave) {
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) share += __shfl_xor(share, d);
+    if (tid == 0) {
+      // The share and the counter are the only words that cross workgroups,
+      // and both are atomics of the whole GPU, which no cache holds back;
+      // that the share is there before the count is this wait.  (A release
+      // would write back the XCD's whole L2.)
+      __hip_atomic_store(reinterpret_cast<unsigned long long*>(part + blockIdx.x),
+                         __builtin_bit_cast(unsigned long long, share), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      sh_last = __hip_atomic_fetch_add(arrivals, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+    }
+  }
   __syncthreads();
   if (!sh_last) return;
   double sum = 0.0;
-  for (int i = tid; i < int(gridDim.x); i += kBalFinThreads)
+  for (int i = tid; i < int(gridDim.x); i += threads)
     sum += __builtin_bit_cast(double, __hip_atomic_load(reinterpret_cast<unsigned long long*>(part + i),
-                                                        __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_AGENT));
-  sh_p[way][col] = sum;
+                                                        __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) sum += __shfl_xor(sum, d);
+  if ((tid & 63) == 0) sh_p[tid >> 6] = sum;
   __syncthreads();
   if (tid == 0) {
     double all = 0.0;
-    for (int i = 0; i < kBalFinThreads; ++i) all += sh_p[i >> 4][i & 15];
+    for (int w = 0; w < threads / kWave; ++w) all += sh_p[w];
     *loss = float(all);
   }
 }
@@ -448,7 +531,10 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_bwd(
     bool lv = !valid || valid[lr] != 0;
     int q = 0;
     if (seq_off) {
-      q = bal_find(seq_off, B, int(lr));
+      // nearly always one sequence holds all of the wave's rows
+      const int64_t w0 = rb + wave * RPW, w1 = (w0 + RPW < N ? w0 + RPW : int64_t(N)) - 1;
+      q = bal_find_wave(seq_off, B, int(w0), lane);
+      if (q < B && seq_off[q + 1] <= w1) q = bal_find(seq_off, B, int(lr));
       lv = lv && q < B && lr >= seq_off[0];
       q = q < B ? q : B - 1;
     }
@@ -537,9 +623,10 @@ static int fwd_ep(const BalFwd& a, const BalWs& w, hipStream_t st) {
 
 template <int E>
 static int fwd_e(const BalFwd& a, const BalWs& w, hipStream_t st) {
-  // lists of the next of 4, 8 and 16 slots at or above K
-  if (a.K <= 4) return fwd_ep<E, 4>(a, w, st);
-  if (a.K <= 8) return fwd_ep<E, 8>(a, w, st);
+  // lists of the next of 4, 7, 9 and 16 entries above K
+  if (a.K <= 3) return fwd_ep<E, 4>(a, w, st);
+  if (a.K <= 6) return fwd_ep<E, 7>(a, w, st);
+  if (a.K <= 8) return fwd_ep<E, 9>(a, w, st);
   return fwd_ep<E, 16>(a, w, st);
 }
 
@@ -555,7 +642,8 @@ int launch_balance_fwd(const BalFwd& a, hipStream_t st) {
   }
   if (rc != int(hipSuccess) || !a.ws) return rc;
   uint8_t* ws = a.ws;
-  hipLaunchKernelGGL(k_balance_fin, dim3(unsigned(w.groups)), dim3(kBalFinThreads), 0, st, a.seq_off, a.B, int(a.N),
+  hipLaunchKernelGGL(k_balance_fin, dim3(unsigned(w.groups)), dim3(kBalFinWays * bal_fin_cols(a.E)), 0,
+                     st, a.seq_off, a.B, int(a.N),
                      a.E, a.K, w.T, a.coef, reinterpret_cast<const float*>(ws + w.psum),
                      reinterpret_cast<const int32_t*>(ws + w.cnt), reinterpret_cast<const int32_t*>(ws + w.live),
                      reinterpret_cast<double*>(ws + w.part), reinterpret_cast<uint32_t*>(ws), a.count, a.weight,
