@@ -85,6 +85,58 @@ __device__ __forceinline__ float bal_col_sum(float x) {
   return x + bal_swapped<32>(x);
 }
 
+// The larger and the smaller of two packed scores.  As medians with the type's
+// ends: fmaxf would first quiet each operand, which comes from an integer and
+// might be a signalling NaN for all the compiler knows (90 of the 810
+// instructions of a wave's step).
+constexpr float kBalMost = 3.4028234663852886e38f;
+__device__ __forceinline__ float bal_max(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, kBalMost); }
+__device__ __forceinline__ float bal_min(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, -kBalMost); }
+
+// v into a descending list (its least entry leaves).
+template <int P>
+__device__ __forceinline__ void bal_insert(float (&t)[P], float v) {
+#pragma unroll
+  for (int k = P - 1; k > 0; --k) t[k] = __builtin_amdgcn_fmed3f(v, t[k - 1], t[k]);
+  t[0] = bal_max(v, t[0]);
+}
+
+// One stage at distance D of a bitonic merge of the last P of W entries, the
+// others counting as infinite.
+template <int P, int W, int D>
+__device__ __forceinline__ void bal_stage(float (&c)[P]) {
+  if constexpr (D >= 1) {
+#pragma unroll
+    for (int i = W - P; i < W; ++i)
+      if ((i & D) == 0) {
+        float &a = c[i - (W - P)], &b = c[i + D - (W - P)];
+        const float hi = bal_max(a, b);
+        b = bal_min(a, b);
+        a = hi;
+      }
+    bal_stage<P, W, D / 2>(c);
+  }
+}
+
+// This lane's list and the partner's into the P largest of both: the larger
+// of entry k here and entry P - 1 - k there are those, first falling, then
+// rising.
+template <int P, int CTRL>
+__device__ __forceinline__ void bal_merge(float (&t)[P]) {
+  constexpr int W = P <= 4 ? 4 : (P <= 8 ? 8 : 16);
+  float c[P];
+#pragma unroll
+  for (int k = 0; k < P; ++k) c[k] = bal_max(t[k], quad_mov<CTRL>(t[P - 1 - k]));
+  bal_stage<P, W, W / 2>(c);
+#pragma unroll
+  for (int k = 0; k < P; ++k) t[k] = c[k];
+}
+
+// What a row is multiplied by before it is divided by this sum of its scores:
+// a sum below 2^-100 (all of them far down the sigmoid) may have no inverse in
+// 32 bits.  1 - s is 1 in such a row.
+__device__ __forceinline__ float bal_up(float sum) { return sum < 0x1p-100f ? 0x1p100f : 1.0f; }
+
 // The sequence that row r belongs to: the number of ends off[1..B] at or
 // below r (B: past the last sequence).  off need not be sorted for this to
 // stay within [0, B].
@@ -149,26 +201,28 @@ __device__ __forceinline__ void bal_edge(const float* src, const float* lds_b, i
                                          uint2* stage) {
   using S = BalShape<E>;
   constexpr int LPR = S::LPR;
-  float v[S::V];
-  uint32_t rem = 0;
-#pragma unroll
-  for (int t = 0; t < S::F4; ++t) {
-    const f32x4 x = *reinterpret_cast<const f32x4*>(src + 4 * (LPR * t + ql));
-    const f32x4 bb = *reinterpret_cast<const f32x4*>(lds_b + 4 * (LPR * t + ql));
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      v[4 * t + c] = x[c] + bb[c];
-      rem |= ((__builtin_bit_cast(uint32_t, v[4 * t + c]) ^ edge) < uint32_t(E) ? 1u : 0u) << (4 * t + c);
-    }
-  }
+  constexpr int STEP = S::F4 < 4 ? S::F4 : 4;
+  uint32_t rem = ~0u;
   for (int k = m; k < K; ++k) {
     float best = 0.f;
     int at = E;
+#pragma unroll 1
+    for (int t0 = 0; t0 < S::F4; t0 += STEP) {
+      f32x4 v[STEP];
 #pragma unroll
-    for (int n = 0; n < S::V; ++n) {
-      const bool take = ((rem >> n) & 1u) && (at == E || v[n] > best);
-      best = take ? v[n] : best;
-      at = take ? 4 * (LPR * (n >> 2) + ql) + (n & 3) : at;
+      for (int t = 0; t < STEP; ++t) v[t] = *reinterpret_cast<const f32x4*>(src + 4 * (LPR * (t0 + t) + ql));
+#pragma unroll
+      for (int t = 0; t < STEP; ++t) {
+        const f32x4 bb = *reinterpret_cast<const f32x4*>(lds_b + 4 * (LPR * (t0 + t) + ql));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float w = v[t][c] + bb[c];
+          const bool take = (__builtin_bit_cast(uint32_t, w) ^ edge) < uint32_t(E) &&
+                            ((rem >> (4 * (t0 + t) + c)) & 1u) && (at == E || w > best);
+          best = take ? w : best;
+          at = take ? 4 * (LPR * (t0 + t) + ql) + c : at;
+        }
+      }
     }
     auto join = [&](float ov, int oa) {
       const bool take = oa < E && (at == E || ov > best || (ov == best && oa < at));
@@ -196,7 +250,7 @@ __global__ __launch_bounds__(kBalThreads, P <= 9 ? 4 : 3) void k_balance_fwd(
   __shared__ uint2 stage[kBalWaves][RPW][P];  // a row's chosen biased scores and experts
   __shared__ int lds_cnt[STATS ? E : 1];
   __shared__ int lds_live[kBalWaves];
-  __shared__ __align__(16) float lds_p[STATS ? kBalWaves : 1][E];
+  __shared__ __align__(16) float lds_p[kBalWaves][STATS ? E : 4];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int rho = lane / LPR, ql = lane % LPR;
@@ -210,35 +264,64 @@ __global__ __launch_bounds__(kBalThreads, P <= 9 ? 4 : 3) void k_balance_fwd(
     if (blockIdx.x == 0 && tid == 0) *arrivals = 0;
   __syncthreads();
 
-  int q = seq_off ? bal_find_wave(seq_off, B, r0, lane) : 0;
-  for (int row0 = r0; row0 < r1;) {
-    // rows [row0, end) belong to sequence q, or to none
-    int end = r1, begin = 0;
-    bool in_seq = true;
-    if (seq_off) {
-      in_seq = q < B;
-      if (in_seq) {
-        end = seq_off[q + 1];
-        end = end < r1 ? end : r1;
-        begin = q == 0 ? seq_off[0] : 0;
-      }
-    }
-    f32x4 acc[STATS ? F4 : 1];
-    if constexpr (STATS)
+  // The sequence whose rows come next.  A chunk's rows are taken step by step
+  // whatever sequences they belong to, so that short sequences share a step's
+  // reading and sorting; q's sums are written once its end is passed.
+  const int first = seq_off ? seq_off[0] : 0, last = seq_off ? seq_off[B] : N;
+  struct Run {
+    int q, begin, end;  // begin: its first row in this chunk
+  };
+  auto end_of = [&](int i) { return seq_off && i < B ? seq_off[i + 1] : N; };
+  const int q0 = seq_off ? bal_find_wave(seq_off, B, r0, lane) : 0;
+  Run now{q0, r0, end_of(q0)};
+  f32x4 acc[STATS ? F4 : 1];
+  int n_live = 0;
+  if constexpr (STATS)
 #pragma unroll
-      for (int t = 0; t < F4; ++t) acc[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    int n_live = 0;
-    for (int rb = row0; rb + wave * RPW < end; rb += R) {  // no barrier inside
-      const int row = rb + wave * RPW + rho;
-      const bool here = row < end;
-      const int64_t ld_row = here ? row : end - 1;
-      const float* src = s + ld_row * E;
+    for (int t = 0; t < F4; ++t) acc[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  // this chunk's sum of p of sequence i: the lanes of one wave that hold the same columns, then the waves
+  auto write_p = [&](int i) {
+#pragma unroll
+    for (int t = 0; t < F4; ++t) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[t][c] = bal_col_sum<LPR>(acc[t][c]);
+      if (rho == 0) *reinterpret_cast<f32x4*>(&lds_p[wave][4 * (LPR * t + ql)]) = acc[t];
+      acc[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    }
+    __syncthreads();
+    const int64_t slot = int64_t(blockIdx.x) + i;
+    for (int j = tid; j < E; j += kBalThreads)
+      psum[slot * E + j] = (lds_p[0][j] + lds_p[1][j]) + (lds_p[2][j] + lds_p[3][j]);
+    __syncthreads();
+  };
+  auto write_count = [&](int i) {
+    if (lane == 0) lds_live[wave] = n_live;
+    n_live = 0;
+    __syncthreads();
+    const int64_t slot = int64_t(blockIdx.x) + i;
+    for (int j = tid; j < E; j += kBalThreads) {
+      cnt[slot * E + j] = lds_cnt[j];
+      lds_cnt[j] = 0;
+    }
+    if (tid == 0) live[slot] = (lds_live[0] + lds_live[1]) + (lds_live[2] + lds_live[3]);
+    __syncthreads();
+  };
+  for (int rb = r0; rb < r1; rb += R) {
+    const int step_end = rb + R < r1 ? rb + R : r1;
+    const bool busy = rb + wave * RPW < step_end;
+    const int row = rb + wave * RPW + rho;
+    const bool here = row < step_end;
+    const int64_t ld_row = here ? row : r1 - 1;
+    const float* src = s + ld_row * E;
+    const bool lv = here && row >= first && row < last && (!valid || valid[ld_row] != 0);
+    const bool whole = now.end >= step_end;  // the step's rows are all of one sequence
+    Run now_p = now;
+    float top[P], inv = 0.f, up = 1.0f;
+    if (busy) {
       f32x4 x[F4];
 #pragma unroll
       for (int t = 0; t < F4; ++t) x[t] = *reinterpret_cast<const f32x4*>(src + 4 * (LPR * t + ql));
-      const bool lv = here && in_seq && row >= begin && (!valid || valid[ld_row] != 0);
       // the P largest biased scores, each with its expert in the low bits
-      float top[P];
 #pragma unroll
       for (int k = 0; k < P; ++k) top[k] = __builtin_bit_cast(float, 0xFF7FFFFFu & ~uint32_t(E - 1));
       float z = 0.f;
@@ -248,16 +331,56 @@ __global__ __launch_bounds__(kBalThreads, P <= 9 ? 4 : 3) void k_balance_fwd(
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const uint32_t v = __builtin_bit_cast(uint32_t, x[t][c] + comp(bb, c));
-          top_insert<P>(top, __builtin_bit_cast(float, (v & ~uint32_t(E - 1)) | uint32_t(4 * t + c)));
+          bal_insert<P>(top, __builtin_bit_cast(float, (v & ~uint32_t(E - 1)) | uint32_t(4 * t + c)));
         }
         if constexpr (STATS) z += (x[t].x + x[t].y) + (x[t].z + x[t].w);
       }
 #pragma unroll
       for (int k = 0; k < P; ++k)
         top[k] = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, top[k]) | uint32_t(ql * S::V));
-      top_merge<P, kQuadXor1>(top);
-      top_merge<P, kQuadXor2>(top);
-      if constexpr (LPR >= 8) top_merge<P, kHalfMirror>(top);
+      bal_merge<P, kQuadXor1>(top);
+      bal_merge<P, kQuadXor2>(top);
+      if constexpr (LPR >= 8) bal_merge<P, kHalfMirror>(top);
+      if constexpr (STATS) {
+        z = bal_row_sum<LPR>(z);
+        up = bal_up(z);
+        inv = z > 0.f ? 1.0f / (z * up) : 0.f;
+        if (up != 1.0f)
+#pragma unroll
+          for (int t = 0; t < F4; ++t) x[t] *= up;
+        if (whole && lv)  // a dead row's scores may be anything
+#pragma unroll
+          for (int t = 0; t < F4; ++t)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[t][c] = fmaf(x[t][c], inv, acc[t][c]);
+      }
+    }
+    // The step's rows to their sequences: `add` takes those of i, `write` what
+    // the chunk held of i, once its end or the chunk's is passed.
+    auto deal = [&](auto&& add, auto&& write, Run& g) {
+      for (int from = rb;;) {
+        add(row >= from && row < g.end);
+        if (g.end >= step_end && step_end < r1) break;
+        if (g.q < B && (g.end < r1 ? g.end : r1) > g.begin) write(g.q);
+        if (g.end >= step_end) break;
+        from = g.end > from ? g.end : from;
+        g = {g.q + 1, from, end_of(g.q + 1)};
+      }
+    };
+    if constexpr (STATS)
+      deal(
+          [&](bool mine) {
+            if (!whole && busy && mine && lv)  // the rows are read again: kept, they would cost the sorting its registers
+#pragma unroll
+              for (int t = 0; t < F4; ++t) {
+                const f32x4 x = *reinterpret_cast<const f32x4*>(src + 4 * (LPR * t + ql));
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[t][c] = fmaf(x[c] * up, inv, acc[t][c]);
+              }
+          },
+          write_p, now_p);
+    int id[KU];
+    if (busy) {
       // the set of the K is certain unless the next one differs in the bits below only
       uint32_t edge = 0;
       bool tie = false;
@@ -267,24 +390,10 @@ __global__ __launch_bounds__(kBalThreads, P <= 9 ? 4 : 3) void k_balance_fwd(
         edge = k == K ? above : edge;
         tie = k == K ? (__builtin_bit_cast(uint32_t, top[k]) ^ above) < uint32_t(E) : tie;
       }
-      if constexpr (STATS) {
-        z = bal_row_sum<LPR>(z);
-        if (lv) {  // a dead row's scores may be anything
-          const float inv = z > 0.f ? 1.0f / z : 0.f;
-#pragma unroll
-          for (int t = 0; t < F4; ++t) {
-            acc[t].x = fmaf(x[t].x, inv, acc[t].x);
-            acc[t].y = fmaf(x[t].y, inv, acc[t].y);
-            acc[t].z = fmaf(x[t].z, inv, acc[t].z);
-            acc[t].w = fmaf(x[t].w, inv, acc[t].w);
-          }
-        }
-        n_live += __popcll(__ballot(lv)) / LPR;
-      }
       // lane ql holds the list's entries ql, ql + LPR, ...
       uint2* mine = stage[wave][rho];
       float sv[KU], v[KU], total = 0.f;
-      int id[KU], rank[KU];
+      int rank[KU];
 #pragma unroll
       for (int u = 0; u < KU; ++u) {
         uint32_t m = __builtin_bit_cast(uint32_t, top[u * LPR < P ? u * LPR : 0]);
@@ -333,44 +442,30 @@ __global__ __launch_bounds__(kBalThreads, P <= 9 ? 4 : 3) void k_balance_fwd(
         }
       }
       total = bal_row_sum<LPR>(total);
-      const float per = total > 0.f ? 1.0f / total : 0.f;
+      const float c = bal_up(total), per = total > 0.f ? 1.0f / (total * c) : 0.f;
 #pragma unroll
       for (int u = 0; u < KU; ++u) {
         if (here && ql + u * LPR < K) {
           const int64_t o = int64_t(row) * K + (lv ? rank[u] : ql + u * LPR);  // a dead row may hold NaN
           topk[o] = lv ? id[u] : -1;
-          if (gate) gate[o] = lv ? sv[u] * per : 0.f;
-          if constexpr (STATS)
-            if (lv) atomicAdd(&lds_cnt[id[u]], 1);
+          if (gate) gate[o] = lv ? sv[u] * c * per : 0.f;
         }
       }
       asm volatile("" ::: "memory");
       __builtin_amdgcn_wave_barrier();
     }
     if constexpr (STATS) {
-      if (in_seq && end > row0) {
-        // the lanes of one wave that hold the same columns, then the waves
+      deal(
+          [&](bool mine) {
+            const bool on = mine && lv;
+            n_live += __popcll(__ballot(on)) / LPR;
+            if (busy && on)
 #pragma unroll
-        for (int t = 0; t < F4; ++t) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) acc[t][c] = bal_col_sum<LPR>(acc[t][c]);
-          if (rho == 0) *reinterpret_cast<f32x4*>(&lds_p[wave][4 * (LPR * t + ql)]) = acc[t];
-        }
-        if (lane == 0) lds_live[wave] = n_live;
-        __syncthreads();
-        const int64_t slot = int64_t(blockIdx.x) + q;
-        for (int j = tid; j < E; j += kBalThreads) {
-          psum[slot * E + j] = (lds_p[0][j] + lds_p[1][j]) + (lds_p[2][j] + lds_p[3][j]);
-          cnt[slot * E + j] = lds_cnt[j];
-          lds_cnt[j] = 0;
-        }
-        if (tid == 0) live[slot] = (lds_live[0] + lds_live[1]) + (lds_live[2] + lds_live[3]);
-        __syncthreads();
-      }
+              for (int u = 0; u < KU; ++u)
+                if (ql + u * LPR < K) atomicAdd(&lds_cnt[id[u]], 1);
+          },
+          write_count, now);
     }
-    row0 = end > row0 ? end : row0;
-    ++q;
-    if (!in_seq) break;
   }
 }
 
@@ -525,9 +620,9 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_bwd(
     const bool here = row < N;
     const int64_t lr = here ? row : N - 1;
     const float* src = s + lr * E;
-    float4 x[F4];
+    f32x4 x[F4];
 #pragma unroll
-    for (int t = 0; t < F4; ++t) x[t] = ld4(src + 4 * (LPR * t + ql));
+    for (int t = 0; t < F4; ++t) x[t] = *reinterpret_cast<const f32x4*>(src + 4 * (LPR * t + ql));
     bool lv = !valid || valid[lr] != 0;
     int q = 0;
     if (seq_off) {
@@ -550,25 +645,28 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_bwd(
         sv[u] = on ? src[id[u]] : 0.f;
         dg[u] = on ? dgate[lr * K + k] : 0.f;
         total += sv[u];
-        inner = fmaf(dg[u], sv[u], inner);
       }
       total = bal_row_sum<LPR>(total);
+      const float c = bal_up(total), per = total > 0.f ? 1.0f / (total * c) : 0.f;
+#pragma unroll
+      for (int u = 0; u < KU; ++u) {
+        sv[u] *= c * per;  // the gate
+        inner = fmaf(dg[u], sv[u], inner);
+      }
       inner = bal_row_sum<LPR>(inner);
-      const float per = total > 0.f ? 1.0f / total : 0.f;
-      inner *= per;
 #pragma unroll
       for (int u = 0; u < KU; ++u)
-        if (id[u] >= 0) mine[id[u]] = (dg[u] - inner) * per;
+        if (id[u] >= 0) mine[id[u]] = (dg[u] - inner) * sv[u];
     }
     __builtin_amdgcn_wave_barrier();
     asm volatile("" ::: "memory");
     float z = 0.f, dot = 0.f;
-    float4 w[F4];
+    f32x4 w[F4];
     if (weight) {
       const float* wr = weight + int64_t(q) * E;
 #pragma unroll
       for (int t = 0; t < F4; ++t) {
-        w[t] = ld4(wr + 4 * (LPR * t + ql));
+        w[t] = *reinterpret_cast<const f32x4*>(wr + 4 * (LPR * t + ql));
         z += (x[t].x + x[t].y) + (x[t].z + x[t].w);
         dot = fmaf(w[t].x, x[t].x, dot);
         dot = fmaf(w[t].y, x[t].y, dot);
@@ -579,20 +677,33 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_bwd(
       dot = bal_row_sum<LPR>(dot);
     } else {
 #pragma unroll
-      for (int t = 0; t < F4; ++t) w[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int t = 0; t < F4; ++t) w[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
     }
-    const float inv = lv && z > 0.f ? 1.0f / z : 0.f;
+    const float up = weight ? bal_up(z) : 1.0f;
+    if (up != 1.0f) {
+      dot = 0.f;
+#pragma unroll
+      for (int t = 0; t < F4; ++t)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          x[t][c] *= up;
+          dot = fmaf(w[t][c], x[t][c], dot);
+        }
+      dot = bal_row_sum<LPR>(dot);
+    }
+    const float inv = lv && z > 0.f ? 1.0f / (z * up) : 0.f;
     const float mean = dot * inv, scale = dl * inv;
 #pragma unroll
     for (int t = 0; t < F4; ++t) {
-      float4 g = dgate ? *reinterpret_cast<const float4*>(mine + 4 * (LPR * t + ql)) : make_float4(0.f, 0.f, 0.f, 0.f);
-      float4 o;
-      o.x = fmaf(w[t].x - mean, scale, g.x) * (x[t].x * (1.0f - x[t].x));
-      o.y = fmaf(w[t].y - mean, scale, g.y) * (x[t].y * (1.0f - x[t].y));
-      o.z = fmaf(w[t].z - mean, scale, g.z) * (x[t].z * (1.0f - x[t].z));
-      o.w = fmaf(w[t].w - mean, scale, g.w) * (x[t].w * (1.0f - x[t].w));
-      if (!lv) o = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (here) *reinterpret_cast<float4*>(dlogits + row * E + 4 * (LPR * t + ql)) = o;
+      f32x4 g = (f32x4){0.f, 0.f, 0.f, 0.f}, o;
+      if (dgate) g = *reinterpret_cast<const f32x4*>(mine + 4 * (LPR * t + ql));
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float rest = up != 1.0f ? 1.0f : 1.0f - x[t][c];
+        o[c] = fmaf((w[t][c] - mean) * scale, x[t][c] * rest, g[c] * rest);
+      }
+      if (!lv) o = (f32x4){0.f, 0.f, 0.f, 0.f};
+      if (here) *reinterpret_cast<f32x4*>(dlogits + row * E + 4 * (LPR * t + ql)) = o;
     }
     asm volatile("" ::: "memory");
     __builtin_amdgcn_wave_barrier();

@@ -303,3 +303,45 @@ def test_graph_replays_on_another_stream():
         for name, a, t in zip(("topk", "gate", "count", "weight", "loss", "dlogits"), got,
                               (topk, gate, count, weight, loss, dx)):
             G.assert_same(f"replay {seed} {name}", a, G.host(t))
+
+
+@pytest.mark.parametrize("E,K", [(16, 3), (32, 8), (64, 7), (128, 15), (256, 1), (256, 6), (256, 8), (256, 15)])
+def test_values_that_differ_in_their_last_bits(E, K):
+    """Every row's scores lie within 64 float32 steps of each other, so the
+    order is decided below any coarser key; half of the rows are separated
+    again by the bias."""
+    rng = np.random.default_rng(E + K)
+    N = 301
+    s = (0.5 + 2.0 ** -24 * rng.integers(0, 65, (N, E))).astype(np.float32)
+    s[::3] -= np.float32(0.25)
+    s[1::3] = (2.0 ** -140 * rng.integers(0, 9, s[1::3].shape)).astype(np.float32)    # subnormal, and zeros
+    G.say(f"balance last bits E={E} K={K}")
+    everything(s, np.zeros(E, np.float32), K, [0, 7, 300])
+    b = np.where(rng.random(E) < 0.5, 0.25, 0.0).astype(np.float32)
+    s[1::3] = scores(rng, len(s[1::3]), E)
+    everything(s, b, K, [0, 7, 300])
+
+
+@pytest.mark.parametrize("E,K,allowed", [(16, 4, 1), (64, 6, 3), (256, 8, 0), (256, 6, 6), (128, 15, 16)])
+def test_experts_barred_by_the_lowest_value(E, K, allowed):
+    """A bias of the lowest float32 bars an expert; with fewer experts left
+    than K the barred ones follow by index (their sums are all that value)."""
+    rng = np.random.default_rng(E + allowed)
+    b = np.full(E, np.finfo(np.float32).min, np.float32)
+    b[rng.permutation(E)[:allowed]] = 0.1
+    G.say(f"balance barred E={E} K={K} allowed={allowed}")
+    everything(scores(rng, 205, E), b, K, [0, 100, 205])
+
+
+@pytest.mark.parametrize("E,K", [(32, 4), (128, 6), (256, 6)])
+@pytest.mark.parametrize("N", [31, 500, 33000])
+def test_short_sequences(E, K, N):
+    """Sequences of one to five tokens with empty ones among them, so that one
+    workgroup's rows end many; at 33,000 tokens a workgroup takes several steps."""
+    rng = np.random.default_rng(E + N)
+    lengths = rng.integers(0, 6, 3 * N // 10)
+    off = [0] + [int(x) for x in np.minimum(np.cumsum(lengths), N)]
+    off += [off[-1], N]
+    valid = (rng.random(N) > 0.2).astype(np.uint8)
+    G.say(f"balance short sequences N={N} E={E} B={len(off) - 1}")
+    everything(scores(rng, N, E), rng.uniform(-0.1, 0.1, E).astype(np.float32), K, off, valid)
