@@ -835,14 +835,34 @@ static int gemm_thin(const Gemm& g, hipStream_t st) {
   return int(hipGetLastError());
 }
 
+// How many waves share a column tile's K: as many as give every CU a
+// workgroup, and two where a wave's part is then still four blocks long (one
+// token through 4096 x 4096: 20.5, 11.6, 7.4, 5.2 us with 1, 2, 4, 8; 128 rows
+// over 256 experts of 1024 x 2048: 47, 44, 50, 90, since each workgroup of
+// eight has so little of the weight that finding its tile counts).
+template <int MT>
+static int gemm_few(const Gemm& g, hipStream_t st) {
+  const int64_t waves = row_tiles(g, 16 * MT) * ((g.N + 15) / 16);
+  int kw = g.ldk >= 8 * kQBlock ? 2 : 1;
+  while (kw < 8 && waves * kw < 8 * int64_t(device_cu_count())) kw *= 2;
+  switch (kw) {
+    case 1: return gemm_thin<MT, 1>(g, st);
+    case 2: return gemm_thin<MT, 2>(g, st);
+    case 4: return gemm_thin<MT, 4>(g, st);
+    default: return gemm_thin<MT, 8>(g, st);
+  }
+}
+
 int launch_fp8_product(const uint8_t* xq, const uint8_t* xs, const uint8_t* w, const uint8_t* ws, int64_t M, int N,
                        int64_t ldk, const int32_t* off, int G, bool exact, uint16_t* y, hipStream_t st) {
   const Gemm g{xq, xs, w, ws, M, N, ldk, fp8_sld(ldk), off, G, y};
   const int64_t rows = off ? (M + G - 1) / G : M;  // rows of an expert, on average
-  if (rows <= 64) {
-    if (rows <= 16) return gemm_thin<1, 8>(g, st);
-    if (rows <= 32) return gemm_thin<2, 8>(g, st);
-    return gemm_thin<4, 8>(g, st);
+  // few rows and too few tiles for the CUs: one wave's 16 columns at a time (64 rows, 4096 x 4096: 16.3 us, tiles
+  // 21.8; 64 rows over 16 experts of 1024 x 2048: 10.1, tiles 13.0, but 1024 rows over them 46, tiles 15)
+  if (rows <= 64 && row_tiles(g, 128) * ((N + 127) / 128) <= device_cu_count() / 2) {
+    if (rows <= 16) return gemm_few<1>(g, st);
+    if (rows <= 32) return gemm_few<2>(g, st);
+    return gemm_few<4>(g, st);
   }
   if (row_tiles(g, 256) * ((N + 255) / 256) >= QB_F8_WIDE)
     return exact ? gemm_tiled<256, 256, 2, 4, false, true>(g, st) : gemm_tiled<256, 256, 2, 4, false, false>(g, st);
