@@ -35,6 +35,7 @@
 //     keeps 32 bits, and the products of few rows, where the weight's bytes
 //     cost more than either instruction, always use it.
 #include <algorithm>
+#include <type_traits>
 
 #include "qb_device.hpp"
 #include "qb_internal.hpp"
@@ -428,12 +429,47 @@ __device__ __forceinline__ Tile group_find(int t, int lane, const int (&lo)[4], 
   return r;
 }
 
-// Workgroups are dealt out to the 8 XCDs in turn; each XCD takes a
-// consecutive stretch of the tiles, so the tiles in flight on one L2 share
-// rows.  A permutation of [0, n).
-__device__ __forceinline__ int xcd_tile(int b, int n) {
-  const int per = n / 8, more = n % 8, x = b % 8, i = b / 8;
-  return x * per + (x < more ? x : more) + i;
+// Workgroups are dealt out to the 8 XCDs in turn, and each takes every
+// grid'th number; each XCD takes a consecutive stretch of the tiles, so the
+// tiles in flight on one L2 share rows.  A permutation of [0, n).
+__device__ __forceinline__ int tile_at(int i, int grid, int n) {
+  // numbers of XCD x: those i < n with (i mod grid) mod 8 = x
+  const int x = (i % grid) % 8, full = n / grid, rest = n % grid;
+  auto of = [&](int y) { return full * ((grid + 7 - y) / 8) + (rest + 7 - y) / 8; };
+  int first = 0;
+#pragma unroll
+  for (int y = 0; y < 8; ++y) first += y < x ? of(y) : 0;
+  return first + (i / grid) * ((grid + 7 - x) / 8) + (i % grid) / 8;
+}
+
+// The same for experts whose sums are of unequal length: the XCDs take turns
+// at chunks of C tiles, so that a long expert's do not all fall to one of them
+// (one of 16 experts with all of 2048 rows, 768 x 1152: 59 us with stretches).
+template <int C>
+__device__ __forceinline__ int tile_in_turn(int i, int n) {
+  const int s = i / 8;
+  return i < n / (8 * C) * (8 * C) ? ((s / C) * 8 + i % 8) * C + s % C : i;
+}
+
+// s_waitcnt's immediate: at most n vector memory operations outstanding, and
+// every LDS read back.
+constexpr int vm_count(int n) { return 0x0070 | (n & 15) | ((n >> 4) << 14); }
+
+// Zeros in rows m0 .. (below M) and columns n0 .. (below N) of a tile.
+template <int BM, int BN, int W>
+__device__ __forceinline__ void zero_tile(float* out, int64_t out_row, int64_t m0, int64_t M, int n0, int N, int tid) {
+  const Float4 zero = {};
+  for (int i = tid; i < BM * BN / 4; i += W * kWave) {
+    const int64_t row = m0 + i / (BN / 4);
+    const int col = n0 + i % (BN / 4) * 4;
+    if (row >= M) break;
+    float* o = out + (out_row + row) * N + col;
+    if (col + 3 < N) {
+      *reinterpret_cast<Float4*>(o) = zero;
+    } else {
+      for (int c = 0; col + c < N; ++c) o[c] = 0.f;
+    }
+  }
 }
 
 // Tiles in groups of GM rows of tiles, column by column inside a group.
@@ -447,235 +483,404 @@ __device__ __forceinline__ void tile_order(int t, int tm_all, int tn_all, int GM
 // ---------------------------------------------------------------------------
 // the tiled product
 
-// A workgroup computes BM x BN of the result from an LDS ring of two stages
-// of 128 bytes of K, filled by loads that go to LDS directly; the waves tile
-// it WM x WN.  A row's 128 bytes are 8 slots of 16, XORed with (row / 2) mod
-// 8, so 16 lanes reading one slot number of 16 rows touch all banks once.
-// The scales of four blocks of K are one word a row, staged beside the tiles.
-// GRAD: the weight gradient (float out, K = an expert's rows, every expert's
-// output is written); else the product (bf16 out, an expert's rows tiled).
-template <int BM, int BN, int WM, int WN, bool GRAD, bool EXACT>
-__global__ __launch_bounds__(WM* WN* kWave) void k_fp8_gemm(const uint8_t* __restrict__ A,
+// A workgroup computes BM x BN tiles of the result from an LDS ring of S
+// stages of 128 bytes of K, filled by loads that go to LDS directly; the waves
+// tile it WM x WN.  It takes one tile after another (XCD by XCD, see
+// tile_at), and the loads run ahead of the products over the end of a tile,
+// so that only the first tile of a workgroup waits for its operands and its
+// results leave beside the next one's.  GRAD: the weight gradient (float out,
+// K = an expert's rows, every expert's output is written); else the product
+// (bf16 out, an expert's rows tiled).
+//
+// A row's 128 bytes are 8 slots of 16, XORed with a number of the row's, so
+// that the 16 rows that the lanes of a quarter wave read in one slot lie in
+// all banks once (two rows fill them).  For float results a wave's column
+// tile j holds columns 16 j .. 16 j + 15: lane groups g of 16 lanes write 16
+// bytes side by side.  For bf16 results column tile j takes columns 16 g + 4
+// j + c instead, so that a lane ends up with 16 columns side by side, 32
+// bytes, and four lanes with a row's 128.
+//
+// S = 2, where every CU has tiles enough: four blocks' scales are one word a
+// row and loaded every fourth stage.  S = 4, for the smallest tiles, one or
+// two workgroups a CU: a block's loads are three steps ahead, and each stage
+// loads its scales' word so that the number of loads in flight is known.
+template <int BM, int BN, int WM, int WN, int S, bool GRAD, bool EXACT>
+__global__ __launch_bounds__(WM* WN* kWave, 2) void k_fp8_gemm(const uint8_t* __restrict__ A,
                                                             const uint8_t* __restrict__ As,
                                                             const uint8_t* __restrict__ Bm,
                                                             const uint8_t* __restrict__ Bs, int64_t M, int N,
                                                             int64_t ldk, int64_t sld, const int32_t* __restrict__ off,
-                                                            int G, void* __restrict__ outp) {
+                                                            int G, int tiles, void* __restrict__ outp) {
   constexpr int W = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
   constexpr int A_BYTES = BM * kQBlock, B_BYTES = BN * kQBlock;
   constexpr int A_PW = A_BYTES / 1024 / W, B_PW = B_BYTES / 1024 / W;  // 1 KiB loads per wave and stage
   constexpr int ROWS = BM + BN;
-  static_assert(A_PW * W * 1024 == A_BYTES && B_PW * W * 1024 == B_BYTES, "tile split");
-  __shared__ __align__(1024) uint8_t lds[2 * (A_BYTES + B_BYTES) + 2 * ROWS * 4];
+  constexpr int S_PW = (ROWS / kWave + W - 1) / W;  // loads of 64 rows' scale words per wave
+  constexpr bool WIDE = !GRAD;
+  constexpr int JT = TN < 4 ? TN : 4;  // column tiles that share a stretch of 16 JT columns
+  static_assert(A_PW * W * 1024 == A_BYTES && B_PW * W * 1024 == B_BYTES && ROWS % kWave == 0, "tile split");
+  static_assert(TN % JT == 0 && JT >= 2, "a bf16 result's columns");
+  // a row's number in the swizzle of its slots
+  auto key_a = [](int row) { return (row >> 1) & 7; };
+  auto key_b = [](int row) { return WIDE ? ((row >> 1) & 1) | ((row >> (JT == 4 ? 3 : 2)) & 6) : (row >> 1) & 7; };
+  // one array: with several, the compiler waits for the loads to LDS before it reads any of them
+  __shared__ __align__(1024) uint8_t lds[S * (A_BYTES + B_BYTES) + S * ROWS * 4 + 1024 * 3 + 16];
+  uint8_t* const lds_b = lds + S * A_BYTES;
+  uint8_t* const lds_s = lds + S * (A_BYTES + B_BYTES);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  const int tn_all = (N + BN - 1) / BN;
+  const int tn_all = (N + BN - 1) / BN, kb_all = int(ldk / kQBlock);
 
-  // this workgroup's tile: rows [m0, m_end) of A and of the result, rows
-  // n0... of B, blocks [k0, k1) of K
-  int64_t m0, m_end;
-  int n0, k0 = 0, k1 = int(ldk / kQBlock);
-  int64_t out_row = 0;  // what the result's row number is counted from
-  if constexpr (GRAD) {
-    const int tm_all = int((M + BM - 1) / BM), per = tm_all * tn_all;
-    const int t = xcd_tile(int(blockIdx.x), int(gridDim.x));
-    const int e = t / per;
-    int tm, tn;
-    tile_order(t % per, tm_all, tn_all, 8, tm, tn);
-    if (off) {
-      int a = off[e] / kQBlock, b = off[e + 1] / kQBlock;
-      a = a < 0 ? 0 : (a > k1 ? k1 : a);
-      b = b < a ? a : (b > k1 ? k1 : b);
-      k0 = a;
-      k1 = b;
+  // the experts' first and last rows (GRAD: blocks of rows) and their tiles of rows before each, kept in LDS: a
+  // tile's expert is found while the last tile's products wait for it
+  int* const first_of = reinterpret_cast<int*>(lds_s + S * ROWS * 4);
+  int *const end_of = first_of + 256, *const before_of = end_of + 256;  // 256, 256 and 257 of them
+  if (off) {
+    int total = 0;
+    if constexpr (GRAD) {
+      for (int e = tid; e < G; e += W * kWave) {
+        int a = off[e] / kQBlock, b = off[e + 1] / kQBlock;
+        a = a < 0 ? 0 : (a > kb_all ? kb_all : a);
+        b = b < a ? a : (b > kb_all ? kb_all : b);
+        first_of[e] = a;
+        end_of[e] = b;
+      }
+    } else if (wave == 0) {
+      int lo[4], hi[4], n[4], before;
+      total = group_tiles(off, G, M, BM, lane, lo, hi, n, before);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        first_of[4 * lane + j] = lo[j];
+        end_of[4 * lane + j] = hi[j];
+        before_of[4 * lane + j] = before;
+        before += n[j];
+      }
+      if (lane == 0) before_of[256] = total;
     }
-    m0 = int64_t(tm) * BM;
-    m_end = M;
-    n0 = tn * BN;
-    out_row = int64_t(e) * M;
-  } else if (off) {
-    int lo[4], hi[4], n[4], before;
-    const int total = group_tiles(off, G, M, BM, lane, lo, hi, n, before);
-    if (int(blockIdx.x) >= total * tn_all) return;
-    const int t = xcd_tile(int(blockIdx.x), total * tn_all);
-    int tm, tn;
-    tile_order(t, total, tn_all, 8, tm, tn);
-    const Tile g = group_find(tm, lane, lo, hi, n, before);
-    if (g.e < 0) return;
-    m0 = g.lo + int64_t(g.at) * BM;
-    m_end = g.hi;
-    n0 = tn * BN;
-    Bm += int64_t(g.e) * N * ldk;
-    Bs += int64_t(g.e) * ((N + kQBlock - 1) / kQBlock) * sld;
-  } else {
-    const int tm_all = int((M + BM - 1) / BM);
-    const int t = xcd_tile(int(blockIdx.x), int(gridDim.x));
-    int tm, tn;
-    tile_order(t, tm_all, tn_all, 8, tm, tn);
-    m0 = int64_t(tm) * BM;
-    m_end = M;
-    n0 = tn * BN;
+    __syncthreads();
+    // (offsets out of order could make more than there are)
+    if constexpr (!GRAD) tiles = (before_of[256] < tiles / tn_all ? before_of[256] : tiles / tn_all) * tn_all;
   }
 
-  // per-lane sources: rows past the end re-read the last one
-  const uint8_t* a_base = A + m0 * ldk;
-  const uint8_t* b_base = Bm + int64_t(n0) * ldk;
+  // What a tile's results need: rows m0 .. m_end - 1 and columns n0 ... of
+  // the result, whose rows are counted from out_row; blocks k0 .. k1 - 1.
+  struct Place {
+    int m0, m_end, out_row, n0, k0, k1;
+  };
+  // and what its loads need
+  const uint8_t *a_base, *b_base, *s_src[S_PW];
   uint32_t a_off[A_PW], b_off[B_PW];
+  auto place = [&](int t) {
+    Place p{0, int(M), 0, 0, 0, kb_all};
+    const uint8_t *bm = Bm, *bsc = Bs;
+    int tm, tn;
+    if constexpr (GRAD) {
+      const int tm_all = int((M + BM - 1) / BM), per = tm_all * tn_all, e = t / per;
+      tile_order(t % per, tm_all, tn_all, 8, tm, tn);
+      if (off) {
+        p.k0 = __builtin_amdgcn_readfirstlane(first_of[e]);
+        p.k1 = __builtin_amdgcn_readfirstlane(end_of[e]);
+      }
+      p.m0 = tm * BM;
+      p.out_row = e * int(M);
+    } else if (off) {
+      tile_order(t, tiles / tn_all, tn_all, 8, tm, tn);
+      // the expert whose tiles hold tm: the one before the first that begins past it
+      int begun = 0;
 #pragma unroll
-  for (int j = 0; j < A_PW; ++j) {
-    const int p = (wave * A_PW + j) * kWave + lane, q = p ^ ((p >> 4) & 7);
-    int row = q >> 3;
-    row = m0 + row < m_end ? row : int(m_end - 1 - m0);
-    a_off[j] = uint32_t(row) * uint32_t(ldk) + (q & 7) * 16;
-  }
-#pragma unroll
-  for (int j = 0; j < B_PW; ++j) {
-    const int p = (wave * B_PW + j) * kWave + lane, q = p ^ ((p >> 4) & 7);
-    int row = q >> 3;
-    row = n0 + row < N ? row : N - 1 - n0;
-    b_off[j] = uint32_t(row) * uint32_t(ldk) + (q & 7) * 16;
-  }
-  // scales: ROWS words, 64 a load
-  constexpr int S_PW = (ROWS / kWave + W - 1) / W;
-  const uint8_t* s_src[S_PW];
-#pragma unroll
-  for (int j = 0; j < S_PW; ++j) {
-    const int i = (wave * S_PW + j) * kWave + lane;
-    if (i < BM) {
-      int64_t row = m0 + i;
-      row = row < m_end ? row : m_end - 1;
-      s_src[j] = As + row * sld;
+      for (int j = 0; j < 4; ++j) begun += __popcll(__ballot(before_of[4 * lane + j] <= tm));
+      const int e = begun > 0 ? begun - 1 : 0;  // the last of those that begin at tm: the ones before it have no tile
+      p.m0 = __builtin_amdgcn_readfirstlane(first_of[e] + (tm - before_of[e]) * BM);
+      p.m_end = __builtin_amdgcn_readfirstlane(end_of[e]);
+      bm += int64_t(e) * N * ldk;
+      bsc += int64_t(e) * ((N + kQBlock - 1) / kQBlock) * sld;
     } else {
-      int row = n0 + (i - BM);
-      row = row < N ? row : N - 1;
-      s_src[j] = Bs + int64_t(GRAD ? row : row / kQBlock) * sld;
+      tile_order(t, int((M + BM - 1) / BM), tn_all, 8, tm, tn);
+      p.m0 = tm * BM;
     }
-  }
-  uint8_t* lds_s = lds + 2 * (A_BYTES + B_BYTES);
-  auto issue = [&](int kb, bool first) {
-    const int st = kb & 1;
-    const int64_t ko = int64_t(kb) * kQBlock;
-    uint8_t* sa = lds + st * A_BYTES;
-    uint8_t* sb = lds + 2 * A_BYTES + st * B_BYTES;
-    const uint8_t* ak = a_base + ko;
-    const uint8_t* bk = b_base + ko;
+    p.n0 = tn * BN;
+    // per-lane sources: rows past the end re-read the last one
+    a_base = A + int64_t(p.m0) * ldk;
+    b_base = bm + int64_t(p.n0) * ldk;
 #pragma unroll
-    for (int j = 0; j < A_PW; ++j)
-      __builtin_amdgcn_global_load_lds((glb_vptr)(ak + a_off[j]), (lds_vptr)(sa + (wave * A_PW + j) * 1024), 16, 0, 0);
-#pragma unroll
-    for (int j = 0; j < B_PW; ++j)
-      __builtin_amdgcn_global_load_lds((glb_vptr)(bk + b_off[j]), (lds_vptr)(sb + (wave * B_PW + j) * 1024), 16, 0, 0);
-    if (first || (kb & 3) == 0) {
-      uint8_t* ss = lds_s + ((kb >> 2) & 1) * (ROWS * 4);
-#pragma unroll
-      for (int j = 0; j < S_PW; ++j)
-        if ((wave * S_PW + j) * kWave < ROWS)
-          __builtin_amdgcn_global_load_lds((glb_vptr)(s_src[j] + (kb & ~3)), (lds_vptr)(ss + (wave * S_PW + j) * 256),
-                                           4, 0, 0);
+    for (int j = 0; j < A_PW; ++j) {
+      const int at = (wave * A_PW + j) * kWave + lane, r = at >> 3, q = (at & 7) ^ key_a(r);
+      const int row = p.m0 + r < p.m_end ? r : p.m_end - 1 - p.m0;
+      a_off[j] = uint32_t(row) * uint32_t(ldk) + q * 16;
     }
+#pragma unroll
+    for (int j = 0; j < B_PW; ++j) {
+      const int at = (wave * B_PW + j) * kWave + lane, r = at >> 3, q = (at & 7) ^ key_b(r);
+      const int row = p.n0 + r < N ? r : N - 1 - p.n0;
+      b_off[j] = uint32_t(row) * uint32_t(ldk) + q * 16;
+    }
+#pragma unroll
+    for (int j = 0; j < S_PW; ++j) {
+      const int i = (wave * S_PW + j) % (ROWS / kWave) * kWave + lane;  // (with fewer than waves, some load them twice)
+      if (i < BM) {
+        const int row = p.m0 + i < p.m_end ? p.m0 + i : p.m_end - 1;
+        s_src[j] = As + int64_t(row) * sld;
+      } else {
+        int row = p.n0 + (i - BM);
+        row = row < N ? row : N - 1;
+        s_src[j] = bsc + int64_t(GRAD ? row : row / kQBlock) * sld;
+      }
+    }
+    return p;
+  };
+  // Load u of a stage's tiles.
+  constexpr int LOADS = A_PW + B_PW;
+  auto issue = [&](int u, int64_t ko, int st) {
+    if (u < A_PW)
+      __builtin_amdgcn_global_load_lds((glb_vptr)(a_base + ko + a_off[u < A_PW ? u : 0]),
+                                       (lds_vptr)(lds + st * A_BYTES + (wave * A_PW + u) * 1024), 16, 0, 0);
+    else
+      __builtin_amdgcn_global_load_lds((glb_vptr)(b_base + ko + b_off[u < A_PW ? 0 : u - A_PW]),
+                                       (lds_vptr)(lds_b + st * B_BYTES + (wave * B_PW + u - A_PW) * 1024), 16, 0, 0);
+  };
+  auto issue_scales = [&](int kb, int slot) {
+#pragma unroll
+    for (int j = 0; j < S_PW; ++j)
+      __builtin_amdgcn_global_load_lds((glb_vptr)(s_src[j] + (kb & ~3)),
+                                       (lds_vptr)(lds_s + slot * (ROWS * 4) + (wave * S_PW + j) % (ROWS / kWave) * 256), 4, 0,
+                                       0);
+  };
+  auto issue_all = [&](int kb, int st, int slot) {
+#pragma unroll
+    for (int u = 0; u < LOADS; ++u) issue(u, int64_t(kb) * kQBlock, st);
+    issue_scales(kb, slot);
   };
 
   v4f acc[TM][TN];
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
-
   const int r = lane & 15, g4 = lane >> 4;
-  const int frag = r * kQBlock + ((g4 ^ ((r >> 1) & 7)) * 16), frag4 = frag ^ 64;  // slots g4 and g4 + 4
-  if (k0 < k1) issue(k0, true);
-  for (int kb = k0; kb < k1; ++kb) {
-    // the tile's loads are the only ones in flight; the barrier publishes
-    // every wave's and retires all reads of the stage that is filled next
-    __builtin_amdgcn_s_waitcnt(0x0F70);
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    if (kb + 1 < k1) issue(kb + 1, false);
-    const uint8_t* sa = lds + (kb & 1) * A_BYTES + wm * (TM * 16) * kQBlock;
-    const uint8_t* sb = lds + 2 * A_BYTES + (kb & 1) * B_BYTES + wn * (TN * 16) * kQBlock;
-    const uint8_t* ss = lds_s + ((kb >> 2) & 1) * (ROWS * 4) + (kb & 3);
+  // this lane's slots g4 and g4 + 4 of its row
+  const int frag_a = r * kQBlock + ((g4 ^ key_a(r)) * 16);
+  const int br = WIDE ? (r >> 2) * (4 * JT) + (r & 3) : r;  // its row of column tile 0, and what tile j adds
+  auto b_row = [](int j) { return WIDE ? j / JT * (16 * JT) + j % JT * 4 : j * 16; };
+  auto frag_b = [&](int j) {
+    const int row = br + b_row(j);
+    return row * kQBlock + ((g4 ^ key_b(row)) * 16);
+  };
+  // block kb's products out of stage st, its scales out of `slot`, while block
+  // `load`'s tiles go to stage `into`: after the first row tile's products
+  // (8192 x 8192 x 4096: 249 us; before them all 261, spread over the rows 265)
+  auto multiply = [&](int kb, int st, int slot, int load, int into) {
+    const int64_t ko = int64_t(load) * kQBlock;
+    const uint8_t* sa = lds + st * A_BYTES + wm * (TM * 16) * kQBlock;
+    const uint8_t* sb = lds_b + st * B_BYTES + wn * (TN * 16) * kQBlock;
+    const uint8_t* ss = lds_s + slot * (ROWS * 4) + (kb & 3);
+    const uint8_t *ssa = ss + (wm * TM * 16 + r) * 4, *ssb = ss + (BM + wn * TN * 16 + br) * 4;
     if constexpr (!EXACT) {
       v8i b[TN];
       int bs[TN];
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
-        const v4i lo = *reinterpret_cast<const v4i*>(sb + j * 16 * kQBlock + frag);
-        const v4i hi = *reinterpret_cast<const v4i*>(sb + j * 16 * kQBlock + frag4);
-        b[j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        bs[j] = ss[(BM + (wn * TN + j) * 16 + r) * 4];
+        const v4i lo4 = *reinterpret_cast<const v4i*>(sb + frag_b(j));
+        const v4i hi4 = *reinterpret_cast<const v4i*>(sb + (frag_b(j) ^ 64));
+        b[j] = __builtin_shufflevector(lo4, hi4, 0, 1, 2, 3, 4, 5, 6, 7);
+        bs[j] = ssb[b_row(j) * 4];
       }
+      // row tile i + 1 is read while i's products run
+      v8i a[2];
+      int as[2];
+      auto read = [&](int i) {
+        const v4i lo4 = *reinterpret_cast<const v4i*>(sa + i * 16 * kQBlock + frag_a);
+        const v4i hi4 = *reinterpret_cast<const v4i*>(sa + i * 16 * kQBlock + (frag_a ^ 64));
+        a[i & 1] = __builtin_shufflevector(lo4, hi4, 0, 1, 2, 3, 4, 5, 6, 7);
+        as[i & 1] = ssa[i * 64];
+      };
+      read(0);
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
-        const v4i lo = *reinterpret_cast<const v4i*>(sa + i * 16 * kQBlock + frag);
-        const v4i hi = *reinterpret_cast<const v4i*>(sa + i * 16 * kQBlock + frag4);
-        const v8i a = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        const int as = ss[((wm * TM + i) * 16 + r) * 4];
+        if (i + 1 < TM) read(i + 1);
 #pragma unroll
         for (int j = 0; j < TN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j], a, acc[i][j], 0, 0, 0, bs[j], 0, as);
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j], a[i & 1], acc[i][j], 0, 0, 0, bs[j], 0,
+                                                                      as[i & 1]);
+        if (i == 0)
+#pragma unroll
+          for (int u = 0; u < LOADS; ++u) issue(u, ko, into);
       }
     } else {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int at = h ? frag4 : frag;
         bf16x8 b[TN][2];
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
-          const v4i t = *reinterpret_cast<const v4i*>(sb + j * 16 * kQBlock + at);
-          const float f = scale_value(ss[(BM + (wn * TN + j) * 16 + r) * 4]);
+          const v4i t = *reinterpret_cast<const v4i*>(sb + (frag_b(j) ^ (h * 64)));
+          const float f = scale_value(ssb[b_row(j) * 4]);
           b[j][0] = widen(t[0], t[1], f);
           b[j][1] = widen(t[2], t[3], f);
         }
+        v4i a[2];
+        int as[2];
+        auto read = [&](int i) {
+          a[i & 1] = *reinterpret_cast<const v4i*>(sa + i * 16 * kQBlock + (frag_a ^ (h * 64)));
+          as[i & 1] = ssa[i * 64];
+        };
+        read(0);
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-          const v4i t = *reinterpret_cast<const v4i*>(sa + i * 16 * kQBlock + at);
-          const float f = scale_value(ss[((wm * TM + i) * 16 + r) * 4]);
+          if (i + 1 < TM) read(i + 1);
+          const v4i t = a[i & 1];
+          const float f = scale_value(as[i & 1]);
           const bf16x8 a0 = widen(t[0], t[1], f), a1 = widen(t[2], t[3], f);
 #pragma unroll
           for (int j = 0; j < TN; ++j) {
             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j][0], a0, acc[i][j], 0, 0, 0);
             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j][1], a1, acc[i][j], 0, 0, 0);
           }
+          if (h == 0 && i == 0)
+#pragma unroll
+            for (int u = 0; u < LOADS; ++u) issue(u, ko, into);
         }
       }
     }
-  }
+  };
 
-  // element c of acc[i][j]: row 16 i + l % 16, column 16 j + 4 (l / 16) + c
+  // element c of acc[i][j]: row 16 i + r, column 16 j + 4 g4 + c (WIDE: 4 JT g4 + 4 j + c of its JT column tiles);
+  // returns whether every store of the tile was issued
+  constexpr int STORES = TM * (WIDE ? TN / 2 : TN);
+  auto store_some = [&](const Place& p, auto whole) {
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int64_t row = m0 + (wm * TM + i) * 16 + r;
-    if (row >= m_end) continue;
-#pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const int col = n0 + (wn * TN + j) * 16 + g4 * 4;
-      const v4f v = acc[i][j];
+    for (int i = 0; i < TM; ++i) {
+      const int row = p.m0 + (wm * TM + i) * 16 + r;
+      if (!whole() && row >= p.m_end) continue;
       if constexpr (GRAD) {
-        float* o = static_cast<float*>(outp) + (out_row + row) * N + col;
-        if (col + 3 < N) {
-          Float4 t;
+        float* o = static_cast<float*>(outp) + int64_t(p.out_row + row) * N;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) t.v[c] = v[c];
-          *reinterpret_cast<Float4*>(o) = t;
-        } else {
+        for (int j = 0; j < TN; ++j) {
+          const int col = p.n0 + (wn * TN + j) * 16 + g4 * 4;
+          const v4f v = acc[i][j];
+          if (whole() || col + 3 < N) {
+            Float4 t;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (col + c < N) o[c] = v[c];
+            for (int c = 0; c < 4; ++c) t.v[c] = v[c];
+            *reinterpret_cast<Float4*>(o + col) = t;
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (col + c < N) o[col + c] = v[c];
+          }
         }
       } else {
-        uint16_t* o = static_cast<uint16_t*>(outp) + row * N + col;
-        Half4 t;
-        t.v[0] = bf16x2_rne(v[0], v[1]);
-        t.v[1] = bf16x2_rne(v[2], v[3]);
-        if (col + 3 < N) {
-          *reinterpret_cast<Half4*>(o) = t;
-        } else {
+        uint16_t* o = static_cast<uint16_t*>(outp) + int64_t(row) * N;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (col + c < N) o[c] = uint16_t(t.v[c >> 1] >> (16 * (c & 1)));
+        for (int h = 0; h < TN / 2; ++h) {  // 8 columns each
+          const int col = p.n0 + (wn * TN + 2 * h / JT * JT) * 16 + g4 * (4 * JT) + 8 * (h % (JT / 2));
+          Half8 t;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            t.v[k] = bf16x2_rne(acc[i][2 * h + k / 2][2 * (k & 1)], acc[i][2 * h + k / 2][2 * (k & 1) + 1]);
+          if (whole() || col + 7 < N) {
+            *reinterpret_cast<Half8*>(o + col) = t;
+          } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              if (col + c < N) o[col + c] = uint16_t(t.v[c >> 1] >> (16 * (c & 1)));
+          }
         }
       }
+    }
+  };
+  auto store = [&](const Place& p) {
+    const bool whole = p.m0 + BM <= p.m_end && p.n0 + BN <= N;
+    if (whole)
+      store_some(p, std::true_type{});
+    else
+      store_some(p, std::false_type{});
+    return whole;
+  };
+  auto clear = [&]() {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+  };
+
+  int at = int(blockIdx.x);
+  Place now{};
+  // the next tile that has a product to compute; those without (an expert without rows) are written as zeros
+  auto advance = [&](bool& found) {
+    found = false;
+    for (; at < tiles; at += int(gridDim.x)) {
+      const bool in_turn = GRAD && off && gridDim.x % 8 == 0;
+      const Place p = place(in_turn ? tile_in_turn<BM == 256 ? 16 : 8>(at, tiles) : tile_at(at, int(gridDim.x), tiles));
+      if (p.k0 < p.k1) {
+        found = true;
+        at += int(gridDim.x);
+        return p;
+      }
+      if constexpr (GRAD) zero_tile<BM, BN, W>(static_cast<float*>(outp), p.out_row, p.m0, M, p.n0, N, tid);
+    }
+    return Place{};
+  };
+  bool more;
+  now = advance(more);
+  if constexpr (S == 2) {
+    int put = 0, get = 1, st = 0;  // the halves of the scales' ring that was filled last and that is read
+    if (more) issue_all(now.k0, 0, 0);
+    bool behind = false;  // the last tile's stores are younger than the loads that are waited for
+    while (more) {
+      clear();
+      Place then{};
+      bool next = false;
+      for (int kb = now.k0; kb < now.k1; ++kb) {
+        // this wave's loads of the stage; the barrier publishes every wave's
+        // and retires all reads of the stage that is filled next
+        if (behind && kb == now.k0)
+          __builtin_amdgcn_s_waitcnt(vm_count(STORES));
+        else
+          __builtin_amdgcn_s_waitcnt(vm_count(0));
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (kb == now.k0 || (kb & 3) == 0) get ^= 1;
+        // the next block: of this tile, of the next one, or (no more tiles) this one again, which nothing reads
+        int load = kb + 1;
+        bool scales = (load & 3) == 0;
+        if (load == now.k1) {
+          then = advance(next);
+          scales = next;
+          load = next ? then.k0 : kb;
+        }
+        if (scales) {
+          put ^= 1;
+          issue_scales(load, put);
+        }
+        multiply(kb, st, get, load, st ^ 1);
+        st ^= 1;
+      }
+      behind = store(now);
+      now = then;
+      more = next;
+    }
+    __builtin_amdgcn_s_waitcnt(vm_count(0));  // no load may land after the LDS has changed hands
+  } else {
+    constexpr int PER = LOADS + S_PW;
+    while (more) {
+      clear();
+#pragma unroll
+      for (int u = 0; u < S - 1; ++u) {
+        const int kb = now.k0 + u < now.k1 ? now.k0 + u : now.k1 - 1;
+        issue_all(kb, u, u);
+      }
+      int st = 0;
+      for (int kb = now.k0; kb < now.k1; ++kb) {
+        __builtin_amdgcn_s_waitcnt(vm_count((S - 2) * PER));
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        // past the tile's end the last block again, which nothing reads
+        const int load = kb + S - 1 < now.k1 ? kb + S - 1 : now.k1 - 1, into = st == 0 ? S - 1 : st - 1;
+        issue_scales(load, into);
+        multiply(kb, st, st, load, into);
+        st = st + 1 < S ? st + 1 : 0;
+      }
+      store(now);
+      __builtin_amdgcn_s_waitcnt(vm_count(0));
+      now = advance(more);
+      if (more) __syncthreads();  // all have read the ring
     }
   }
 }
@@ -795,10 +1000,6 @@ __global__ __launch_bounds__(512) void k_fp8_thin(const uint8_t* __restrict__ A,
 
 // ---------------------------------------------------------------------------
 
-#ifndef QB_F8_WIDE
-#define QB_F8_WIDE 192
-#endif
-
 struct Gemm {
   const uint8_t *A, *As, *B, *Bs;
   int64_t M;
@@ -815,14 +1016,33 @@ static int64_t row_tiles(const Gemm& g, int BM) {
   return g.M / BM + std::min<int64_t>(g.G, g.M);
 }
 
-template <int BM, int BN, int WM, int WN, bool GRAD, bool EXACT>
+template <int BM, int BN, int WM, int WN, int S, bool GRAD, bool EXACT>
 static int gemm_tiled(const Gemm& g, hipStream_t st) {
   const int64_t tn = (g.N + BN - 1) / BN;
-  const int64_t blocks = GRAD ? int64_t(g.G) * ((g.M + BM - 1) / BM) * tn : row_tiles(g, BM) * tn;
-  if (blocks > INT32_MAX) return int(hipErrorInvalidValue);
-  hipLaunchKernelGGL((k_fp8_gemm<BM, BN, WM, WN, GRAD, EXACT>), dim3(unsigned(blocks)), dim3(WM * WN * kWave), 0, st, g.A,
-                     g.As, g.B, g.Bs, g.M, g.N, g.ldk, g.sld, g.off, g.G, g.out);
+  const int64_t tiles = GRAD ? int64_t(g.G) * ((g.M + BM - 1) / BM) * tn : row_tiles(g, BM) * tn;
+  if (tiles > INT32_MAX) return int(hipErrorInvalidValue);
+  // as many workgroups as run at once (a 256 x 256 tile's ring fills a CU's LDS, a 128 x 128 tile's half of it)
+  const int64_t most = int64_t(device_cu_count()) * (S * (BM + BN) > 512 ? 1 : 2);
+  hipLaunchKernelGGL((k_fp8_gemm<BM, BN, WM, WN, S, GRAD, EXACT>), dim3(unsigned(std::min(tiles, most))),
+                     dim3(WM * WN * kWave), 0, st, g.A, g.As, g.B, g.Bs, g.M, g.N, g.ldk, g.sld, g.off, g.G, int(tiles),
+                     g.out);
   return int(hipGetLastError());
+}
+
+// Which tiles: 64 x 64 while two workgroups a CU take them all at once (768 x
+// 2048 x 1024: 7.7 us, 128 x 128 tiles 9.5; 2048 x 2048 x 2048: 19.4 and 16.5).
+// Above that 128 x 128, two at a time on a CU, or 256 x 256, which read half
+// the operands' bytes per product and cost 3.3 small ones' time where two
+// small ones at a time cost 2 (8192 x 8192 x 4096: 226 us, 271), whichever has
+// the cheaper number of rounds over the CUs.  `uneven`: the part of a round
+// that large tiles lose where experts of unequal length leave some CUs waiting.
+template <bool GRAD, bool EXACT>
+static int gemm(const Gemm& g, int64_t t256, int64_t t128, int64_t t64, double uneven, hipStream_t st) {
+  const int64_t cu = device_cu_count();
+  if (t64 <= 2 * cu) return gemm_tiled<64, 64, 2, 2, 4, GRAD, EXACT>(g, st);
+  const double rounds256 = double((t256 + cu - 1) / cu), rounds128 = double((t128 + 2 * cu - 1) / (2 * cu));
+  if (t256 > 0 && 3.3 * (rounds256 + uneven) < 2 * rounds128) return gemm_tiled<256, 256, 2, 4, 2, GRAD, EXACT>(g, st);
+  return gemm_tiled<128, 128, 2, 2, 2, GRAD, EXACT>(g, st);
 }
 
 template <int MT, int KW>
@@ -864,16 +1084,19 @@ int launch_fp8_product(const uint8_t* xq, const uint8_t* xs, const uint8_t* w, c
     if (rows <= 32) return gemm_few<2>(g, st);
     return gemm_few<4>(g, st);
   }
-  if (row_tiles(g, 256) * ((N + 255) / 256) >= QB_F8_WIDE)
-    return exact ? gemm_tiled<256, 256, 2, 4, false, true>(g, st) : gemm_tiled<256, 256, 2, 4, false, false>(g, st);
-  return exact ? gemm_tiled<128, 128, 2, 2, false, true>(g, st) : gemm_tiled<128, 128, 2, 2, false, false>(g, st);
+  auto tiles = [&](int b) { return row_tiles(g, b) * ((N + b - 1) / b); };
+  // an expert of up to 128 rows fills no more than half of a large tile
+  const int64_t t256 = rows <= 128 && off ? 0 : tiles(256);
+  const double uneven = off ? 0.1 : 0.0;
+  return exact ? gemm<false, true>(g, t256, tiles(128), tiles(64), uneven, st)
+               : gemm<false, false>(g, t256, tiles(128), tiles(64), uneven, st);
 }
 
 int launch_fp8_weight_grad(const uint8_t* dyt, const uint8_t* dyts, const uint8_t* xt, const uint8_t* xts, int N,
                            int C, int64_t ldm, const int32_t* off, int G, float* dw, hipStream_t st) {
   const Gemm g{dyt, dyts, xt, xts, N, C, ldm, fp8_sld(ldm), off, G, dw};
-  if (int64_t(G) * ((N + 255) / 256) * ((C + 255) / 256) >= QB_F8_WIDE) return gemm_tiled<256, 256, 2, 4, true, true>(g, st);
-  return gemm_tiled<128, 128, 2, 2, true, true>(g, st);
+  auto tiles = [&](int b) { return int64_t(G) * ((N + b - 1) / b) * ((C + b - 1) / b); };
+  return gemm<true, true>(g, tiles(256), tiles(128), tiles(64), off ? 0.25 : 0.0, st);
 }
 
 }  // namespace qbk
