@@ -18,11 +18,12 @@
 // combine:           out_t   = sum_k gate_tk rows[pos_tk]
 // combine backward:  dgate_tk = <dout_t, rows[pos_tk]>,  drows[pos_tk] = gate_tk dout_t,
 //                    0 in rows that no pair fills
-// Both are streams of rows bound by HBM: a token is owned by up to 64 lanes
+// Both are streams of rows bound by HBM: a token is owned by up to 256 lanes
 // with 8 columns each per step, so a row of `dout` is read once for its K
 // rows and every access is 16 bytes a lane; sums are held in 32 bits and
 // rounded once.
 #include <algorithm>
+#include <type_traits>
 
 #include "qb_device.hpp"
 #include "qb_internal.hpp"
@@ -218,45 +219,51 @@ int launch_dispatch(const Dispatch& a, hipStream_t st) {
 
 // ---------------------------------------------------------------------------
 
-// 8 bf16 of a row from element `at`; VEC: all 8 lie inside the row (the
-// address needs only the element's alignment), else those below `n`.
-struct __attribute__((packed, aligned(2))) Bf8 {
-  uint32_t v[4];
-};
+// 8 bf16 of a row (the address needs only the element's alignment); NT: past
+// the caches, for what no cache holds long enough to be read again.
+typedef uint32_t bf8 __attribute__((ext_vector_type(4), aligned(2)));
 
 __device__ __forceinline__ float bf_lo(uint32_t p) { return __builtin_bit_cast(float, p << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t p) { return __builtin_bit_cast(float, p & 0xFFFF0000u); }
 
-__device__ __forceinline__ void ld_bf8(const uint16_t* p, int n, uint32_t (&v)[4]) {
-  if (n >= 8) {
-    const Bf8 t = *reinterpret_cast<const Bf8*>(p);
+// A lane's 8 columns, h0 on.  Near a row's end they begin earlier, at H - 8,
+// so that every access is whole: the columns that the lane before has too are
+// computed and written twice, to the same values.  Rows of fewer than 8
+// columns go element by element.
+template <bool NT>
+__device__ __forceinline__ bf8 ld_bf8(const uint16_t* p, int H) {
+  if (H >= 8) {
+    if constexpr (NT) return __builtin_nontemporal_load(reinterpret_cast<const bf8*>(p));
+    return *reinterpret_cast<const bf8*>(p);
+  }
+  bf8 v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = t.v[i];
-  } else {
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = 2 * i < H ? p[2 * i] : 0, hi = 2 * i + 1 < H ? p[2 * i + 1] : 0;
+    v[i] = lo | (hi << 16);
+  }
+  return v;
+}
+template <bool NT>
+__device__ __forceinline__ void st_bf8(uint16_t* p, int H, bf8 v) {
+  if (H >= 8) {
+    if constexpr (NT)
+      __builtin_nontemporal_store(v, reinterpret_cast<bf8*>(p));
+    else
+      *reinterpret_cast<bf8*>(p) = v;
+    return;
+  }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t lo = 2 * i < n ? p[2 * i] : 0, hi = 2 * i + 1 < n ? p[2 * i + 1] : 0;
-      v[i] = lo | (hi << 16);
-    }
+  for (int i = 0; i < 4; ++i) {
+    if (2 * i < H) p[2 * i] = uint16_t(v[i]);
+    if (2 * i + 1 < H) p[2 * i + 1] = uint16_t(v[i] >> 16);
   }
 }
-__device__ __forceinline__ void st_bf8(uint16_t* p, int n, const uint32_t (&v)[4]) {
-  if (n >= 8) {
-    Bf8 t;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) t.v[i] = v[i];
-    *reinterpret_cast<Bf8*>(p) = t;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (2 * i < n) p[2 * i] = uint16_t(v[i]);
-      if (2 * i + 1 < n) p[2 * i + 1] = uint16_t(v[i] >> 16);
-    }
-  }
-}
+__device__ __forceinline__ int bf8_column(int h0, int H) { return H < 8 ? 0 : (h0 < H - 8 ? h0 : H - 8); }
 
-// Lanes that own a token: enough for one 8-column step over the row, 64 at most.
-template <int LT>
+// LT lanes own a token: as many as its row has 8 columns for, 256 at most, so
+// that a row's 4 KiB are read by one workgroup at once.
+template <int LT, bool NT>
 __global__ __launch_bounds__(256) void k_combine(const uint16_t* __restrict__ rows, int64_t R,
                                                  const int32_t* __restrict__ pos, const float* __restrict__ gate,
                                                  int64_t N, int K, int H, uint16_t* __restrict__ out) {
@@ -265,12 +272,12 @@ __global__ __launch_bounds__(256) void k_combine(const uint16_t* __restrict__ ro
   if (t >= N) return;
   const int h0 = (int(blockIdx.y) * LT + tl) * 8;
   if (h0 >= H) return;
-  const int n = H - h0;
+  const int at = bf8_column(h0, H);
   float acc[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.f;
   for (int k0 = 0; k0 < K; k0 += 8) {
-    uint32_t v[8][4];
+    bf8 v[8];
     float g[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
@@ -278,12 +285,7 @@ __global__ __launch_bounds__(256) void k_combine(const uint16_t* __restrict__ ro
       const int p = k < K ? pos[t * K + k] : -1;
       const bool on = p >= 0 && p < R;
       g[u] = on ? (gate ? gate[t * K + k] : 1.0f) : 0.f;
-      if (on) {
-        ld_bf8(rows + int64_t(p) * H + h0, n, v[u]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[u][i] = 0;
-      }
+      v[u] = on ? ld_bf8<NT>(rows + int64_t(p) * H + at, H) : (bf8){0, 0, 0, 0};
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u)
@@ -293,37 +295,62 @@ __global__ __launch_bounds__(256) void k_combine(const uint16_t* __restrict__ ro
         acc[2 * i + 1] = fmaf(g[u], bf_hi(v[u][i]), acc[2 * i + 1]);
       }
   }
-  uint32_t o[4];
+  bf8 o;
 #pragma unroll
   for (int i = 0; i < 4; ++i) o[i] = bf16x2_rne(acc[2 * i], acc[2 * i + 1]);
-  st_bf8(out + t * H + h0, n, o);
+  st_bf8<NT>(out + t * H + at, H, o);
 }
 
-template <int LT, bool DG>
+// The sums of eight values over L lanes (64 at most), value (lane >> 3) & 7
+// of them in every lane for L = 64: each exchange halves how many a lane
+// carries, so that they cost 10 shuffles together and not 48.
+template <int L>
+__device__ __forceinline__ void sum8(float (&v)[8], int lane) {
+  int have = 8;
+#pragma unroll
+  for (int d = L / 2; d >= 1; d >>= 1) {
+    if (have > 1) {
+      const bool up = lane & d;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (u < have / 2) {
+          const float keep = up ? v[u + have / 2] : v[u], give = up ? v[u] : v[u + have / 2];
+          v[u] = keep + __shfl_xor(give, d);
+        }
+      have /= 2;
+    } else {
+      v[0] += __shfl_xor(v[0], d);
+    }
+  }
+}
+
+template <int LT, bool DG, bool NT>
 __global__ __launch_bounds__(256) void k_combine_bwd(const uint16_t* __restrict__ dout,
                                                      const uint16_t* __restrict__ rows, int64_t R,
                                                      const int32_t* __restrict__ pos,
                                                      const int32_t* __restrict__ row_src,
                                                      const float* __restrict__ gate, int64_t N, int K, int H,
-                                                     int64_t token_blocks, uint16_t* __restrict__ drows,
+                                                     int64_t row_blocks, uint16_t* __restrict__ drows,
                                                      float* __restrict__ dgate) {
+  constexpr int L = LT < kWave ? LT : kWave;  // of one wave
+  __shared__ float part[4][8];
   const int lane = threadIdx.x & 63;
-  if (blockIdx.x >= token_blocks) {
-    // rows that no pair fills: 64 rows a wave, zeroed by all its lanes
-    const int64_t r0 = ((int64_t(blockIdx.x) - token_blocks) * 4 + (threadIdx.x >> 6)) * kWave;
-    const bool empty = r0 + lane < R && row_src[r0 + lane] < 0;
+  if (blockIdx.x < row_blocks) {
+    // rows that no pair fills: 16 rows a wave, zeroed by all its lanes (they come first, so that they fill the gaps
+    // between the tokens' work rather than follow it)
+    const int64_t r0 = (int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6)) * 16;
+    const bool empty = lane < 16 && r0 + lane < R && row_src[r0 + lane] < 0;
     uint64_t m = __ballot(empty);
-    const uint32_t zero[4] = {0, 0, 0, 0};
     while (m) {
       const int j = __builtin_ctzll(m);
       m &= m - 1;
       uint16_t* dst = drows + (r0 + j) * H;
-      for (int h = lane * 8; h < H; h += kWave * 8) st_bf8(dst + h, H - h, zero);
+      for (int h = lane * 8; h < H; h += kWave * 8) st_bf8<NT>(dst + bf8_column(h, H), H, (bf8){0, 0, 0, 0});
     }
     return;
   }
   const int tl = threadIdx.x % LT;
-  const int64_t t = int64_t(blockIdx.x) * (256 / LT) + threadIdx.x / LT;
+  const int64_t t = (int64_t(blockIdx.x) - row_blocks) * (256 / LT) + threadIdx.x / LT;
   const bool live = t < N;
   for (int k0 = 0; k0 < K; k0 += 8) {
     int p[8];
@@ -338,13 +365,13 @@ __global__ __launch_bounds__(256) void k_combine_bwd(const uint16_t* __restrict_
     }
     if (live) {
       for (int h0 = tl * 8; h0 < H; h0 += LT * 8) {
-        const int n = H - h0;
-        uint32_t d[4], v[DG ? 8 : 1][4];
-        ld_bf8(dout + t * H + h0, n, d);
+        const int at = bf8_column(h0, H);
+        const bf8 d = ld_bf8<false>(dout + t * H + at, H);
+        bf8 v[DG ? 8 : 1];
         if constexpr (DG) {
 #pragma unroll
           for (int u = 0; u < 8; ++u)
-            if (p[u] >= 0) ld_bf8(rows + int64_t(p[u]) * H + h0, n, v[u]);
+            if (p[u] >= 0) v[u] = ld_bf8<NT>(rows + int64_t(p[u]) * H + at, H);
         }
         float df[8];
 #pragma unroll
@@ -352,71 +379,115 @@ __global__ __launch_bounds__(256) void k_combine_bwd(const uint16_t* __restrict_
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           if (p[u] < 0) continue;
-          if constexpr (DG) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              dot[u] = fmaf(df[2 * i], bf_lo(v[u][i]), dot[u]);
-              dot[u] = fmaf(df[2 * i + 1], bf_hi(v[u][i]), dot[u]);
-            }
-          }
-          uint32_t o[4];
+          bf8 o;
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[i] = bf16x2_rne(g[u] * df[2 * i], g[u] * df[2 * i + 1]);
-          st_bf8(drows + int64_t(p[u]) * H + h0, n, o);
+          st_bf8<NT>(drows + int64_t(p[u]) * H + at, H, o);
+        }
+        if constexpr (DG) {
+          const int seen = h0 - at;  // columns that the lane before counts
+          auto add = [&](auto all) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              if (p[u] < 0) continue;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (all() || 2 * i >= seen) dot[u] = fmaf(df[2 * i], bf_lo(v[u][i]), dot[u]);
+                if (all() || 2 * i + 1 >= seen) dot[u] = fmaf(df[2 * i + 1], bf_hi(v[u][i]), dot[u]);
+              }
+            }
+          };
+          if (seen == 0)
+            add(std::true_type{});
+          else
+            add(std::false_type{});
         }
       }
     }
     if constexpr (DG) {
+      sum8<L>(dot, lane);
+      // bits of the lane, from the highest that sum8 exchanged, number the value
+      constexpr int TOP = L >= 8 ? L / 8 : 1;  // lanes that end up with the same value
+      const int u = (tl % L) / TOP;
+      if constexpr (LT > kWave) {
+        __syncthreads();
+        if (lane % TOP == 0) part[threadIdx.x >> 6][lane / TOP] = dot[0];
+        __syncthreads();
+        constexpr int WT = LT / kWave;  // waves of a token
+        if (tl < 8 && live && k0 + tl < K) {
+          float sum = 0.f;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-#pragma unroll
-        for (int s = LT / 2; s >= 1; s >>= 1) dot[u] += __shfl_xor(dot[u], s);
-        const int k = k0 + u;
-        if (live && k < K && tl == (u % LT)) dgate[t * K + k] = dot[u];
+          for (int w = 0; w < WT; ++w) sum += part[(threadIdx.x >> 6) + w][tl];
+          dgate[t * K + k0 + tl] = sum;
+        }
+      } else if (live && tl % TOP == 0 && k0 + u < K) {
+        dgate[t * K + k0 + u] = dot[0];
       }
     }
   }
 }
 
-static int lanes_per_token(int H) { return H <= 64 ? 8 : (H <= 128 ? 16 : (H <= 256 ? 32 : 64)); }
+// Lanes that own a token, and whether its rows are too many bytes for any
+// cache (256 MiB, the last one's size): then they pass it by (262,144 rows of
+// 2048: 239 -> 195 us, the backward 495 -> 451).
+static int lanes_per_token(int H) {
+  return H <= 64 ? 8 : (H <= 128 ? 16 : (H <= 256 ? 32 : (H <= 512 ? 64 : (H <= 1024 ? 128 : 256))));
+}
+static bool past_caches(int64_t R, int H) { return R * H * 2 > (int64_t(256) << 20); }
+
+template <int LT>
+static int combine_lt(const uint16_t* rows, int64_t R, const int32_t* pos, const float* gate, int64_t N, int K, int H,
+                      uint16_t* out, hipStream_t st) {
+  const dim3 grid{unsigned((N * LT + 255) / 256), unsigned((H + LT * 8 - 1) / (LT * 8)), 1u}, block{256u, 1u, 1u};
+  if (past_caches(R, H))
+    hipLaunchKernelGGL((k_combine<LT, true>), grid, block, 0, st, rows, R, pos, gate, N, K, H, out);
+  else
+    hipLaunchKernelGGL((k_combine<LT, false>), grid, block, 0, st, rows, R, pos, gate, N, K, H, out);
+  return int(hipGetLastError());
+}
 
 int launch_combine(const uint16_t* rows, int64_t R, const int32_t* pos, const float* gate, int64_t N, int K, int H,
                    uint16_t* out, hipStream_t st) {
-  const int LT = lanes_per_token(H);
-  const dim3 grid{unsigned((N * LT + 255) / 256), unsigned((H + LT * 8 - 1) / (LT * 8)), 1u}, block{256u, 1u, 1u};
-#define QB_COMBINE(L) hipLaunchKernelGGL((k_combine<L>), grid, block, 0, st, rows, R, pos, gate, N, K, H, out)
-  switch (LT) {
-    case 8: QB_COMBINE(8); break;
-    case 16: QB_COMBINE(16); break;
-    case 32: QB_COMBINE(32); break;
-    default: QB_COMBINE(64); break;
+  switch (lanes_per_token(H)) {
+    case 8: return combine_lt<8>(rows, R, pos, gate, N, K, H, out, st);
+    case 16: return combine_lt<16>(rows, R, pos, gate, N, K, H, out, st);
+    case 32: return combine_lt<32>(rows, R, pos, gate, N, K, H, out, st);
+    case 64: return combine_lt<64>(rows, R, pos, gate, N, K, H, out, st);
+    case 128: return combine_lt<128>(rows, R, pos, gate, N, K, H, out, st);
+    default: return combine_lt<256>(rows, R, pos, gate, N, K, H, out, st);
   }
-#undef QB_COMBINE
-  return int(hipGetLastError());
 }
 
 template <int LT>
 static int bwd_lt(const uint16_t* dout, const uint16_t* rows, int64_t R, const int32_t* pos, const int32_t* row_src,
                   const float* gate, int64_t N, int K, int H, uint16_t* drows, float* dgate, hipStream_t st) {
-  const int64_t tb = (N * LT + 255) / 256, rb = (R + 255) / 256;
+  const int64_t tb = (N * LT + 255) / 256, rb = (R + 63) / 64;
   const dim3 grid{unsigned(tb + rb), 1u, 1u}, block{256u, 1u, 1u};
-  if (dgate)
-    hipLaunchKernelGGL((k_combine_bwd<LT, true>), grid, block, 0, st, dout, rows, R, pos, row_src, gate, N, K, H, tb,
-                       drows, dgate);
-  else
-    hipLaunchKernelGGL((k_combine_bwd<LT, false>), grid, block, 0, st, dout, rows, R, pos, row_src, gate, N, K, H, tb,
-                       drows, dgate);
+#define QB_BWD(DG, NT) \
+  hipLaunchKernelGGL((k_combine_bwd<LT, DG, NT>), grid, block, 0, st, dout, rows, R, pos, row_src, gate, N, K, H, rb, \
+                     drows, dgate)
+  const bool nt = past_caches(R, H);
+  if (dgate) {
+    if (nt) QB_BWD(true, true); else QB_BWD(true, false);
+  } else {
+    if (nt) QB_BWD(false, true); else QB_BWD(false, false);
+  }
+#undef QB_BWD
   return int(hipGetLastError());
 }
 
 int launch_combine_bwd(const uint16_t* dout, const uint16_t* rows, int64_t R, const int32_t* pos,
                        const int32_t* row_src, const float* gate, int64_t N, int K, int H, uint16_t* drows,
                        float* dgate, hipStream_t st) {
-  switch (lanes_per_token(H)) {
+  // 64 lanes a token while its rows stay in the caches: more need a barrier for the sums over their waves (3001 tokens
+  // of 1101: 31 us, 48 with 256 lanes; 32,768 of 2048: 471 and 451)
+  switch (past_caches(R, H) ? lanes_per_token(H) : std::min(lanes_per_token(H), 64)) {
     case 8: return bwd_lt<8>(dout, rows, R, pos, row_src, gate, N, K, H, drows, dgate, st);
     case 16: return bwd_lt<16>(dout, rows, R, pos, row_src, gate, N, K, H, drows, dgate, st);
     case 32: return bwd_lt<32>(dout, rows, R, pos, row_src, gate, N, K, H, drows, dgate, st);
-    default: return bwd_lt<64>(dout, rows, R, pos, row_src, gate, N, K, H, drows, dgate, st);
+    case 64: return bwd_lt<64>(dout, rows, R, pos, row_src, gate, N, K, H, drows, dgate, st);
+    case 128: return bwd_lt<128>(dout, rows, R, pos, row_src, gate, N, K, H, drows, dgate, st);
+    default: return bwd_lt<256>(dout, rows, R, pos, row_src, gate, N, K, H, drows, dgate, st);
   }
 }
 

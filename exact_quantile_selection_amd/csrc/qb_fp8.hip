@@ -63,11 +63,15 @@ struct __attribute__((packed, aligned(4))) Float4 {
 // quantising
 
 // 8 bf16 of a row from p, of which n lie inside it; the others are zero.
+// NT: past the caches.
+template <bool NT>
 __device__ __forceinline__ void ld_half8(const uint16_t* p, int n, uint32_t (&v)[4]) {
   if (n >= 8) {
-    const Half8 t = *reinterpret_cast<const Half8*>(p);
+    typedef uint32_t half8 __attribute__((ext_vector_type(4), aligned(2)));
+    const half8* q = reinterpret_cast<const half8*>(p);
+    const half8 t = NT ? __builtin_nontemporal_load(q) : *q;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = t.v[i];
+    for (int i = 0; i < 4; ++i) v[i] = t[i];
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -116,7 +120,7 @@ __device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t p) {
 
 // Along the rows: a wave takes 512 columns (one word of four scales) of U
 // rows, 16 lanes a block.  Bound by its 2 bytes in, 1 byte out a value.
-template <int U>
+template <int U, bool NT>
 __global__ __launch_bounds__(256) void k_fp8_quantize(const uint16_t* __restrict__ x, int64_t Mx,
                                                       const int32_t* __restrict__ row_src, int64_t M, int C,
                                                       uint8_t* __restrict__ xq, uint8_t* __restrict__ xs) {
@@ -135,7 +139,7 @@ __global__ __launch_bounds__(256) void k_fp8_quantize(const uint16_t* __restrict
       if (src >= Mx) src = -1;
     }
     if (src >= 0 && c0 < C) {
-      ld_half8(x + src * C + c0, C - c0, v[u]);
+      ld_half8<NT>(x + src * C + c0, C - c0, v[u]);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[u][i] = 0;
@@ -172,6 +176,7 @@ __global__ __launch_bounds__(256) void k_fp8_quantize(const uint16_t* __restrict
 // columns of 4 consecutive rows, so that a column's 4 bytes are one word; the
 // words cross to the columns' order through LDS (33 words a column: the 64
 // lanes of a store lie in 64 banks).
+template <bool NT>
 __global__ __launch_bounds__(256) void k_fp8_quantize_cols(const uint16_t* __restrict__ x, int64_t Mx,
                                                            const int32_t* __restrict__ row_src, int64_t M, int C,
                                                            int64_t ld, int64_t sld, uint8_t* __restrict__ xt,
@@ -193,7 +198,7 @@ __global__ __launch_bounds__(256) void k_fp8_quantize_cols(const uint16_t* __res
       if (src >= Mx) src = -1;
     }
     if (src >= 0 && c0 < C) {
-      ld_half8(x + src * C + c0, C - c0, v[u]);
+      ld_half8<NT>(x + src * C + c0, C - c0, v[u]);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[u][i] = 0;
@@ -246,24 +251,34 @@ __global__ __launch_bounds__(256) void k_fp8_quantize_cols(const uint16_t* __res
   }
 }
 
+// An input larger than the last cache (256 MiB) passes it by (135,000 rows of
+// 2048: along the rows 169 -> 145 us, along the columns 177 -> 157).
+static bool past_caches(int64_t rows, int C) { return rows * C * 2 > (int64_t(256) << 20); }
+
 int launch_fp8_quantize(const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M, int C, uint8_t* xq,
                         uint8_t* xs, hipStream_t st) {
   const unsigned chunks = unsigned(fp8_sld(C) / 4);
   // four rows a wave once that still gives every CU its waves
-  if (M * chunks >= 16 * 1024)
-    hipLaunchKernelGGL((k_fp8_quantize<4>), dim3(unsigned((M + 15) / 16), chunks), dim3(256), 0, st, x, Mx, row_src,
-                       M, C, xq, xs);
+  const bool four = M * chunks >= 16 * 1024;
+  const dim3 grid{unsigned(four ? (M + 15) / 16 : (M + 3) / 4), chunks, 1u};
+  if (four && past_caches(M, C))
+    hipLaunchKernelGGL((k_fp8_quantize<4, true>), grid, dim3(256), 0, st, x, Mx, row_src, M, C, xq, xs);
+  else if (four)
+    hipLaunchKernelGGL((k_fp8_quantize<4, false>), grid, dim3(256), 0, st, x, Mx, row_src, M, C, xq, xs);
   else
-    hipLaunchKernelGGL((k_fp8_quantize<1>), dim3(unsigned((M + 3) / 4), chunks), dim3(256), 0, st, x, Mx, row_src, M,
-                       C, xq, xs);
+    hipLaunchKernelGGL((k_fp8_quantize<1, false>), grid, dim3(256), 0, st, x, Mx, row_src, M, C, xq, xs);
   return int(hipGetLastError());
 }
 
 int launch_fp8_quantize_cols(const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M, int C, uint8_t* xt,
                              uint8_t* xts, hipStream_t st) {
   const int64_t ld = fp8_ld(M);
-  hipLaunchKernelGGL(k_fp8_quantize_cols, dim3(unsigned((C + 63) / 64), unsigned(ld / kQBlock)), dim3(256), 0, st, x,
-                     Mx, row_src, M, C, ld, fp8_sld(M), xt, xts);
+  const dim3 grid{unsigned((C + 63) / 64), unsigned(ld / kQBlock), 1u};
+  if (past_caches(M, C))
+    hipLaunchKernelGGL(k_fp8_quantize_cols<true>, grid, dim3(256), 0, st, x, Mx, row_src, M, C, ld, fp8_sld(M), xt, xts);
+  else
+    hipLaunchKernelGGL(k_fp8_quantize_cols<false>, grid, dim3(256), 0, st, x, Mx, row_src, M, C, ld, fp8_sld(M), xt,
+                       xts);
   return int(hipGetLastError());
 }
 
@@ -1059,7 +1074,8 @@ static int gemm_thin(const Gemm& g, hipStream_t st) {
 // workgroup, and two where a wave's part is then still four blocks long (one
 // token through 4096 x 4096: 20.5, 11.6, 7.4, 5.2 us with 1, 2, 4, 8; 128 rows
 // over 256 experts of 1024 x 2048: 47, 44, 50, 90, since each workgroup of
-// eight has so little of the weight that finding its tile counts).
+// eight has so little of the weight that finding its tile counts; tiles take
+// 34).
 template <int MT>
 static int gemm_few(const Gemm& g, hipStream_t st) {
   const int64_t waves = row_tiles(g, 16 * MT) * ((g.N + 15) / 16);
@@ -1077,19 +1093,18 @@ int launch_fp8_product(const uint8_t* xq, const uint8_t* xs, const uint8_t* w, c
                        int64_t ldk, const int32_t* off, int G, bool exact, uint16_t* y, hipStream_t st) {
   const Gemm g{xq, xs, w, ws, M, N, ldk, fp8_sld(ldk), off, G, y};
   const int64_t rows = off ? (M + G - 1) / G : M;  // rows of an expert, on average
-  // few rows and too few tiles for the CUs: one wave's 16 columns at a time (64 rows, 4096 x 4096: 16.3 us, tiles
-  // 21.8; 64 rows over 16 experts of 1024 x 2048: 10.1, tiles 13.0, but 1024 rows over them 46, tiles 15)
-  if (rows <= 64 && row_tiles(g, 128) * ((N + 127) / 128) <= device_cu_count() / 2) {
-    if (rows <= 16) return gemm_few<1>(g, st);
-    if (rows <= 32) return gemm_few<2>(g, st);
-    return gemm_few<4>(g, st);
-  }
   auto tiles = [&](int b) { return row_tiles(g, b) * ((N + b - 1) / b); };
-  // an expert of up to 128 rows fills no more than half of a large tile
+  const int64_t cu = device_cu_count();
+  // few rows and no tile for every CU: 16 columns of the weight a wave (32 rows, 4096 x 4096: 10.4 us, tiles 11.4; one
+  // row 5.3 and 11.2; 64 rows 16.7 and 11.5)
+  if (rows <= 32 && tiles(64) <= cu) return rows <= 16 ? gemm_few<1>(g, st) : gemm_few<2>(g, st);
+  // an expert of up to 128 rows fills no more than half of a 256 x 256 tile, and one of up to 16 a quarter of a 64 x
+  // 64 one; of the tiles that experts' rows make at most, some are not there
   const int64_t t256 = rows <= 128 && off ? 0 : tiles(256);
+  const int64_t t64 = !off ? tiles(64) : (rows <= 16 ? 0 : tiles(64) * 2 / 3);
   const double uneven = off ? 0.1 : 0.0;
-  return exact ? gemm<false, true>(g, t256, tiles(128), tiles(64), uneven, st)
-               : gemm<false, false>(g, t256, tiles(128), tiles(64), uneven, st);
+  return exact ? gemm<false, true>(g, t256, tiles(128), t64, uneven, st)
+               : gemm<false, false>(g, t256, tiles(128), t64, uneven, st);
 }
 
 int launch_fp8_weight_grad(const uint8_t* dyt, const uint8_t* dyts, const uint8_t* xt, const uint8_t* xts, int N,
