@@ -354,3 +354,55 @@ def test_graph_replays():
         step()
         torch.cuda.synchronize()
         assert torch.equal(a.view(torch.int16), y.view(torch.int16)) and torch.equal(a, y) and torch.equal(b, dw)
+
+
+# many tiles a workgroup: 128 x 128 and 256 x 256 ones, with partial tiles at both ends
+@pytest.mark.parametrize("M,N,C", [(4097, 3000, 130), (4090, 4090, 384), (8101, 8190, 300)])
+def test_product_of_many_tiles(M, N, C):
+    rng = np.random.default_rng(M)
+    G.say(f"product of many tiles M={M} N={N} C={C}")
+    xq, xs, x = quantised(data(rng, M, C))
+    wq, ws, w = weight(rng, N, C)
+    for exact in (True, False):
+        y = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device=G.DEV)
+        qb.qb_fp8_product(xq, xs, wq, ws, y, exact=exact)
+        torch.cuda.synchronize()
+        near(y, x, w, C, HALF, 0.0 if exact else DROP)
+
+
+@pytest.mark.parametrize("kind", ["any", "one"])
+@pytest.mark.parametrize("N,C,align", [(2047, 257, 1), (2047, 640, 128), (700, 130, 128)])
+def test_experts_of_many_tiles(N, C, align, kind):
+    rng = np.random.default_rng(N + C)
+    G_, M = 16, 20000
+    off = offsets(rng, G_, M, kind, align)
+    rows = int(off[-1]) + 3
+    G.say(f"experts of many tiles N={N} C={C} align={align} {kind}")
+    xq, xs, x = quantised(data(rng, rows, C))
+    wq, ws, w = weight(rng, N, C, (G_,))
+    y = torch.full((rows, N), 77.0, dtype=torch.bfloat16, device=G.DEV)
+    qb.qb_fp8_product(xq, xs, wq, ws, y, off=G.dev(off))
+    torch.cuda.synchronize()
+    for e in range(G_):
+        i, j = int(off[e]), int(off[e + 1])
+        if i < j:
+            near(y[i:j], x[i:j], w[e], C, HALF, DROP)
+    assert (y[off[-1]:] == 77.0).all()
+
+
+@pytest.mark.parametrize("G_,M,N,C,kind", [(0, 300, 4000, 4100, ""), (0, 700, 4093, 4090, ""),
+                                           (16, 3000, 1000, 2000, "any"), (16, 3000, 700, 1163, "any"),
+                                           (16, 2000, 1000, 2000, "one")])
+def test_weight_gradient_of_many_tiles(G_, M, N, C, kind):
+    rng = np.random.default_rng(N + C)
+    off = offsets(rng, G_, M, kind, 128) if G_ else np.array([0, M])
+    rows = int(off[-1])
+    G.say(f"weight gradient of many tiles G={G_} M={rows} N={N} C={C} {kind}")
+    dq, ds, d = quantised_cols(data(rng, rows, N))
+    xq, xs, x = quantised_cols(data(rng, rows, C))
+    dw = torch.full(((G_,) if G_ else ()) + (N, C), float("nan"), device=G.DEV)
+    qb.qb_fp8_weight_grad(dq, ds, xq, xs, dw, off=G.dev(off) if G_ else None)
+    torch.cuda.synchronize()
+    for e in range(max(G_, 1)):
+        i, j = int(off[e]), int(off[e + 1])
+        near(dw[e] if G_ else dw, d[:, i:j], x[:, i:j], j - i, 0.0)
