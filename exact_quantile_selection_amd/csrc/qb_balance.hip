@@ -193,9 +193,9 @@ BalWs balance_ws_layout(int64_t N, int E, int B) {
 
 // Entries m .. K - 1 of a row's list, where the K-th and the next share their
 // upper bits (`edge`): the largest whole values among those that do, equal
-// ones by lower expert.  It reads the row again rather than hold registers in
-// every row's way; a row needs it once in some 300 (scores as of a router of
-// 256 experts), and then mostly for one entry.
+// ones by lower expert.  It reads the row from LDS again rather than hold
+// registers in every row's way; a row needs it once in some 300 (scores as of
+// a router of 256 experts), and then mostly for one entry.
 template <int E>
 __device__ __forceinline__ void bal_edge(const float* src, const float* lds_b, int ql, int m, int K, uint32_t edge,
                                          uint2* stage) {
@@ -247,10 +247,12 @@ __global__ __launch_bounds__(kBalThreads, P <= 9 ? 4 : 3) void k_balance_fwd(
   using S = BalShape<E>;
   constexpr int LPR = S::LPR, F4 = S::F4, RPW = S::RPW, R = S::R, KU = (P - 1 + LPR - 1) / LPR;
   __shared__ __align__(16) float lds_b[E];
-  __shared__ uint2 stage[kBalWaves][RPW][P];  // a row's chosen biased scores and experts
+  __shared__ uint2 stage[kBalWaves][RPW][P - 1];  // a row's chosen biased scores and experts
+  // the step's rows: a chosen score is read from here by its expert's number (from memory it is a trip to L2 more)
+  __shared__ __align__(16) float lds_x[kBalWaves][RPW][E];
   __shared__ int lds_cnt[STATS ? E : 1];
-  __shared__ int lds_live[kBalWaves];
   __shared__ __align__(16) float lds_p[kBalWaves][STATS ? E : 4];
+  int* const lds_live = reinterpret_cast<int*>(&lds_p[0][0]);  // the two are never in use together
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int rho = lane / LPR, ql = lane % LPR;
@@ -316,11 +318,14 @@ __global__ __launch_bounds__(kBalThreads, P <= 9 ? 4 : 3) void k_balance_fwd(
     const bool lv = here && row >= first && row < last && (!valid || valid[ld_row] != 0);
     const bool whole = now.end >= step_end;  // the step's rows are all of one sequence
     Run now_p = now;
+    float* xrow = lds_x[wave][rho];
     float top[P], inv = 0.f, up = 1.0f;
     if (busy) {
       f32x4 x[F4];
 #pragma unroll
       for (int t = 0; t < F4; ++t) x[t] = *reinterpret_cast<const f32x4*>(src + 4 * (LPR * t + ql));
+#pragma unroll
+      for (int t = 0; t < F4; ++t) *reinterpret_cast<f32x4*>(xrow + 4 * (LPR * t + ql)) = x[t];
       // the P largest biased scores, each with its expert in the low bits
 #pragma unroll
       for (int k = 0; k < P; ++k) top[k] = __builtin_bit_cast(float, 0xFF7FFFFFu & ~uint32_t(E - 1));
@@ -373,7 +378,7 @@ __global__ __launch_bounds__(kBalThreads, P <= 9 ? 4 : 3) void k_balance_fwd(
             if (!whole && busy && mine && lv)  // the rows are read again: kept, they would cost the sorting its registers
 #pragma unroll
               for (int t = 0; t < F4; ++t) {
-                const f32x4 x = *reinterpret_cast<const f32x4*>(src + 4 * (LPR * t + ql));
+                const f32x4 x = *reinterpret_cast<const f32x4*>(xrow + 4 * (LPR * t + ql));
 #pragma unroll
                 for (int c = 0; c < 4; ++c) acc[t][c] = fmaf(x[c] * up, inv, acc[t][c]);
               }
@@ -402,7 +407,7 @@ __global__ __launch_bounds__(kBalThreads, P <= 9 ? 4 : 3) void k_balance_fwd(
           if (u * LPR + j < P) m = ql == j ? __builtin_bit_cast(uint32_t, top[u * LPR + j]) : m;
         const int k = ql + u * LPR, n = int(m & uint32_t(S::V - 1)), from = int(m & uint32_t(E - 1)) / S::V;
         id[u] = 4 * (LPR * (n >> 2) + from) + (n & 3);
-        sv[u] = src[id[u]];
+        sv[u] = xrow[id[u]];
         v[u] = sv[u] + lds_b[id[u]];
         if (k < K) mine[k] = make_uint2(__builtin_bit_cast(uint32_t, v[u]), uint32_t(id[u]));
       }
@@ -411,7 +416,7 @@ __global__ __launch_bounds__(kBalThreads, P <= 9 ? 4 : 3) void k_balance_fwd(
           int m = 0;
 #pragma unroll
           for (int k = 0; k < P - 1; ++k) m += k < K && (__builtin_bit_cast(uint32_t, top[k]) ^ edge) >= uint32_t(E) ? 1 : 0;
-          bal_edge<E>(src, lds_b, ql, m, K, edge, mine);
+          bal_edge<E>(xrow, lds_b, ql, m, K, edge, mine);
         }
         __builtin_amdgcn_wave_barrier();
         asm volatile("" ::: "memory");
@@ -419,7 +424,7 @@ __global__ __launch_bounds__(kBalThreads, P <= 9 ? 4 : 3) void k_balance_fwd(
         for (int u = 0; u < KU; ++u) {
           const int k = ql + u * LPR;
           id[u] = k < K ? int(mine[k].y & uint32_t(E - 1)) : 0;
-          sv[u] = src[id[u]];
+          sv[u] = xrow[id[u]];
           v[u] = sv[u] + lds_b[id[u]];
         }
       }

@@ -171,6 +171,17 @@ __global__ __launch_bounds__(256) void k_fp8_quantize(const uint16_t* __restrict
   }
 }
 
+// Lane l ^ D's word, D 16 or 32 (the instruction exchanges the D-lane halves of
+// two registers: one result is the own word, the other the partner's).
+template <int D>
+__device__ __forceinline__ uint32_t swapped(uint32_t a) {
+  uint32_t b = a;
+  asm volatile("" : "+v"(b));  // two registers: with one and the same operand the compiler takes the results as equal
+  const auto h = D == 16 ? __builtin_amdgcn_permlane16_swap(a, b, false, false)
+                         : __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  return threadIdx.x & D ? h[0] : h[1];
+}
+
 // Along the columns: a workgroup takes 128 rows (one block) of 64 columns and
 // writes them transposed, 128 contiguous bytes a column.  A thread holds 8
 // columns of 4 consecutive rows, so that a column's 4 bytes are one word; the
@@ -217,11 +228,10 @@ __global__ __launch_bounds__(256) void k_fp8_quantize_cols(const uint16_t* __res
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-#pragma unroll
-    for (int d = 8; d < kWave; d <<= 1) {
-      const uint32_t o = __shfl_xor(top[j], d);
-      top[j] = top[j] > o ? top[j] : o;
-    }
+    auto join = [&](uint32_t o) { top[j] = top[j] > o ? top[j] : o; };
+    join(uint32_t(__builtin_amdgcn_mov_dpp(int(top[j]), 0x128, 0xF, 0xF, true)));  // row_ror:8
+    join(swapped<16>(top[j]));
+    join(swapped<32>(top[j]));
     if (lane < 8) tops[wave][cg * 8 + j] = top[j];
   }
   __syncthreads();
