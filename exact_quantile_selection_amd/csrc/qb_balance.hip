@@ -17,8 +17,16 @@
 //   dgate/ds_ik = (g_ik - sum_k' g_ik' gate_ik') / sum_k s_ik
 //   dlogit = ds s (1 - s).
 //
-// Both passes read the scores once from HBM and are bound by that stream.  A
-// row is held by LPR lanes in registers (V = E / LPR scores a lane), so
+// Both passes read the scores once from HBM.  131,072 x 256 with K = 6: the
+// forward takes 32.7 us (4.1 TB/s), bound by its vector instructions (86% of
+// the issue slots; the K largest cost 7 of them a score), the sums 8.7 us, bound
+// by waiting, the gradient 47 us (5.7 TB/s), bound by HBM.  The K largest are
+// kept as biased scores whose low bits are the expert's number: a list's entry
+// is then one register, insertion one median, and no second look for the
+// chosen ones is needed (with a mask of them: 41 us); rows where the K-th and
+// the next share the upper bits are settled by the whole values.
+//
+// A row is held by LPR lanes in registers (V = E / LPR scores a lane), so
 // column sums of p stay in a lane's registers from row to row and only the
 // end of a sequence's stretch of rows reduces them across lanes.  A workgroup
 // takes a chunk of T consecutive rows and leaves one partial row (E counts,
