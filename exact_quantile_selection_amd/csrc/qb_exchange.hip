@@ -196,8 +196,9 @@ __global__ __launch_bounds__(kDispThreads) void k_dispatch(const int32_t* __rest
   // rows past the last expert
   if (blk == 0)
     for (int j = tid; j <= E; j += kDispThreads) off[j] = start[j];
-  for (int e = blk + nblk * wave; e < E; e += nblk * kDispWaves)
-    for (int64_t r = int64_t(start[e]) + used[e] + lane; r < start[e + 1] && r < R; r += kWave) row_src[r] = -1;
+  if (align > 1)  // (else there are none of the former: 16 tokens of 256 experts 4.9 -> 3.8 us)
+    for (int e = blk + nblk * wave; e < E; e += nblk * kDispWaves)
+      for (int64_t r = int64_t(start[e]) + used[e] + lane; r < start[e + 1] && r < R; r += kWave) row_src[r] = -1;
   for (int64_t r = int64_t(start[E]) + int64_t(blk) * kDispThreads + tid; r < R; r += int64_t(nblk) * kDispThreads)
     row_src[r] = -1;
 }
