@@ -231,41 +231,49 @@ __device__ __forceinline__ float bf_hi(uint32_t p) { return __builtin_bit_cast(f
 // A lane's 8 columns, h0 on.  Near a row's end they begin earlier, at H - 8,
 // so that every access is whole: the columns that the lane before has too are
 // computed and written twice, to the same values.  Rows of fewer than 8
-// columns go element by element.
-template <bool NT>
+// columns (SHORT: kernels of their own, as the branches would cost every
+// other row more than its loads) go element by element.
+template <bool NT, bool SHORT>
 __device__ __forceinline__ bf8 ld_bf8(const uint16_t* p, int H) {
-  if (H >= 8) {
-    if constexpr (NT) return __builtin_nontemporal_load(reinterpret_cast<const bf8*>(p));
+  if constexpr (SHORT) {
+    bf8 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = 2 * i < H ? p[2 * i] : 0, hi = 2 * i + 1 < H ? p[2 * i + 1] : 0;
+      v[i] = lo | (hi << 16);
+    }
+    return v;
+  } else if constexpr (NT) {
+    return __builtin_nontemporal_load(reinterpret_cast<const bf8*>(p));
+  } else {
     return *reinterpret_cast<const bf8*>(p);
   }
-  bf8 v;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = 2 * i < H ? p[2 * i] : 0, hi = 2 * i + 1 < H ? p[2 * i + 1] : 0;
-    v[i] = lo | (hi << 16);
-  }
-  return v;
 }
-template <bool NT>
+template <bool NT, bool SHORT>
 __device__ __forceinline__ void st_bf8(uint16_t* p, int H, bf8 v) {
-  if (H >= 8) {
-    if constexpr (NT)
-      __builtin_nontemporal_store(v, reinterpret_cast<bf8*>(p));
-    else
-      *reinterpret_cast<bf8*>(p) = v;
-    return;
-  }
+  if constexpr (SHORT) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (2 * i < H) p[2 * i] = uint16_t(v[i]);
-    if (2 * i + 1 < H) p[2 * i + 1] = uint16_t(v[i] >> 16);
+    for (int i = 0; i < 4; ++i) {
+      if (2 * i < H) p[2 * i] = uint16_t(v[i]);
+      if (2 * i + 1 < H) p[2 * i + 1] = uint16_t(v[i] >> 16);
+    }
+  } else if constexpr (NT) {
+    __builtin_nontemporal_store(v, reinterpret_cast<bf8*>(p));
+  } else {
+    *reinterpret_cast<bf8*>(p) = v;
   }
+}
+// A value that all lanes of a token hold: one for the wave where the token has all of it.
+template <int LT, class V>
+__device__ __forceinline__ V of_token(V x) {
+  if constexpr (LT >= kWave) return __builtin_bit_cast(V, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
+  return x;
 }
 __device__ __forceinline__ int bf8_column(int h0, int H) { return H < 8 ? 0 : (h0 < H - 8 ? h0 : H - 8); }
 
 // LT lanes own a token: as many as its row has 8 columns for, 256 at most, so
 // that a row's 4 KiB are read by one workgroup at once.
-template <int LT, bool NT>
+template <int LT, bool NT, bool SHORT = false>
 __global__ __launch_bounds__(256) void k_combine(const uint16_t* __restrict__ rows, int64_t R,
                                                  const int32_t* __restrict__ pos, const float* __restrict__ gate,
                                                  int64_t N, int K, int H, uint16_t* __restrict__ out) {
@@ -284,10 +292,10 @@ __global__ __launch_bounds__(256) void k_combine(const uint16_t* __restrict__ ro
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int k = k0 + u;
-      const int p = k < K ? pos[t * K + k] : -1;
+      const int p = of_token<LT>(k < K ? pos[t * K + k] : -1);
       const bool on = p >= 0 && p < R;
       g[u] = on ? (gate ? gate[t * K + k] : 1.0f) : 0.f;
-      v[u] = on ? ld_bf8<NT>(rows + int64_t(p) * H + at, H) : (bf8){0, 0, 0, 0};
+      v[u] = on ? ld_bf8<NT, SHORT>(rows + int64_t(p) * H + at, H) : (bf8){0, 0, 0, 0};
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u)
@@ -300,7 +308,7 @@ __global__ __launch_bounds__(256) void k_combine(const uint16_t* __restrict__ ro
   bf8 o;
 #pragma unroll
   for (int i = 0; i < 4; ++i) o[i] = bf16x2_rne(acc[2 * i], acc[2 * i + 1]);
-  st_bf8<NT>(out + t * H + at, H, o);
+  st_bf8<NT, SHORT>(out + t * H + at, H, o);
 }
 
 // The sums of eight values over L lanes (64 at most), value (lane >> 3) & 7
@@ -326,7 +334,7 @@ __device__ __forceinline__ void sum8(float (&v)[8], int lane) {
   }
 }
 
-template <int LT, bool DG, bool NT>
+template <int LT, bool DG, bool NT, bool SHORT = false>
 __global__ __launch_bounds__(256) void k_combine_bwd(const uint16_t* __restrict__ dout,
                                                      const uint16_t* __restrict__ rows, int64_t R,
                                                      const int32_t* __restrict__ pos,
@@ -347,7 +355,7 @@ __global__ __launch_bounds__(256) void k_combine_bwd(const uint16_t* __restrict_
       const int j = __builtin_ctzll(m);
       m &= m - 1;
       uint16_t* dst = drows + (r0 + j) * H;
-      for (int h = lane * 8; h < H; h += kWave * 8) st_bf8<NT>(dst + bf8_column(h, H), H, (bf8){0, 0, 0, 0});
+      for (int h = lane * 8; h < H; h += kWave * 8) st_bf8<NT, SHORT>(dst + bf8_column(h, H), H, (bf8){0, 0, 0, 0});
     }
     return;
   }
@@ -360,20 +368,20 @@ __global__ __launch_bounds__(256) void k_combine_bwd(const uint16_t* __restrict_
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int k = k0 + u;
-      int q = live && k < K ? pos[t * K + k] : -1;
-      p[u] = q < R ? q : -1;
-      g[u] = p[u] >= 0 ? (gate ? gate[t * K + k] : 1.0f) : 0.f;
+      const int q = live && k < K ? pos[t * K + k] : -1;
+      p[u] = of_token<LT>(q < R ? q : -1);
+      g[u] = of_token<LT>(p[u] >= 0 ? (gate ? gate[t * K + k] : 1.0f) : 0.f);
       dot[u] = 0.f;
     }
     if (live) {
       for (int h0 = tl * 8; h0 < H; h0 += LT * 8) {
         const int at = bf8_column(h0, H);
-        const bf8 d = ld_bf8<false>(dout + t * H + at, H);
+        const bf8 d = ld_bf8<false, SHORT>(dout + t * H + at, H);
         bf8 v[DG ? 8 : 1];
         if constexpr (DG) {
 #pragma unroll
           for (int u = 0; u < 8; ++u)
-            if (p[u] >= 0) v[u] = ld_bf8<NT>(rows + int64_t(p[u]) * H + at, H);
+            if (p[u] >= 0) v[u] = ld_bf8<NT, SHORT>(rows + int64_t(p[u]) * H + at, H);
         }
         float df[8];
 #pragma unroll
@@ -384,7 +392,7 @@ __global__ __launch_bounds__(256) void k_combine_bwd(const uint16_t* __restrict_
           bf8 o;
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[i] = bf16x2_rne(g[u] * df[2 * i], g[u] * df[2 * i + 1]);
-          st_bf8<NT>(drows + int64_t(p[u]) * H + at, H, o);
+          st_bf8<NT, SHORT>(drows + int64_t(p[u]) * H + at, H, o);
         }
         if constexpr (DG) {
           const int seen = h0 - at;  // columns that the lane before counts
@@ -441,7 +449,9 @@ template <int LT>
 static int combine_lt(const uint16_t* rows, int64_t R, const int32_t* pos, const float* gate, int64_t N, int K, int H,
                       uint16_t* out, hipStream_t st) {
   const dim3 grid{unsigned((N * LT + 255) / 256), unsigned((H + LT * 8 - 1) / (LT * 8)), 1u}, block{256u, 1u, 1u};
-  if (past_caches(R, H))
+  if (LT == 8 && H < 8)
+    hipLaunchKernelGGL((k_combine<8, false, true>), grid, block, 0, st, rows, R, pos, gate, N, K, H, out);
+  else if (past_caches(R, H))
     hipLaunchKernelGGL((k_combine<LT, true>), grid, block, 0, st, rows, R, pos, gate, N, K, H, out);
   else
     hipLaunchKernelGGL((k_combine<LT, false>), grid, block, 0, st, rows, R, pos, gate, N, K, H, out);
@@ -465,14 +475,15 @@ static int bwd_lt(const uint16_t* dout, const uint16_t* rows, int64_t R, const i
                   const float* gate, int64_t N, int K, int H, uint16_t* drows, float* dgate, hipStream_t st) {
   const int64_t tb = (N * LT + 255) / 256, rb = (R + 63) / 64;
   const dim3 grid{unsigned(tb + rb), 1u, 1u}, block{256u, 1u, 1u};
-#define QB_BWD(DG, NT) \
-  hipLaunchKernelGGL((k_combine_bwd<LT, DG, NT>), grid, block, 0, st, dout, rows, R, pos, row_src, gate, N, K, H, rb, \
-                     drows, dgate)
-  const bool nt = past_caches(R, H);
-  if (dgate) {
-    if (nt) QB_BWD(true, true); else QB_BWD(true, false);
+#define QB_BWD(LANES, DG, NT, SHORT)                                                                                \
+  hipLaunchKernelGGL((k_combine_bwd<LANES, DG, NT, SHORT>), grid, block, 0, st, dout, rows, R, pos, row_src, gate, N, \
+                     K, H, rb, drows, dgate)
+  if (LT == 8 && H < 8) {
+    if (dgate) QB_BWD(8, true, false, true); else QB_BWD(8, false, false, true);
+  } else if (past_caches(R, H)) {
+    if (dgate) QB_BWD(LT, true, true, false); else QB_BWD(LT, false, true, false);
   } else {
-    if (nt) QB_BWD(false, true); else QB_BWD(false, false);
+    if (dgate) QB_BWD(LT, true, false, false); else QB_BWD(LT, false, false, false);
   }
 #undef QB_BWD
   return int(hipGetLastError());
@@ -482,7 +493,7 @@ int launch_combine_bwd(const uint16_t* dout, const uint16_t* rows, int64_t R, co
                        const int32_t* row_src, const float* gate, int64_t N, int K, int H, uint16_t* drows,
                        float* dgate, hipStream_t st) {
   // 64 lanes a token while its rows stay in the caches: more need a barrier for the sums over their waves (3001 tokens
-  // of 1101: 31 us, 48 with 256 lanes; 32,768 of 2048: 471 and 451)
+  // of 1101: 31 us, 36 with 256 lanes; 32,768 of 2048: 471 and 451)
   switch (past_caches(R, H) ? lanes_per_token(H) : std::min(lanes_per_token(H), 64)) {
     case 8: return bwd_lt<8>(dout, rows, R, pos, row_src, gate, N, K, H, drows, dgate, st);
     case 16: return bwd_lt<16>(dout, rows, R, pos, row_src, gate, N, K, H, drows, dgate, st);
