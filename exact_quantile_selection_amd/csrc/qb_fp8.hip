@@ -269,9 +269,11 @@ __global__ __launch_bounds__(256) void k_fp8_quantize_cols(const uint16_t* __res
   }
 }
 
-// An input larger than the last cache (256 MiB) passes it by (135,000 rows of
-// 2048: along the rows 169 -> 145 us, along the columns 177 -> 157).
-static bool past_caches(int64_t rows, int C) { return rows * C * 2 > (int64_t(256) << 20); }
+// An input of half the last cache (256 MiB) or more, which the results push
+// out of it, passes it by (135,000 rows of 2048: along the rows 169 -> 145 us,
+// along the columns 177 -> 157; 8192 of 8192: 53 -> 50 and 50 -> 47; 8192 of
+// 4096: 25 -> 23 but 23 -> 25).
+static bool past_caches(int64_t rows, int C) { return rows * C * 2 >= (int64_t(128) << 20); }
 
 int launch_fp8_quantize(const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M, int C, uint8_t* xq,
                         uint8_t* xs, hipStream_t st) {
