@@ -348,14 +348,15 @@ __global__ __launch_bounds__(256) void k_combine_bwd(const uint16_t* __restrict_
   if (blockIdx.x < row_blocks) {
     // rows that no pair fills: 16 rows a wave, zeroed by all its lanes (they come first, so that they fill the gaps
     // between the tokens' work rather than follow it)
-    const int64_t r0 = (int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6)) * 16;
-    const bool empty = lane < 16 && r0 + lane < R && row_src[r0 + lane] < 0;
-    uint64_t m = __ballot(empty);
-    while (m) {
-      const int j = __builtin_ctzll(m);
-      m &= m - 1;
-      uint16_t* dst = drows + (r0 + j) * H;
-      for (int h = lane * 8; h < H; h += kWave * 8) st_bf8<NT, SHORT>(dst + bf8_column(h, H), H, (bf8){0, 0, 0, 0});
+    for (int64_t r0 = (int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6)) * 16; r0 < R; r0 += row_blocks * 64) {
+      const bool empty = lane < 16 && r0 + lane < R && row_src[r0 + lane] < 0;
+      uint64_t m = __ballot(empty);
+      while (m) {
+        const int j = __builtin_ctzll(m);
+        m &= m - 1;
+        uint16_t* dst = drows + (r0 + j) * H;
+        for (int h = lane * 8; h < H; h += kWave * 8) st_bf8<NT, SHORT>(dst + bf8_column(h, H), H, (bf8){0, 0, 0, 0});
+      }
     }
     return;
   }
@@ -437,11 +438,17 @@ __global__ __launch_bounds__(256) void k_combine_bwd(const uint16_t* __restrict_
   }
 }
 
+// A launch takes fewer than 2^32 threads along an axis: above 2^23 tokens one
+// has 128 lanes at most, and the rows that no pair fills are gone through by
+// kZeroBlocks workgroups at most, 64 rows each at a time.
+constexpr int64_t kZeroBlocks = int64_t(1) << 17;
+
 // Lanes that own a token, and whether its rows are too many bytes for any
 // cache (256 MiB, the last one's size): then they pass it by (262,144 rows of
 // 2048: 239 -> 195 us, the backward 495 -> 451).
-static int lanes_per_token(int H) {
-  return H <= 64 ? 8 : (H <= 128 ? 16 : (H <= 256 ? 32 : (H <= 512 ? 64 : (H <= 1024 ? 128 : 256))));
+static int lanes_per_token(int64_t N, int H) {
+  if (H > 1024 && N <= (int64_t(1) << 23)) return 256;
+  return H <= 64 ? 8 : (H <= 128 ? 16 : (H <= 256 ? 32 : (H <= 512 ? 64 : 128)));
 }
 static bool past_caches(int64_t R, int H) { return R * H * 2 > (int64_t(256) << 20); }
 
@@ -460,7 +467,7 @@ static int combine_lt(const uint16_t* rows, int64_t R, const int32_t* pos, const
 
 int launch_combine(const uint16_t* rows, int64_t R, const int32_t* pos, const float* gate, int64_t N, int K, int H,
                    uint16_t* out, hipStream_t st) {
-  switch (lanes_per_token(H)) {
+  switch (lanes_per_token(N, H)) {
     case 8: return combine_lt<8>(rows, R, pos, gate, N, K, H, out, st);
     case 16: return combine_lt<16>(rows, R, pos, gate, N, K, H, out, st);
     case 32: return combine_lt<32>(rows, R, pos, gate, N, K, H, out, st);
@@ -473,7 +480,7 @@ int launch_combine(const uint16_t* rows, int64_t R, const int32_t* pos, const fl
 template <int LT>
 static int bwd_lt(const uint16_t* dout, const uint16_t* rows, int64_t R, const int32_t* pos, const int32_t* row_src,
                   const float* gate, int64_t N, int K, int H, uint16_t* drows, float* dgate, hipStream_t st) {
-  const int64_t tb = (N * LT + 255) / 256, rb = (R + 63) / 64;
+  const int64_t tb = (N * LT + 255) / 256, rb = std::min((R + 63) / 64, kZeroBlocks);
   const dim3 grid{unsigned(tb + rb), 1u, 1u}, block{256u, 1u, 1u};
 #define QB_BWD(LANES, DG, NT, SHORT)                                                                                \
   hipLaunchKernelGGL((k_combine_bwd<LANES, DG, NT, SHORT>), grid, block, 0, st, dout, rows, R, pos, row_src, gate, N, \
@@ -494,7 +501,7 @@ int launch_combine_bwd(const uint16_t* dout, const uint16_t* rows, int64_t R, co
                        float* dgate, hipStream_t st) {
   // 64 lanes a token while its rows stay in the caches: more need a barrier for the sums over their waves (3001 tokens
   // of 1101: 31 us, 36 with 256 lanes; 32,768 of 2048: 471 and 451)
-  switch (past_caches(R, H) ? lanes_per_token(H) : std::min(lanes_per_token(H), 64)) {
+  switch (past_caches(R, H) ? lanes_per_token(N, H) : std::min(lanes_per_token(N, H), 64)) {
     case 8: return bwd_lt<8>(dout, rows, R, pos, row_src, gate, N, K, H, drows, dgate, st);
     case 16: return bwd_lt<16>(dout, rows, R, pos, row_src, gate, N, K, H, drows, dgate, st);
     case 32: return bwd_lt<32>(dout, rows, R, pos, row_src, gate, N, K, H, drows, dgate, st);

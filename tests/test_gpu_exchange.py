@@ -203,3 +203,50 @@ def test_graph_replays():
         torch.cuda.synchronize()
         for a, t in zip(got, (off, src, pos, out, drows, dgate)):
             G.assert_same(f"replay {seed}", a, G.host(t.view(torch.int16) if t.dtype == torch.bfloat16 else t))
+
+
+def test_the_most_tokens():
+    """2^24 tokens of more than 1024 columns: 32 bits do not number their
+    columns' threads.  Each token copies one row, so everything is exact but
+    dgate, a sum of H products."""
+    N, H, R = 1 << 24, 1032, 3
+    rng = np.random.default_rng(31)
+    rows = bf16(rng, R, H)
+    i = torch.arange(N, dtype=torch.int32, device=G.DEV)
+    pos = (i % R)[:, None].contiguous()
+    out = torch.full((N, H), 7.0, dtype=torch.bfloat16, device=G.DEV)
+    qb.qb_combine(rows, pos, out)
+    step = 1 << 20
+    for a in range(0, N, step):
+        assert torch.equal(out[a:a + step], rows[pos[a:a + step, 0].long()])
+    # the gradients: token t has row N - 1 - t, whose value is the token's own `out`
+    back = (N - 1 - i).contiguous()
+    drows = torch.full((N, H), 7.0, dtype=torch.bfloat16, device=G.DEV)
+    dgate = torch.full((N, 1), 7.0, device=G.DEV)
+    qb.qb_combine_backward(out, out, back[:, None].contiguous(), back, drows, dgate=dgate)
+    r = rows.double().cpu()
+    dots, sizes = (r @ r.T).to(G.DEV), (r.abs() @ r.abs().T).to(G.DEV)
+    for a in range(0, N, step):
+        mine = (i[a:a + step] % R).long()
+        other = ((N - 1 - i[a:a + step]) % R).long()
+        assert torch.equal(drows[a:a + step], rows[other])
+        off = (dgate[a:a + step, 0].double() - dots[mine, other]).abs()
+        assert bool((off <= (H + 8) * U * sizes[mine, other]).all())
+    del out, drows
+    torch.cuda.empty_cache()
+
+
+def test_the_most_empty_rows():
+    """2^30 rows, more than a launch has threads for, of which a few belong to a pair."""
+    R = (1 << 30) + 77
+    src = torch.full((R,), -1, dtype=torch.int32, device=G.DEV)
+    kept = torch.tensor([0, 15, 16, 64, (1 << 23) - 1, 1 << 23, (1 << 29) + 5, R - 1], device=G.DEV)
+    src[kept] = 0
+    drows = torch.full((R, 1), 7.0, dtype=torch.bfloat16, device=G.DEV)
+    none = torch.zeros(0, 1, device=G.DEV)
+    qb.qb_combine_backward(none.bfloat16(), None, none.int(), src, drows)
+    assert bool((drows[kept] == 7.0).all())
+    drows[kept] = 0.0
+    assert not bool(drows.view(torch.int16).any())
+    del src, drows
+    torch.cuda.empty_cache()
