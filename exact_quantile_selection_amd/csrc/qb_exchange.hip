@@ -13,7 +13,8 @@
 // pair its rank among its wave's pairs without atomics.  Up to 8192 pairs one
 // workgroup does everything in one launch; above, one launch counts blocks of
 // pairs and a second ranks them, each workgroup adding up the counts of the
-// blocks before its own (from L2; no scan launch between).
+// blocks before its own (from L2); only where those are many does a launch
+// between add them up once for all.
 //
 // combine:           out_t   = sum_k gate_tk rows[pos_tk]
 // combine backward:  dgate_tk = <dout_t, rows[pos_tk]>,  drows[pos_tk] = gate_tk dout_t,
@@ -49,10 +50,14 @@ static int64_t dispatch_blocks(int64_t pairs) {
   return std::max<int64_t>(1, (pairs + b - 1) / b);
 }
 static int table_row(int E) { return (E + 3) / 4 * 4; }
+// Above this many blocks a launch between turns the counts into sums (8 of 256
+// experts each: 2^18 tokens, 256 blocks, 28 us either way; 2^20 tokens 102 us
+// without it and 68 with it, 2^24 11.1 ms and 1.04).
+constexpr int64_t kDispScan = 256;
 
 int64_t dispatch_ws_bytes(int64_t pairs, int E) {
   const int64_t n = dispatch_blocks(pairs);
-  return n <= 1 ? 0 : n * table_row(E) * 4;
+  return n <= 1 ? 0 : (n + (n > kDispScan)) * table_row(E) * 4;
 }
 
 __global__ __launch_bounds__(kDispThreads) void k_dispatch_count(const int32_t* __restrict__ topk, int64_t pairs,
@@ -72,9 +77,47 @@ __global__ __launch_bounds__(kDispThreads) void k_dispatch_count(const int32_t* 
   if (tid < ER) table[int64_t(blockIdx.x) * ER + tid] = cnt[tid];
 }
 
+// The table's counts become those of the blocks before each; a last row has
+// all blocks'.  A workgroup takes 4 experts, a thread a run of blocks.
+__global__ __launch_bounds__(kDispThreads) void k_dispatch_scan(int32_t* __restrict__ table, int n, int ER) {
+  __shared__ int part[kDispWaves][4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int each = (n + kDispThreads - 1) / kDispThreads;
+  const int j0 = tid * each < n ? tid * each : n, j1 = j0 + each < n ? j0 + each : n;
+  int32_t* const col = table + 4 * blockIdx.x;
+  int sum[4] = {0, 0, 0, 0}, run[4];
+  for (int j = j0; j < j1; ++j) {
+    const int4 v = *reinterpret_cast<const int4*>(col + int64_t(j) * ER);
+    sum[0] += v.x, sum[1] += v.y, sum[2] += v.z, sum[3] += v.w;
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    run[c] = sum[c];
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+      const int o = __shfl_up(run[c], d);
+      run[c] += lane >= d ? o : 0;
+    }
+    if (lane == kWave - 1) part[wave][c] = run[c];
+    run[c] -= sum[c];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    for (int w = 0; w < wave; ++w) run[c] += part[w][c];
+  for (int j = j0; j < j1; ++j) {
+    int4* const at = reinterpret_cast<int4*>(col + int64_t(j) * ER);
+    const int4 v = *at;
+    *at = make_int4(run[0], run[1], run[2], run[3]);
+    run[0] += v.x, run[1] += v.y, run[2] += v.z, run[3] += v.w;
+  }
+  if (tid == kDispThreads - 1)
+    *reinterpret_cast<int4*>(col + int64_t(n) * ER) = make_int4(run[0], run[1], run[2], run[3]);
+}
+
 __global__ __launch_bounds__(kDispThreads) void k_dispatch(const int32_t* __restrict__ topk, int64_t pairs,
                                                            int64_t per, int K, int E, int ER, int align,
-                                                           const int32_t* __restrict__ table,
+                                                           const int32_t* __restrict__ table, bool scanned,
                                                            int32_t* __restrict__ off, int64_t R,
                                                            int32_t* __restrict__ row_src,
                                                            int32_t* __restrict__ pos) {
@@ -122,7 +165,12 @@ __global__ __launch_bounds__(kDispThreads) void k_dispatch(const int32_t* __rest
     }
   }
   // the counts of the blocks before this one, and of all
-  if (nblk > 1) {
+  if (scanned) {
+    if (tid < ER) {
+      before[tid] = table[int64_t(blk) * ER + tid];
+      total[tid] = table[int64_t(nblk) * ER + tid];
+    }
+  } else if (nblk > 1) {
     const int quads = ER / 4;              // 64 threads or fewer take one row of the table, 4 experts each
     const int qd = tid & 63, slice = tid >> 6;
     if (qd < quads) {
@@ -209,13 +257,18 @@ int launch_dispatch(const Dispatch& a, hipStream_t st) {
   if (n > 1) {
     hipLaunchKernelGGL(k_dispatch_count, dim3(unsigned(n)), dim3(kDispThreads), 0, st, a.topk, a.pairs, per, a.E, ER,
                        a.ws);
-    const int rc = int(hipGetLastError());
+    int rc = int(hipGetLastError());
     if (rc != int(hipSuccess)) return rc;
+    if (n > kDispScan) {
+      hipLaunchKernelGGL(k_dispatch_scan, dim3(unsigned(ER / 4)), dim3(kDispThreads), 0, st, a.ws, int(n), ER);
+      rc = int(hipGetLastError());
+      if (rc != int(hipSuccess)) return rc;
+    }
   }
   // one workgroup takes only as many steps as its pairs need
   const int64_t mine = n > 1 ? per : std::max<int64_t>(1, (a.pairs + kDispThreads - 1) / kDispThreads) * kDispThreads;
   hipLaunchKernelGGL(k_dispatch, dim3(unsigned(n)), dim3(kDispThreads), 0, st, a.topk, a.pairs, mine, a.K, a.E, ER,
-                     a.align, a.ws, a.off, a.R, a.row_src, a.pos);
+                     a.align, a.ws, n > kDispScan, a.off, a.R, a.row_src, a.pos);
   return int(hipGetLastError());
 }
 

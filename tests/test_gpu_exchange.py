@@ -250,3 +250,14 @@ def test_the_most_empty_rows():
     assert not bool(drows.view(torch.int16).any())
     del src, drows
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("N,K,E,align", [(300001, 8, 250, 16), (2100001, 1, 3, 1)])
+def test_order_of_more_blocks_than_one_adds_up(N, K, E, align):
+    rng = np.random.default_rng(N)
+    topk = rng.integers(-1, E + 1, (N, K)).astype(np.int32)
+    off, src, pos, R = dispatch(topk, E, align, extra=5)
+    ro, rs, rp = order(topk, E, align, R)
+    G.assert_same("off", G.host(off), ro)
+    G.assert_same("row_src", G.host(src), rs)
+    G.assert_same("pos", G.host(pos), rp)
