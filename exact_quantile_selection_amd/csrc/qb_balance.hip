@@ -183,6 +183,11 @@ int balance_chunk_rows(int64_t N) { return N <= 32768 ? 32 : 128; }
 // Threads of the second kernel: 16 for each of up to 64 experts.
 constexpr int kBalFinWays = 16;
 constexpr int kBalFinCols = 64;
+// Its workgroups at most, one a CU: each counts the sequences and arrives at
+// one word (8192 sequences of 16 tokens, 256 experts: the forward takes 344
+// us, 354 with 512, 372 with 1024, 953 with one for each 64 experts of a
+// sequence; 131,072 of one token 5.1 and 105 ms).
+constexpr int kBalFinMost = 256;
 static int bal_fin_cols(int E) { return E < kBalFinCols ? E : kBalFinCols; }
 
 BalWs balance_ws_layout(int64_t N, int E, int B) {
@@ -190,7 +195,7 @@ BalWs balance_ws_layout(int64_t N, int E, int B) {
   w.T = balance_chunk_rows(N);
   w.chunks = (N + w.T - 1) / w.T;
   w.slots = w.chunks + B;
-  w.groups = int64_t(B) * (E / bal_fin_cols(E));
+  w.groups = std::min<int64_t>(int64_t(B) * (E / bal_fin_cols(E)), kBalFinMost);
   w.part = 16;  // the arrival counter comes first
   w.psum = w.part + (w.groups * 8 + 15) / 16 * 16;
   w.cnt = w.psum + w.slots * E * 4;
@@ -484,7 +489,8 @@ __global__ __launch_bounds__(kBalThreads, P <= 9 ? 4 : 3) void k_balance_fwd(
 
 // ---------------------------------------------------------------------------
 // The sums of each sequence's slots, its weights and its share of the loss:
-// one workgroup for up to 64 experts of one sequence, 16 threads an expert.
+// one workgroup for up to 64 experts of one sequence at a time, 16 threads an
+// expert.
 // Every workgroup counts the sequences that have a live token itself (a scan
 // of a few live words); the last one to arrive adds the shares of the loss in
 // a fixed order.  All of it is waiting (each load is of memory that another
@@ -515,66 +521,76 @@ __global__ __launch_bounds__(kBalFinWays* kBalFinCols) void k_balance_fin(
   const int threads = int(blockDim.x), cols = threads / kBalFinWays;
   const int tid = threadIdx.x, col = tid % cols, way = tid / cols;
   const int eg = E / cols;
-  const int q = int(blockIdx.x) / eg, e = (int(blockIdx.x) % eg) * cols + col;
   if (tid == 0) {
     sh_filled = 0;
     sh_tok = 0;
   }
-  int64_t s0, s1, a0 = 0, a1 = 0;
-  bal_slots(seq_off, N, T, q, s0, s1);
+  int64_t a0 = 0, a1 = 0;
   if (tid < B) bal_slots(seq_off, N, T, tid, a0, a1);
-  // eight slots a thread, the sequence's live words and another's first one are on their way at once
-  bool any = a0 < a1 && live[a0] != 0;
-  double p = 0.0;
-  int c = 0, tok = 0;
-  for (int64_t t = s0; t < s1; t += 8 * kBalFinWays) {
-    float pv[8];
-    int cv[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int64_t at = t + u * kBalFinWays + way, from = at < s1 ? at : s1 - 1;
-      pv[u] = psum[from * E + e];
-      cv[u] = cnt[from * E + e];
-    }
-    const int64_t mine = t + tid;
-    if (tid < 8 * kBalFinWays && mine < s1) tok += live[mine];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const bool on = t + u * kBalFinWays + way < s1;
-      p += on ? double(pv[u]) : 0.0;
-      c += on ? cv[u] : 0;
-    }
-  }
-  sh_p[tid] = p;
-  sh_c[tid] = c;
-  __syncthreads();
-  if (tok) atomicAdd(&sh_tok, tok);
-  int filled = 0;
-  for (int j = tid; j < B;) {
-    for (++a0; a0 < a1 && !any; ++a0) any = live[a0] != 0;
-    filled += any ? 1 : 0;
-    j += threads;
-    if (j < B) {
-      bal_slots(seq_off, N, T, j, a0, a1);
-      any = a0 < a1 && live[a0] != 0;
-    }
-  }
-  if (filled) atomicAdd(&sh_filled, filled);
-  __syncthreads();
   double share = 0.0;
-  if (tid < cols) {
+  for (int g = int(blockIdx.x);;) {
+    const int q = g / eg, e = (g % eg) * cols + col;
+    int64_t s0, s1;
+    bal_slots(seq_off, N, T, q, s0, s1);
+    // eight slots a thread, the sequence's live words and another's first one are on their way at once
+    const bool first = g == int(blockIdx.x);
+    bool any = first && a0 < a1 && live[a0] != 0;
+    double p = 0.0;
+    int c = 0, tok = 0;
+    for (int64_t t = s0; t < s1; t += 8 * kBalFinWays) {
+      float pv[8];
+      int cv[8];
 #pragma unroll
-    for (int w = 1; w < kBalFinWays; ++w) {
-      p += sh_p[w * cols + col];
-      c += sh_c[w * cols + col];
+      for (int u = 0; u < 8; ++u) {
+        const int64_t at = t + u * kBalFinWays + way, from = at < s1 ? at : s1 - 1;
+        pv[u] = psum[from * E + e];
+        cv[u] = cnt[from * E + e];
+      }
+      const int64_t mine = t + tid;
+      if (tid < 8 * kBalFinWays && mine < s1) tok += live[mine];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const bool on = t + u * kBalFinWays + way < s1;
+        p += on ? double(pv[u]) : 0.0;
+        c += on ? cv[u] : 0;
+      }
     }
-    const double toks = double(sh_tok);
-    const double per = sh_tok > 0 ? 1.0 / toks : 0.0;
-    const double scale = double(coef) / double(sh_filled > 0 ? sh_filled : 1);
-    const double f = double(c) * per * (double(E) / double(K));
-    if (count) count[int64_t(q) * E + e] = c;
-    if (weight) weight[int64_t(q) * E + e] = float(scale * (f - 1.0) * per);
-    share = scale * f * p * per;
+    sh_p[tid] = p;
+    sh_c[tid] = c;
+    __syncthreads();
+    if (tok) atomicAdd(&sh_tok, tok);
+    if (first) {
+      int filled = 0;
+      for (int j = tid; j < B;) {
+        for (++a0; a0 < a1 && !any; ++a0) any = live[a0] != 0;
+        filled += any ? 1 : 0;
+        j += threads;
+        if (j < B) {
+          bal_slots(seq_off, N, T, j, a0, a1);
+          any = a0 < a1 && live[a0] != 0;
+        }
+      }
+      if (filled) atomicAdd(&sh_filled, filled);
+    }
+    __syncthreads();
+    if (tid < cols) {
+#pragma unroll
+      for (int w = 1; w < kBalFinWays; ++w) {
+        p += sh_p[w * cols + col];
+        c += sh_c[w * cols + col];
+      }
+      const double toks = double(sh_tok);
+      const double per = sh_tok > 0 ? 1.0 / toks : 0.0;
+      const double scale = double(coef) / double(sh_filled > 0 ? sh_filled : 1);
+      const double f = double(c) * per * (double(E) / double(K));
+      if (count) count[int64_t(q) * E + e] = c;
+      if (weight) weight[int64_t(q) * E + e] = float(scale * (f - 1.0) * per);
+      share += scale * f * p * per;
+    }
+    g += int(gridDim.x);
+    if (g >= B * eg) break;
+    __syncthreads();
+    if (tid == 0) sh_tok = 0;
   }
   if (!loss) return;
   if (tid < kWave) {
