@@ -27,21 +27,24 @@
 // than 2^-13 below it is dropped; groups, and the running sum, are added in 32
 // bits.  All 8-bit matrix instructions of this GPU do so, the 16-bit ones do
 // not.  So there are two ways to multiply, with the same tiles:
-//   * the 8-bit instruction: up to 2^-10 of sum |a b|, unseen beside a bf16
-//     result's own 2^-8 unless the sum cancels.  The product's default.
 //   * EXACT: both operands widened in registers to bf16 (e4m3 times its
 //     scale is exact there), whose instruction adds products in full: every
-//     sum in 32 bits, half the peak rate.  The weight gradient, whose result
-//     keeps 32 bits, and the products of few rows, where the weight's bytes
-//     cost more than either instruction, always use it.
+//     sum in 32 bits, half the peak rate.  What a call does unless told
+//     otherwise; the weight gradient, whose result keeps 32 bits, and the
+//     products of few rows, where the weight's bytes cost more than either
+//     instruction, know no other way.
+//   * the 8-bit instruction, where the caller allows it: up to 2^-10 of sum
+//     |a b| is lost, unseen beside a bf16 result's own 2^-8 unless the sum
+//     cancels (256 and -256 among each eight products, the others 2^-9: not
+//     one bit of a result is right).
 // Large products are bound by the matrix units as the loop feeds them: 8192 x
-// 8192 x 4096 takes 226 to 250 us (2.2 to 2.4 PFLOP/s; the vendor library's
-// plain e4m3 product 227), its weight gradient 385 to 430 (1.3 to 1.4; the
-// vendor's bf16 product 433).  What the first spends its 229 us on, by
-// leaving work out: without the loads 216, without seven eighths of the LDS
-// reads of A too 200, with a quarter of the products 165: the products, at the
-// clock that the card holds under them, and the operands' way overlap to
-// within 15%.
+// 8192 x 4096 takes 402 to 434 us (1.3 to 1.4 PFLOP/s; the vendor library's
+// bf16 product 433), as its weight gradient does, and 219 to 255 with the 8-bit
+// instruction (2.2 to 2.5; the vendor's plain e4m3 product 227).  What the
+// last spends 229 us on, by leaving work out: without the loads 216, without
+// seven eighths of the LDS reads of A too 200, with a quarter of the products
+// 165: the products, at the clock that the card holds under them, and the
+// operands' way overlap to within 15%.
 #include <algorithm>
 #include <type_traits>
 
@@ -1067,11 +1070,13 @@ static int gemm_tiled(const Gemm& g, hipStream_t st) {
 }
 
 // Which tiles: 64 x 64 while two workgroups a CU take them all at once (768 x
-// 2048 x 1024: 7.7 us, 128 x 128 tiles 9.5; 2048 x 2048 x 2048: 19.4 and 16.5).
-// Above that 128 x 128, two at a time on a CU, or 256 x 256, which read half
-// the operands' bytes per product and cost 3.3 small ones' time where two
-// small ones at a time cost 2 (8192 x 8192 x 4096: 226 us, 271), whichever has
-// the cheaper number of rounds over the CUs.  `uneven`: the part of a round
+// 2048 x 1024: 10.0 us, 128 x 128 tiles 12.9; 2048 x 2048 x 2048: 29.6 and
+// 24.8).  Above that 128 x 128, two at a time on a CU, or 256 x 256, which read
+// half the operands' bytes per product and cost 3.3 small ones' time where two
+// small ones at a time cost 2 (8192 x 8192 x 4096: 412 us, 459; 4096 x 4096 x
+// 4096: 110 and 123), whichever has the cheaper number of rounds over the CUs.
+// The 8-bit instruction has the same order at each of these sizes (7.4 and
+// 9.2; 19.0 and 17.0; 229 and 278; 60 and 72).  `uneven`: the part of a round
 // that large tiles lose where experts of unequal length leave some CUs waiting.
 template <bool GRAD, bool EXACT>
 static int gemm(const Gemm& g, int64_t t256, int64_t t128, int64_t t64, double uneven, hipStream_t st) {
@@ -1096,8 +1101,8 @@ static int gemm_thin(const Gemm& g, hipStream_t st) {
 // workgroup, and two where a wave's part is then still four blocks long (one
 // token through 4096 x 4096: 20.5, 11.6, 7.4, 5.2 us with 1, 2, 4, 8; 128 rows
 // over 256 experts of 1024 x 2048: 47, 44, 50, 90, since each workgroup of
-// eight has so little of the weight that finding its tile counts; tiles take
-// 34).
+// eight has so little of the weight that finding its tile counts; 64 x 64
+// tiles take 45, 34 with the 8-bit instruction).
 template <int MT>
 static int gemm_few(const Gemm& g, hipStream_t st) {
   const int64_t waves = row_tiles(g, 16 * MT) * ((g.N + 15) / 16);
@@ -1117,8 +1122,8 @@ int launch_fp8_product(const uint8_t* xq, const uint8_t* xs, const uint8_t* w, c
   const int64_t rows = off ? (M + G - 1) / G : M;  // rows of an expert, on average
   auto tiles = [&](int b) { return row_tiles(g, b) * ((N + b - 1) / b); };
   const int64_t cu = device_cu_count();
-  // few rows and no tile for every CU: 16 columns of the weight a wave (32 rows, 4096 x 4096: 10.4 us, tiles 11.4; one
-  // row 5.3 and 11.2; 64 rows 16.7 and 11.5)
+  // few rows and no tile for every CU: 16 columns of the weight a wave (32 rows, 4096 x 4096: 10.4 us, tiles 17.5, with
+  // the 8-bit instruction 11.3; 16 rows 7.5, 17.4 and 11.2; 64 rows 17.6, 17.5 and 11.4)
   if (rows <= 32 && tiles(64) <= cu) return rows <= 16 ? gemm_few<1>(g, st) : gemm_few<2>(g, st);
   // an expert of up to 128 rows fills no more than half of a 256 x 256 tile, and one of up to 16 a quarter of a 64 x
   // 64 one; of the tiles that experts' rows make at most, some are not there

@@ -21,11 +21,13 @@ from . import qb
 
 class ExpertLayer:
     """Router weight wr bf16 [E, H] (E of 32 to 256, as qb_router_scores takes), expert matrices w float [E, M, H] (held in
-    8 bits, in both orders), bias b float [E]; buffers for N tokens a call."""
+    8 bits, in both orders), bias b float [E]; buffers for N tokens a call.  The experts' products hold their sums in 32
+    bits; exact=False lets them use the faster instruction that drops some (see qb_fp8_product)."""
 
-    def __init__(self, wr: torch.Tensor, w: torch.Tensor, K: int, N: int, coef: float = 0.0, B: int = 1):
+    def __init__(self, wr: torch.Tensor, w: torch.Tensor, K: int, N: int, coef: float = 0.0, B: int = 1,
+                 exact: bool = True):
         E, M, H = w.shape
-        self.wr, self.K, self.N, self.coef = wr, K, N, coef
+        self.wr, self.K, self.N, self.coef, self.exact = wr, K, N, coef, exact
         kw = dict(device=w.device)
 
         def new(shape, dtype):
@@ -76,7 +78,7 @@ class ExpertLayer:
         qb.qb_dispatch(self.topk, self.b.numel(), qb.FP8_BLOCK, self.off, self.row_src, self.pos, self.dispatch_ws,
                        stream=stream)
         qb.qb_fp8_quantize(h, self.xq, self.xs, row_src=self.row_src, stream=stream)
-        qb.qb_fp8_product(self.xq, self.xs, self.wq, self.ws, self.rows, off=self.off, stream=stream)
+        qb.qb_fp8_product(self.xq, self.xs, self.wq, self.ws, self.rows, off=self.off, exact=self.exact, stream=stream)
         qb.qb_combine(self.rows, self.pos, self.out, gate=self.gate, stream=stream)
         return self.out
 
@@ -87,7 +89,8 @@ class ExpertLayer:
         qb.qb_combine_backward(dout, self.rows, self.pos, self.row_src, self.drows, gate=self.gate, dgate=self.dgate,
                                stream=stream)
         qb.qb_fp8_quantize(self.drows, self.dq, self.ds, stream=stream)
-        qb.qb_fp8_product(self.dq, self.ds, self.wt, self.wts, self.dx_rows, off=self.off, stream=stream)
+        qb.qb_fp8_product(self.dq, self.ds, self.wt, self.wts, self.dx_rows, off=self.off, exact=self.exact,
+                          stream=stream)
         qb.qb_combine(self.dx_rows, self.pos, self.dx, stream=stream)
         qb.qb_fp8_quantize_cols(self.h, self.xt, self.xts, row_src=self.row_src, stream=stream)
         qb.qb_fp8_quantize_cols(self.drows, self.dt, self.dts, stream=stream)

@@ -565,11 +565,12 @@ def qb_fp8_quantize_weight(w, wq, ws, wt=None, wts=None, stream=None):
     _check(_calls().quantize_weight(w, wq, ws, wt, wts, stream))
 
 
-def qb_fp8_product(xq, xs, w, w_scale, y, off=None, exact=False, stream=None):
+def qb_fp8_product(xq, xs, w, w_scale, y, off=None, exact=True, stream=None):
     """y bf16 [M, N] = xq times w [N, ld] transposed; with off int32 [G + 1]
-    rows off[e] .. off[e + 1] - 1 take w[e] of w [G, N, ld].  exact: sums in
-    32 bits throughout, at half the matrix rate (else the 8-bit instruction's,
-    which drops the parts of products 2^13 below the largest of eight)."""
+    rows off[e] .. off[e + 1] - 1 take w[e] of w [G, N, ld].  Sums are held in
+    32 bits throughout.  exact=False allows the 8-bit instruction's, up to
+    twice the matrix rate, which drop the parts of products 2^13 below the
+    largest of eight: a caller's choice, for sums that do not cancel."""
     _check(_calls().product(xq, xs, w, w_scale, y, off, exact, stream))
 
 

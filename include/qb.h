@@ -557,10 +557,12 @@ QB_API int qb_combine_backward(const uint16_t* dout, const uint16_t* rows, int64
  *
  * qb_fp8_product: y[m][n] = sum_c x[m][c] w[n][c], y bf16 [M][N], with C the
  * summed dimension.  exact = 1: every sum in 32 bits, rounded once.  exact =
- * 0: the 8-bit matrix instruction, nearly twice as fast on large products; of
- * each eight products it drops what lies more than 2^13 below the largest, so
- * up to 2^-10 sum |x w| is lost (some 2^-15 on ordinary data), and adds the
- * rest in 32 bits.  With off (int32 [G +
+ * 0 allows the 8-bit matrix instruction, nearly twice as fast on large
+ * products; of each eight products it drops what lies more than 2^13 below the
+ * largest, so up to 2^-10 sum |x w| is lost (some 2^-15 on ordinary data; a sum
+ * that cancels may lose all of its bits), and adds the rest in 32 bits.  It is
+ * used where it is faster, which depends on the call's shape: the same row may
+ * then give other bits beside another number of rows.  With off (int32 [G +
  * 1], not decreasing, within [0, M]) row m in off[e] .. off[e + 1] - 1 takes
  * w[e]; rows outside every expert are not written.  The gradient of x is the
  * same call on dy and the transposed weight.
