@@ -732,6 +732,33 @@ QB_API int qb_balance_backward(const float* s, const int32_t* topk, int64_t N, i
   return hip_status(qbk::launch_balance_bwd(a, stream), fn);
 }
 
+static int check_unrouted(const char* fn, const int32_t* topk, int64_t N, int E, int K) {
+  if (N < 1 || N > INT32_MAX) return fail(QB_EINVAL, "%s: N=%lld, expected 1 <= N < 2^31", fn, (long long)N);
+  if (!qbk::supported_E(E)) return fail(QB_EUNSUPPORTED, "%s: E=%d, expected E in {16, 32, 64, 128, 256}", fn, E);
+  if (K < 1 || K >= E) return fail(QB_EINVAL, "%s: K=%d, expected 1 <= K < E=%d", fn, K, E);
+  if (!topk) return fail(QB_EINVAL, "%s: topk is NULL (expected int32 [N=%lld][K=%d])", fn, (long long)N, K);
+  return check_elem_align(fn, {topk});
+}
+
+QB_API int qb_unrouted_clear(float* s, const int32_t* topk, int64_t N, int E, int K, qb_stream_t stream) {
+  const char* fn = "qb_unrouted_clear";
+  if (int rc = check_unrouted(fn, topk, N, E, K)) return rc;
+  if (int rc = check_pass(fn, s, 1, N, E)) return rc;
+  return hip_status(qbk::launch_unrouted_clear(topk, N, K, E, s, stream), fn);
+}
+
+QB_API int qb_unrouted_uncount(const int32_t* topk, int64_t N, int E, int K, float* alpha, int32_t* hist_hi,
+                               qb_stream_t stream) {
+  const char* fn = "qb_unrouted_uncount";
+  if (int rc = check_unrouted(fn, topk, N, E, K)) return rc;
+  if (!alpha || !hist_hi)
+    return fail(QB_EINVAL, "%s: alpha (float [N=%lld]) and hist_hi (int32 [E=%d][256]) are required", fn, (long long)N,
+                E);
+  if (!aligned8(hist_hi)) return fail(QB_EINVAL, "%s: hist_hi must be 8-byte aligned", fn);
+  if (int rc = check_elem_align(fn, {alpha})) return rc;
+  return hip_status(qbk::launch_unrouted_uncount(topk, N, K, E, alpha, hist_hi, stream), fn);
+}
+
 static int check_dispatch(const char* fn, int64_t N, int K, int E, int align) {
   if (N < 0 || K < 1 || N > int64_t(INT32_MAX) / K)
     return fail(QB_EINVAL, "%s: N=%lld, K=%d; expected N >= 0, K >= 1 and N K < 2^31", fn, (long long)N, K);

@@ -826,4 +826,69 @@ int launch_balance_bwd(const BalBwd& a, hipStream_t st) {
   return int(hipErrorInvalidValue);
 }
 
+// ---------------------------------------------------------------------------
+// The bias update of a batch with padding.  Its first pass counts every row's
+// margins in a histogram, whose totals give the rank, and its second reads
+// that pass's alpha.  So rows that were routed nowhere leave it in two steps:
+// their scores, which may be anything, become zeros before the first pass,
+// which makes their margins all one value (the (K+1)-th largest bias); that
+// many counts are taken out of its bin again, and their alpha becomes infinity,
+// whose key lies above every finite margin's.  Two launches that read one word
+// of topk a row: an update of 131,072 x 256, a tenth of it padding, takes 80 us
+// with them and 73 over all rows.
+
+constexpr int kUnrThreads = 256;
+
+__device__ __forceinline__ bool unrouted(const int32_t* topk, int64_t row, int64_t N, int K, int E) {
+  return row < N && unsigned(topk[row * K]) >= unsigned(E);
+}
+
+__global__ __launch_bounds__(kUnrThreads) void k_unrouted_clear(const int32_t* __restrict__ topk, int64_t N, int K,
+                                                                int E, float* __restrict__ s) {
+  const int lane = threadIdx.x & 63;
+  const int64_t r0 = int64_t(blockIdx.x) * kUnrThreads + (threadIdx.x - lane);
+  uint64_t m = __ballot(unrouted(topk, r0 + lane, N, K, E));
+  while (m) {
+    float* row = s + (r0 + __builtin_ctzll(m)) * E;
+    m &= m - 1;
+    for (int c = 4 * lane; c < E; c += 4 * kWave) *reinterpret_cast<f32x4*>(row + c) = (f32x4){0.f, 0.f, 0.f, 0.f};
+  }
+}
+
+__global__ __launch_bounds__(kUnrThreads) void k_unrouted_uncount(const int32_t* __restrict__ topk, int64_t N, int K,
+                                                                  int E, float* __restrict__ alpha,
+                                                                  int32_t* __restrict__ hist_hi) {
+  __shared__ int n;
+  __shared__ float a;
+  const int tid = threadIdx.x;
+  if (tid == 0) n = 0;
+  __syncthreads();
+  int mine = 0;
+  for (int64_t row = int64_t(blockIdx.x) * kUnrThreads + tid; row < N; row += int64_t(gridDim.x) * kUnrThreads)
+    if (unrouted(topk, row, N, K, E)) {
+      a = alpha[row];  // the same value for all of them
+      alpha[row] = __builtin_inff();
+      ++mine;
+    }
+  if (mine) atomicAdd(&n, mine);
+  __syncthreads();
+  if (n == 0) return;
+  const uint32_t key = key2(bf16x2_rne(a, a)) & 0xFFFFu;
+  for (int e = tid; e < E; e += kUnrThreads) atomicSub(hist_hi + e * 256 + (key >> 8), n);
+}
+
+int launch_unrouted_clear(const int32_t* topk, int64_t N, int K, int E, float* s, hipStream_t st) {
+  hipLaunchKernelGGL(k_unrouted_clear, dim3(unsigned((N + kUnrThreads - 1) / kUnrThreads)), dim3(kUnrThreads), 0, st,
+                     topk, N, K, E, s);
+  return int(hipGetLastError());
+}
+
+int launch_unrouted_uncount(const int32_t* topk, int64_t N, int K, int E, float* alpha, int32_t* hist_hi,
+                            hipStream_t st) {
+  const int64_t most = device_cu_count();  // each subtracts its rows from every expert's bin
+  hipLaunchKernelGGL(k_unrouted_uncount, dim3(unsigned(std::min((N + kUnrThreads - 1) / kUnrThreads, most))),
+                     dim3(kUnrThreads), 0, st, topk, N, K, E, alpha, hist_hi);
+  return int(hipGetLastError());
+}
+
 }  // namespace qbk

@@ -162,6 +162,9 @@ struct BalBwd {
 };
 int launch_balance_fwd(const BalFwd& a, hipStream_t st);
 int launch_balance_bwd(const BalBwd& a, hipStream_t st);
+int launch_unrouted_clear(const int32_t* topk, int64_t N, int K, int E, float* s, hipStream_t st);
+int launch_unrouted_uncount(const int32_t* topk, int64_t N, int K, int E, float* alpha, int32_t* hist_hi,
+                            hipStream_t st);
 
 // The exchange between tokens and experts.
 struct Dispatch {

@@ -8,7 +8,7 @@ output is the gate-weighted sum of what its experts' matrices make of it:
     out = sum_k g_k (h w[e_k]^T)
 
 ``step`` of the bias (``update_bias``) is the exact quantile update of the
-batch's own scores; ``backward`` gives the gradients of sum(out * dout) +
+live tokens' own scores; ``backward`` gives the gradients of sum(out * dout) +
 dloss * loss, with the loss of sequence-wise balance.  Every step below is a
 libqb call; this module only owns buffers and orders the calls.
 """
@@ -100,6 +100,8 @@ class ExpertLayer:
         return self.dx, self.dw, self.dlogits
 
     def update_bias(self, stream=None):
-        """The exact quantile update of b from the last forward's scores."""
+        """The exact quantile update of b from the scores of the last forward's
+        live tokens (with seq_off or valid, the others' rows of s are cleared)."""
+        masked = any(t is not None for t in self.seqs.values())
         self.eqb.reset(stream)
-        qb.eqb_update(self.s, self.b, self.K, self.alpha, self.eqb, stream=stream)
+        qb.eqb_update(self.s, self.b, self.K, self.alpha, self.eqb, stream=stream, topk=self.topk if masked else None)

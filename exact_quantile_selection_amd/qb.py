@@ -79,6 +79,8 @@ def lib() -> C.CDLL:
         sig |= {
             "qb_balance_forward": [vp, vp, i64, i32, i32, vp, i32, vp, f32, vp, vp, vp, vp, vp, vp, i64, vp],
             "qb_balance_backward": [vp, vp, i64, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp],
+            "qb_unrouted_clear": [vp, vp, i64, i32, i32, vp],
+            "qb_unrouted_uncount": [vp, i64, i32, i32, vp, vp, vp],
             "qb_dispatch": [vp, i64, i32, i32, i32, vp, i64, vp, vp, vp, i64, vp],
             "qb_combine": [vp, i64, vp, vp, i64, i32, i32, vp, vp],
             "qb_combine_backward": [vp, vp, i64, vp, vp, vp, i64, i32, i32, vp, vp, vp],
@@ -520,6 +522,28 @@ def qb_balance_backward(s, topk, weight=None, dloss=None, dgate=None, dlogits=No
     _check(_calls().balance_backward(s, topk, weight, dloss, dgate, dlogits, seq_off, valid, stream))
 
 
+def qb_unrouted_clear(s, topk, stream=None):
+    """s[i] = 0 for the rows that topk [N, K] routes nowhere (topk[i][0]
+    outside [0, E)), before qb_margins_topk and qb_unrouted_uncount."""
+    if s.dim() != 2 or topk.dim() != 2:
+        raise ValueError("s must be [N, E] and topk [N, K]")
+    N, E = s.shape
+    K = topk.shape[1]
+    _check(lib().qb_unrouted_clear(_ptr(s, torch.float32, "s"), _ptr(topk, torch.int32, "topk", (N, K)), N, E, K,
+                                   _stream(stream)))
+
+
+def qb_unrouted_uncount(topk, alpha, hist_hi, stream=None):
+    """Takes those rows out of qb_margins_topk's alpha [N] and hist_hi [E, 256]."""
+    if topk.dim() != 2 or hist_hi.dim() != 2:
+        raise ValueError("topk must be [N, K] and hist_hi [E, 256]")
+    N, K = topk.shape
+    E = hist_hi.shape[0]
+    _check(lib().qb_unrouted_uncount(_ptr(topk, torch.int32, "topk"), N, E, K,
+                                     _ptr(alpha, torch.float32, "alpha", (N,)),
+                                     _ptr(hist_hi, torch.int32, "hist_hi", (E, 256)), _stream(stream)))
+
+
 def qb_dispatch_rows(N, K, E, align=1):
     return _bytes(lib().qb_dispatch_rows(N, K, E, align))
 
@@ -609,12 +633,20 @@ class EqbBuffers:
         qb_fill_i32(self.block, 0, stream)
 
 
-def eqb_update(s, b, K, alpha, buf: EqbBuffers, load=None, stream=None):
+def eqb_update(s, b, K, alpha, buf: EqbBuffers, load=None, stream=None, topk=None):
     """One exact quantile-balancing update: pass 1 (alpha + high-byte
     histogram), high-byte select, pass 2 (low-byte histogram), low-byte select
     and the in-place bias update.  Histograms must be zero on entry
-    (buf.reset() clears them in place)."""
+    (buf.reset() clears them in place).  With topk [N, K] (one layer, no
+    load) the update is of the rows that it routes: the others' scores are
+    cleared and alpha is infinity for them."""
+    if topk is not None:
+        if load is not None:
+            raise ValueError("load counts every row: it goes without topk")
+        qb_unrouted_clear(s, topk, stream=stream)
     qb_margins_topk(s, b, K, alpha, load=load, hist_hi=buf.hist_hi, stream=stream)
+    if topk is not None:
+        qb_unrouted_uncount(topk, alpha, buf.hist_hi, stream=stream)
     qb_select_update(QB_SELECT_HI, K, buf.hist_hi, sel_hi=buf.sel_hi, rank_lo=buf.rank_lo,
                      err=buf.err, stream=stream)
     qb_radix_hist_lo(s, alpha, buf.sel_hi, buf.hist_lo, stream=stream)

@@ -499,6 +499,24 @@ QB_API int qb_balance_backward(const float* s, const int32_t* topk, int64_t N, i
                                const float* dgate, float* dlogits, qb_stream_t stream);
 
 /*
+ * The bias update of a batch in which some rows were routed nowhere (topk[i][0]
+ * outside [0, E): qb_balance_forward's padding and tokens of no sequence), as
+ * if those rows were not there:
+ *   qb_unrouted_clear(s, topk)      their scores, which may be anything, become 0
+ *   qb_margins_topk(s, b, alpha, hist_hi)            no loads: it counts all rows
+ *   qb_unrouted_uncount(topk, alpha, hist_hi)        their counts leave hist_hi,
+ *                                   and alpha[i] becomes +infinity for them, whose
+ *                                   key lies above every finite margin's
+ *   qb_select_update(HI), then the low-byte pass and its select as without them.
+ * With no routed row the selects report QB_ERR_EMPTY and leave the bias.
+ *   s float [N][E], 16-byte aligned; topk int32 [N][K], K < E; alpha float [N];
+ *   hist_hi int32 [E][256], 8-byte aligned.
+ */
+QB_API int qb_unrouted_clear(float* s, const int32_t* topk, int64_t N, int E, int K, qb_stream_t stream);
+QB_API int qb_unrouted_uncount(const int32_t* topk, int64_t N, int E, int K, float* alpha, int32_t* hist_hi,
+                               qb_stream_t stream);
+
+/*
  * qb_dispatch: the order that puts each expert's rows side by side.  Pair i =
  * t K + k goes to expert e = topk[i] (outside [0, E): nowhere).
  *   off[e]  int32 [E + 1]: expert e's first row; off[0] = 0 and each expert
