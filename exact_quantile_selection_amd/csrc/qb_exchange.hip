@@ -206,7 +206,8 @@ __global__ __launch_bounds__(kDispThreads) void k_dispatch(const int32_t* __rest
     for (int j = 0; j < 4; ++j) {
       const int t = total[4 * lane + j];
       used[4 * lane + j] = t;
-      c[j] = (t + align - 1) / align * align;
+      // (t + align - 1 may pass 2^31 though the rows do not)
+      c[j] = int((unsigned(t) + unsigned(align) - 1u) / unsigned(align) * unsigned(align));
       sum += c[j];
     }
     int run = sum;
