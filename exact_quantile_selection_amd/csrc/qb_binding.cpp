@@ -12,6 +12,7 @@
 #include <initializer_list>
 #include <string>
 #include <tuple>
+#include <type_traits>
 
 #include "../../include/qb.h"
 
@@ -69,9 +70,14 @@ void check_shape(const at::Tensor& t, const char* name, std::initializer_list<in
     throw Bad{std::string(name) + " has shape " + shape_name(t.sizes()) + ", expected " + shape_name(want)};
 }
 
+// An input's address, for T const, or an output's, which gets a storage of
+// its own where it shares another tensor's until it is written.
 template <class T>
 T* address(const at::Tensor& t) {
-  return static_cast<T*>(const_cast<void*>(t.const_data_ptr()));
+  if constexpr (std::is_const_v<T>)
+    return static_cast<T*>(t.const_data_ptr());
+  else
+    return static_cast<T*>(t.mutable_data_ptr());
 }
 // The address of a tensor of this shape, nullptr for None (or a refusal).
 template <class T>
@@ -126,10 +132,10 @@ struct Seqs {
   const uint8_t* valid;
 };
 Seqs sequences(PyObject* off, PyObject* valid, int64_t N) {
-  Seqs s{nullptr, 1, opt<uint8_t>(valid, ScalarType::Byte, "valid", {N})};
+  Seqs s{nullptr, 1, opt<const uint8_t>(valid, ScalarType::Byte, "valid", {N})};
   if (off != Py_None) {
     const at::Tensor& t = tensor(off, ScalarType::Int, "seq_off", 1);
-    s.off = address<int32_t>(t);
+    s.off = address<const int32_t>(t);
     s.B = narrow(t.numel() - 1, "seq_off");
   }
   return s;
@@ -164,8 +170,8 @@ int balance_forward(PyObject* const* a) {
   if (coef == -1.0 && PyErr_Occurred()) throw Raised{};
   return std::apply(
       lib.qb_balance_forward,
-      std::tuple{address<float>(s), req<float>(a[1], F32, "b", {E}), N, narrow(E, "s"), int(K), q.off, q.B, q.valid,
-                 float(coef), req<int32_t>(a[3], I32, "topk", {N, K}), opt<float>(a[4], F32, "gate", {N, K}),
+      std::tuple{address<const float>(s), req<const float>(a[1], F32, "b", {E}), N, narrow(E, "s"), int(K), q.off, q.B,
+                 q.valid, float(coef), req<int32_t>(a[3], I32, "topk", {N, K}), opt<float>(a[4], F32, "gate", {N, K}),
                  opt<int32_t>(a[5], I32, "count", {q.B, E}), opt<float>(a[6], F32, "weight", {q.B, E}),
                  opt<float>(a[7], F32, "loss", {1}), ws.p, ws.n, stream_of(a[12])});
 }
@@ -180,9 +186,10 @@ int balance_backward(PyObject* const* a) {
   const Seqs q = sequences(a[6], a[7], N);
   return std::apply(
       lib.qb_balance_backward,
-      std::tuple{address<float>(s), address<int32_t>(topk), N, narrow(E, "s"), narrow(K, "topk"), q.off, q.B, q.valid,
-                 opt<float>(a[2], F32, "weight", {q.B, E}), opt<float>(a[3], F32, "dloss", {1}),
-                 opt<float>(a[4], F32, "dgate", {N, K}), req<float>(a[5], F32, "dlogits", {N, E}), stream_of(a[8])});
+      std::tuple{address<const float>(s), address<const int32_t>(topk), N, narrow(E, "s"), narrow(K, "topk"), q.off,
+                 q.B, q.valid, opt<const float>(a[2], F32, "weight", {q.B, E}),
+                 opt<const float>(a[3], F32, "dloss", {1}), opt<const float>(a[4], F32, "dgate", {N, K}),
+                 req<float>(a[5], F32, "dlogits", {N, E}), stream_of(a[8])});
 }
 
 // topk, E, align, off, row_src, pos, ws, stream
@@ -193,7 +200,7 @@ int dispatch(PyObject* const* a) {
   const Workspace ws = workspace(a[6]);
   return std::apply(
       lib.qb_dispatch,
-      std::tuple{address<int32_t>(topk), N, narrow(K, "topk"), int(E), int(align),
+      std::tuple{address<const int32_t>(topk), N, narrow(K, "topk"), int(E), int(align),
                  req<int32_t>(a[3], I32, "off", {E + 1}), src.numel(), address<int32_t>(src),
                  req<int32_t>(a[5], I32, "pos", {N, K}), ws.p, ws.n, stream_of(a[7])});
 }
@@ -205,8 +212,9 @@ int combine(PyObject* const* a) {
   const int64_t N = pos.size(0), K = pos.size(1), H = rows.size(1);
   return std::apply(
       lib.qb_combine,
-      std::tuple{address<uint16_t>(rows), rows.size(0), address<int32_t>(pos), opt<float>(a[3], F32, "gate", {N, K}),
-                 N, narrow(K, "pos"), narrow(H, "rows"), req<uint16_t>(a[2], BF16, "out", {N, H}), stream_of(a[4])});
+      std::tuple{address<const uint16_t>(rows), rows.size(0), address<const int32_t>(pos),
+                 opt<const float>(a[3], F32, "gate", {N, K}), N, narrow(K, "pos"), narrow(H, "rows"),
+                 req<uint16_t>(a[2], BF16, "out", {N, H}), stream_of(a[4])});
 }
 
 // dout, rows, pos, row_src, drows, gate, dgate, stream
@@ -216,9 +224,9 @@ int combine_backward(PyObject* const* a) {
   const int64_t R = drows.size(0), H = drows.size(1), N = pos.size(0), K = pos.size(1);
   return std::apply(
       lib.qb_combine_backward,
-      std::tuple{req<uint16_t>(a[0], BF16, "dout", {N, H}), opt<uint16_t>(a[1], BF16, "rows", {R, H}), R,
-                 address<int32_t>(pos), req<int32_t>(a[3], I32, "row_src", {R}),
-                 opt<float>(a[5], F32, "gate", {N, K}), N, narrow(K, "pos"), narrow(H, "drows"),
+      std::tuple{req<const uint16_t>(a[0], BF16, "dout", {N, H}), opt<const uint16_t>(a[1], BF16, "rows", {R, H}), R,
+                 address<const int32_t>(pos), req<const int32_t>(a[3], I32, "row_src", {R}),
+                 opt<const float>(a[5], F32, "gate", {N, K}), N, narrow(K, "pos"), narrow(H, "drows"),
                  address<uint16_t>(drows), opt<float>(a[6], F32, "dgate", {N, K}), stream_of(a[7])});
 }
 
@@ -230,7 +238,7 @@ int quantize(PyObject* const* a) {
   if (src) check_shape(*src, "row_src", {M});
   return std::apply(
       lib.qb_fp8_quantize,
-      std::tuple{address<uint16_t>(x), x.size(0), src ? address<int32_t>(*src) : nullptr, M, narrow(C, "x"),
+      std::tuple{address<const uint16_t>(x), x.size(0), src ? address<const int32_t>(*src) : nullptr, M, narrow(C, "x"),
                  req<uint8_t>(a[1], F8, "xq", {M, ld(C)}), req<uint8_t>(a[2], U8, "xs", {M, sld(C)}),
                  stream_of(a[4])});
 }
@@ -241,7 +249,7 @@ int quantize_cols(PyObject* const* a) {
   if (src) check_shape(*src, "row_src", {M});
   return std::apply(
       lib.qb_fp8_quantize_cols,
-      std::tuple{address<uint16_t>(x), x.size(0), src ? address<int32_t>(*src) : nullptr, M, narrow(C, "x"),
+      std::tuple{address<const uint16_t>(x), x.size(0), src ? address<const int32_t>(*src) : nullptr, M, narrow(C, "x"),
                  req<uint8_t>(a[1], F8, "xt", {C, ld(M)}), req<uint8_t>(a[2], U8, "xts", {C, sld(M)}),
                  stream_of(a[4])});
 }
@@ -263,7 +271,7 @@ int quantize_weight(PyObject* const* a) {
   uint8_t* wts = a[4] == Py_None ? nullptr : stack<uint8_t>(a[4], U8, "wts", st, G, ld(C) / 128, sld(N));
   return std::apply(
       lib.qb_fp8_quantize_weight,
-      std::tuple{address<float>(*w), narrow(G, "w"), narrow(N, "w"), narrow(C, "w"),
+      std::tuple{address<const float>(*w), narrow(G, "w"), narrow(N, "w"), narrow(C, "w"),
                  stack<uint8_t>(a[1], F8, "wq", st, G, N, ld(C)),
                  stack<uint8_t>(a[2], U8, "ws", st, G, ld(N) / 128, sld(C)), wt, wts, stream_of(a[5])});
 }
@@ -276,7 +284,7 @@ struct Offsets {
 Offsets offsets(PyObject* o) {
   if (o == Py_None) return {nullptr, 1};
   const at::Tensor& t = tensor(o, I32, "off", 1);
-  return {address<int32_t>(t), narrow(t.numel() - 1, "off")};
+  return {address<const int32_t>(t), narrow(t.numel() - 1, "off")};
 }
 
 // xq, xs, w, w_scale, y, off, exact, stream
@@ -291,9 +299,9 @@ int product(PyObject* const* a) {
   if (exact < 0) throw Raised{};
   return std::apply(
       lib.qb_fp8_product,
-      std::tuple{address<uint8_t>(xq), req<uint8_t>(a[1], U8, "xs", {M, sld(l)}),
-                 stack<uint8_t>(a[2], F8, "w", st, g.G, N, l),
-                 stack<uint8_t>(a[3], U8, "w_scale", st, g.G, ld(N) / 128, sld(l)), M, narrow(N, "w"),
+      std::tuple{address<const uint8_t>(xq), req<const uint8_t>(a[1], U8, "xs", {M, sld(l)}),
+                 stack<const uint8_t>(a[2], F8, "w", st, g.G, N, l),
+                 stack<const uint8_t>(a[3], U8, "w_scale", st, g.G, ld(N) / 128, sld(l)), M, narrow(N, "w"),
                  narrow(l, "xq"), g.off, g.G, exact, req<uint16_t>(a[4], BF16, "y", {M, N}), stream_of(a[7])});
 }
 
@@ -306,8 +314,9 @@ int weight_grad(PyObject* const* a) {
   check_shape(xt, "xt", {C, l});
   return std::apply(
       lib.qb_fp8_weight_grad,
-      std::tuple{address<uint8_t>(dyt), req<uint8_t>(a[1], U8, "dyts", {N, sld(l)}), address<uint8_t>(xt),
-                 req<uint8_t>(a[3], U8, "xts", {C, sld(l)}), l, narrow(N, "dyt"), narrow(C, "xt"), g.off, g.G,
+      std::tuple{address<const uint8_t>(dyt), req<const uint8_t>(a[1], U8, "dyts", {N, sld(l)}),
+                 address<const uint8_t>(xt), req<const uint8_t>(a[3], U8, "xts", {C, sld(l)}), l, narrow(N, "dyt"),
+                 narrow(C, "xt"), g.off, g.G,
                  stack<float>(a[4], F32, "dw", g.off != nullptr, g.G, N, C), stream_of(a[6])});
 }
 
