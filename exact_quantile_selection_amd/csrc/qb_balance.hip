@@ -272,7 +272,7 @@ __global__ __launch_bounds__(kBalThreads, P <= 9 ? 4 : 3) void k_balance_fwd(
   const int r0 = int(blockIdx.x) * T;
   const int r1 = N - r0 < T ? N : r0 + T;
   for (int j = tid; j < E; j += kBalThreads) {
-    lds_b[j] = b[j];
+    lds_b[j] = fminf(fmaxf(b[j], -kBalMost), kBalMost);  // an infinite sum, with an expert in its low bits, is no number
     if constexpr (STATS) lds_cnt[j] = 0;
   }
   if constexpr (STATS)

@@ -474,6 +474,9 @@ QB_API int qb_lei_grad(float* g, const int32_t* load, int64_t N, int E, int K, f
  *   count (int32 [B][E]), weight (float [B][E]; 16-byte aligned), loss (float
  *   [1]): each nullable; with any of them ws (16-byte aligned, at least
  *   qb_balance_workspace_bytes; its contents do not matter) is required.
+ *   A bias of -infinity bars an expert, as the lowest finite value does (an
+ *   infinite bias counts as the largest finite one of its sign): it is chosen
+ *   only where fewer than K others are left, by lower index.
  *   Scores of tokens that are not live may be anything; other NaN or Inf
  *   inputs and offsets out of order give unspecified, memory-safe results.
  */
