@@ -15,6 +15,7 @@ libqb call; this module only owns buffers and orders the calls.
 from __future__ import annotations
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import qb
 
@@ -22,7 +23,11 @@ from . import qb
 class ExpertLayer:
     """Router weight wr bf16 [E, H] (E of 32 to 256, as qb_router_scores takes), expert matrices w float [E, M, H] (held in
     8 bits, in both orders), bias b float [E]; buffers for N tokens a call.  The experts' products hold their sums in 32
-    bits; exact=False lets them use the faster instruction that drops some (see qb_fp8_product)."""
+    bits; exact=False lets them use the faster instruction that drops some (see qb_fp8_product).
+
+    Results are the layer's own buffers, which its next call writes again.  One forward at a time is followed by its
+    backward, which reads that forward's h, seq_off and valid again: they are not copied, and one that torch or a layer
+    has written since is an error."""
 
     def __init__(self, wr: torch.Tensor, w: torch.Tensor, K: int, N: int, coef: float = 0.0, B: int = 1,
                  exact: bool = True):
@@ -61,6 +66,7 @@ class ExpertLayer:
         self.out, self.dx = new((N, M), torch.bfloat16), new((N, H), torch.bfloat16)
         self.dw, self.dlogits = new((E, M, H), torch.float32), new((N, E), torch.float32)
         self.alpha = new((N,), torch.float32)
+        self.h, self.seqs, self.versions = None, {}, {}
         self.eqb = qb.EqbBuffers(1, E, device=w.device, lead=False)
 
     def load_weights(self, w: torch.Tensor, stream=None):
@@ -71,21 +77,32 @@ class ExpertLayer:
         """out bf16 [N, M] of hidden states h bf16 [N, H]; `loss` and `count`
         afterwards hold the balance loss and the per-expert counts of the
         sequences.  Padding (valid 0) goes to no expert, and its out is 0."""
-        self.h, self.seqs = h, dict(seq_off=seq_off, valid=valid)
+        self.h, seqs = None, dict(seq_off=seq_off, valid=valid)
         qb.qb_router_scores(h, self.wr, self.s, stream=stream)
         qb.qb_balance_forward(self.s, self.b, self.K, self.topk, gate=self.gate, count=self.count, weight=self.weight,
-                              loss=self.loss, ws=self.balance_ws, coef=self.coef, **self.seqs, stream=stream)
+                              loss=self.loss, ws=self.balance_ws, coef=self.coef, **seqs, stream=stream)
         qb.qb_dispatch(self.topk, self.b.numel(), qb.FP8_BLOCK, self.off, self.row_src, self.pos, self.dispatch_ws,
                        stream=stream)
         qb.qb_fp8_quantize(h, self.xq, self.xs, row_src=self.row_src, stream=stream)
         qb.qb_fp8_product(self.xq, self.xs, self.wq, self.ws, self.rows, off=self.off, exact=self.exact, stream=stream)
         qb.qb_combine(self.rows, self.pos, self.out, gate=self.gate, stream=stream)
+        increment_version(self.out)
+        self.h, self.seqs = h, seqs
+        self.versions = {n: t._version for n, t in dict(h=h, **seqs).items() if t is not None and not t.is_inference()}
         return self.out
+
+    def _forward_done(self):
+        if self.h is None:
+            raise RuntimeError("there was no forward")
 
     def backward(self, dout: torch.Tensor, dloss=None, stream=None):
         """Gradients of the last forward: dx bf16 [N, H] through the experts, dw
         float [E, M, H] and dlogits float [N, E] of the router's logits (whose
         own product with wr is the caller's)."""
+        self._forward_done()
+        for name, version in self.versions.items():
+            if dict(h=self.h, **self.seqs)[name]._version != version:
+                raise RuntimeError(f"{name} was written after the forward, and backward reads it again")
         qb.qb_combine_backward(dout, self.rows, self.pos, self.row_src, self.drows, gate=self.gate, dgate=self.dgate,
                                stream=stream)
         qb.qb_fp8_quantize(self.drows, self.dq, self.ds, stream=stream)
@@ -97,11 +114,13 @@ class ExpertLayer:
         qb.qb_fp8_weight_grad(self.dt, self.dts, self.xt, self.xts, self.dw, off=self.off, stream=stream)
         qb.qb_balance_backward(self.s, self.topk, weight=self.weight, dloss=dloss, dgate=self.dgate,
                                dlogits=self.dlogits, **self.seqs, stream=stream)
+        increment_version((self.dx, self.dw, self.dlogits))
         return self.dx, self.dw, self.dlogits
 
     def update_bias(self, stream=None):
         """The exact quantile update of b from the scores of the last forward's
         live tokens (with seq_off or valid, the others' rows of s are cleared)."""
+        self._forward_done()
         masked = any(t is not None for t in self.seqs.values())
         self.eqb.reset(stream)
         qb.eqb_update(self.s, self.b, self.K, self.alpha, self.eqb, stream=stream, topk=self.topk if masked else None)
