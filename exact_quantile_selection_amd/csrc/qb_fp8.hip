@@ -277,8 +277,12 @@ __global__ __launch_bounds__(256) void k_fp8_quantize_cols(const uint16_t* __res
 // An input of half the last cache (256 MiB) or more, which the results push
 // out of it, passes it by (135,000 rows of 2048: along the rows 169 -> 145 us,
 // along the columns 177 -> 157; 8192 of 8192: 53 -> 50 and 50 -> 47; 8192 of
-// 4096: 25 -> 23 but 23 -> 25).
-static bool past_caches(int64_t rows, int C) { return rows * C * 2 >= (int64_t(128) << 20); }
+// 4096: 25 -> 23 but 23 -> 25).  Unless its rows are read again: taken by
+// row_src for 2 experts each and more, the caches serve them better at every
+// size (past them -> through them: 16,384 rows of 2048 for 8 experts each 140 ->
+// 117 and 163 -> 138; 32,768 for 8 355 -> 234 and 352 -> 298; 131,072 for 2 391
+// -> 304 and 361 -> 335; but 262,144 of 1024 for one 132 -> 161, 164 -> 185).
+static bool past_caches(int64_t Mx, int64_t M, int C) { return M < 2 * Mx && Mx * C * 2 >= (int64_t(128) << 20); }
 
 int launch_fp8_quantize(const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M, int C, uint8_t* xq,
                         uint8_t* xs, hipStream_t st) {
@@ -286,7 +290,7 @@ int launch_fp8_quantize(const uint16_t* x, int64_t Mx, const int32_t* row_src, i
   // four rows a wave once that still gives every CU its waves
   const bool four = M * chunks >= 16 * 1024;
   const dim3 grid{unsigned(four ? (M + 15) / 16 : (M + 3) / 4), chunks, 1u};
-  if (four && past_caches(M, C))
+  if (four && past_caches(Mx, M, C))
     hipLaunchKernelGGL((k_fp8_quantize<4, true>), grid, dim3(256), 0, st, x, Mx, row_src, M, C, xq, xs);
   else if (four)
     hipLaunchKernelGGL((k_fp8_quantize<4, false>), grid, dim3(256), 0, st, x, Mx, row_src, M, C, xq, xs);
@@ -299,7 +303,7 @@ int launch_fp8_quantize_cols(const uint16_t* x, int64_t Mx, const int32_t* row_s
                              uint8_t* xts, hipStream_t st) {
   const int64_t ld = fp8_ld(M);
   const dim3 grid{unsigned((C + 63) / 64), unsigned(ld / kQBlock), 1u};
-  if (past_caches(M, C))
+  if (past_caches(Mx, M, C))
     hipLaunchKernelGGL(k_fp8_quantize_cols<true>, grid, dim3(256), 0, st, x, Mx, row_src, M, C, ld, fp8_sld(M), xt, xts);
   else
     hipLaunchKernelGGL(k_fp8_quantize_cols<false>, grid, dim3(256), 0, st, x, Mx, row_src, M, C, ld, fp8_sld(M), xt,
