@@ -18,9 +18,10 @@
 //   dlogit = ds s (1 - s).
 //
 // Both passes read the scores once from HBM.  131,072 x 256 with K = 6: the
-// forward takes 32.7 us (4.1 TB/s), bound by its vector instructions (86% of
-// the issue slots; the K largest cost 7 of them a score), the sums 8.7 us, bound
-// by waiting, the gradient 47 us (5.7 TB/s), bound by HBM.  The K largest are
+// forward takes 32.7 us (4.1 TB/s), bound by its vector instructions (745 for 8
+// rows, 81% of the busy CUs' issue slots; the K largest cost 7 of them a score),
+// the sums 9.0 us, bound by waiting, the gradient 43.8 us (6.1 TB/s), bound by
+// HBM.  The K largest are
 // kept as biased scores whose low bits are the expert's number: a list's entry
 // is then one register, insertion one median, and no second look for the
 // chosen ones is needed (with a mask of them: 41 us); rows where the K-th and
@@ -31,7 +32,8 @@
 // end of a sequence's stretch of rows reduces them across lanes.  A workgroup
 // takes a chunk of T consecutive rows and leaves one partial row (E counts,
 // E sums) for every sequence that meets its chunk, at slot chunk + sequence
-// (both only grow along the rows, so no two stretches share a slot).  A
+// (both only grow along the rows, so no two stretches share a slot), summed
+// over at most 128 rows in 32 bits, a quarter or an eighth of them to a lane.  A
 // second kernel adds each sequence's slots in order in 64 bits: the same
 // result on every run, no atomics on floating-point numbers.
 #include <algorithm>

@@ -37,13 +37,13 @@
 //     |a b| is lost, unseen beside a bf16 result's own 2^-8 unless the sum
 //     cancels (256 and -256 among each eight products, the others 2^-9: not
 //     one bit of a result is right).
-// Large products are bound by the matrix units as the loop feeds them: 8192 x
-// 8192 x 4096 takes 402 to 434 us (1.3 to 1.4 PFLOP/s; the vendor library's
-// bf16 product 433), as its weight gradient does, and 219 to 255 with the 8-bit
-// instruction (2.2 to 2.5; the vendor's plain e4m3 product 227).  What the
-// last spends 229 us on, by leaving work out: without the loads 216, without
-// seven eighths of the LDS reads of A too 200, with a quarter of the products
-// 165: the products, at the clock that the card holds under them, and the
+// Large products are bound by the matrix units as the loop feeds them, at the
+// clock that the card holds under them: 8192 x 8192 x 4096 takes 412 to 448 us
+// (1.2 to 1.3 PFLOP/s; the vendor library's bf16 product 433), its weight
+// gradient 405 to 431, and with the 8-bit instruction 231 to 272 (2.0 to 2.4;
+// the vendor's plain e4m3 product 227).  What the last spent 229 us on, by
+// leaving work out: without the loads 216, without seven eighths of the LDS
+// reads of A too 200, with a quarter of the products 165: the products and the
 // operands' way overlap to within 15%.
 #include <algorithm>
 #include <type_traits>
@@ -131,7 +131,8 @@ __device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t p) {
 
 // Along the rows: a wave takes 512 columns (one word of four scales) of U
 // rows, 16 lanes a block.  Bound by its 2 bytes in, 1 byte out a value:
-// 135,000 x 2048 take 145 us, 5.7 TB/s (a copy reaches 5.1 in cached accesses).
+// 135,000 x 2048 take 146 us, 5.7 TB/s (a copy reaches 5.1 in cached accesses).
+// Taken by row_src from 16,384 rows, 139,000 of them take 102.
 template <int U, bool NT>
 __global__ __launch_bounds__(256) void k_fp8_quantize(const uint16_t* __restrict__ x, int64_t Mx,
                                                       const int32_t* __restrict__ row_src, int64_t M, int C,
@@ -198,8 +199,8 @@ __device__ __forceinline__ uint32_t swapped(uint32_t a) {
 // writes them transposed, 128 contiguous bytes a column.  A thread holds 8
 // columns of 4 consecutive rows, so that a column's 4 bytes are one word; the
 // words cross to the columns' order through LDS (33 words a column: the 64
-// lanes of a store lie in 64 banks).  Bound like the one along the rows: 157 us
-// for the same matrix.
+// lanes of a store lie in 64 banks).  Bound like the one along the rows: 156 us
+// for the same matrix, 125 gathered.
 template <bool NT>
 __global__ __launch_bounds__(256) void k_fp8_quantize_cols(const uint16_t* __restrict__ x, int64_t Mx,
                                                            const int32_t* __restrict__ row_src, int64_t M, int C,
@@ -312,9 +313,11 @@ int launch_fp8_quantize_cols(const uint16_t* x, int64_t Mx, const int32_t* row_s
 }
 
 // A weight stack: a workgroup takes one 128 x 128 block of one matrix, in both
-// orders.  A thread holds 4 rows of 16 columns; both layouts leave through the
+// orders.  A thread holds 16 rows of 4 columns; both layouts leave through the
 // same LDS bytes (rows of 132, so that the reads of a column spread over the
-// banks).
+// banks).  64 matrices of 1024 x 2048 take 203 us (805 MB, 4.0 TB/s): the 4-byte
+// loads of a row that may have any alignment, and the transpose's reads of
+// single bytes, stand between it and HBM.
 __global__ __launch_bounds__(256) void k_fp8_quantize_weight(const float* __restrict__ w, int N, int C,
                                                              uint8_t* __restrict__ wq, uint8_t* __restrict__ ws,
                                                              uint8_t* __restrict__ wt, uint8_t* __restrict__ wts) {

@@ -126,8 +126,9 @@ int launch_lei(float* g, const int32_t* load, int64_t N, int E, int K, float eta
 bool supported_E(int E);
 
 // Routing with a balance loss.  Workspace: an arrival counter, one float64
-// share of the loss for every 16 experts of every sequence, then for each
-// slot (chunk of T rows + sequence) E sums, E counts and the live tokens.
+// share of the loss for each workgroup of the sums (`groups` of them: one for
+// up to 64 experts of every sequence, 256 at most), then for each slot (chunk
+// of T rows + sequence) E sums, E counts and the live tokens.
 // Every word that is read was written by the same call.
 struct BalWs {
   int T;                                        // rows per chunk

@@ -464,8 +464,8 @@ QB_API int qb_lei_grad(float* g, const int32_t* load, int64_t N, int E, int K, f
  *   loss      = coef / n sum_q sum_e f[q][e] (1 / T) sum_{i live in q} p[i][e],
  *               n = sequences with a live token (0 if there is none)
  *   weight[q][e] = coef (f[q][e] - 1) / (n T), what qb_balance_backward needs
- * Sums over tokens are added in a fixed order in 64 bits: the same result on
- * every run.
+ * Sums over tokens are added in a fixed order, in 32 bits within 128 rows at
+ * most and in 64 beyond: the same result on every run.
  *   s float [N][E] (16-byte aligned), b float [E]; E in {16, 32, 64, 128,
  *   256}, 1 <= K <= 15, K < E, 1 <= N <= 2^30, 1 <= B <= 2^20.
  *   seq_off nullable int32 [B + 1], not decreasing, within [0, N]; without it
@@ -530,7 +530,7 @@ QB_API int qb_unrouted_uncount(const int32_t* topk, int64_t N, int E, int K, flo
  * R is at least qb_dispatch_rows(N, K, E, align), the rows that any topk of
  * this shape fits in.  ws: at least qb_dispatch_workspace_bytes (0 up to 8192
  * pairs; ws may then be NULL), 16-byte aligned.  1 <= E <= 256, K >= 1, N >=
- * 0, align >= 1; N K and R below 2^31.
+ * 0, 1 <= align <= 2^20; N K and R below 2^31.
  */
 QB_API int64_t qb_dispatch_rows(int64_t N, int K, int E, int align);
 QB_API int64_t qb_dispatch_workspace_bytes(int64_t N, int K, int E);
@@ -542,7 +542,8 @@ QB_API int qb_dispatch(const int32_t* topk, int64_t N, int K, int E, int align, 
  * the order of k and rounded once.  rows and out bf16 bit patterns [R][H] and
  * [N][H]; pos int32 [N][K], a row outside [0, R) adds nothing; gate nullable
  * float [N][K] (1 without it: then this is also the backward of handing each
- * expert its copy of a token).  H >= 1, K >= 1, 0 <= N <= 2^24, R < 2^31.
+ * expert its copy of a token).  1 <= H <= 2^20, K >= 1, 0 <= N <= 2^24, N K
+ * and R below 2^31.
  * qb_combine_backward: dgate[t][k] = sum_h dout[t][h] rows[pos[t][k]][h] (0
  * where pos is outside [0, R)), drows[pos[t][k]] = gate[t][k] dout[t], and 0
  * in the rows with row_src < 0.  dgate nullable (rows is then not read and
