@@ -28,8 +28,8 @@
 // bits.  All 8-bit matrix instructions of this GPU do so, the 16-bit ones do
 // not.  So there are two ways to multiply, with the same tiles:
 //   * EXACT: both operands widened in registers to bf16 (e4m3 times its
-//     scale is exact there), whose instruction adds products in full: every
-//     sum in 32 bits, half the peak rate.  What a call does unless told
+//     scale is exact there from 2^-133 up and below 2^128), whose instruction
+//     adds products in full: every sum in 32 bits, half the peak rate.  What a call does unless told
 //     otherwise; the weight gradient, whose result keeps 32 bits, and the
 //     products of few rows, where the weight's bytes cost more than either
 //     instruction, know no other way.

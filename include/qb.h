@@ -578,7 +578,9 @@ QB_API int qb_combine_backward(const uint16_t* dout, const uint16_t* rows, int64
  * (wt and wts nullable, both or neither).
  *
  * qb_fp8_product: y[m][n] = sum_c x[m][c] w[n][c], y bf16 [M][N], with C the
- * summed dimension.  exact = 1: every sum in 32 bits, rounded once.  exact =
+ * summed dimension.  exact = 1: every sum in 32 bits, rounded once, of values
+ * within bf16's range (2^128, to which the last 1.6% below its end are
+ * quantised, is infinite, and a weight's part below 2^-133 is lost).  exact =
  * 0 allows the 8-bit matrix instruction, nearly twice as fast on large
  * products; of each eight products it drops what lies more than 2^13 below the
  * largest, so up to 2^-10 sum |x w| is lost (some 2^-15 on ordinary data; a sum
