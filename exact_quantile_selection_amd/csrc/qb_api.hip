@@ -925,6 +925,61 @@ QB_API int qb_fp8_weight_grad(const uint8_t* dyt, const uint8_t* dyts, const uin
                     fn);
 }
 
+// x's rows by number, or all of them in order
+static int check_rows(const char* fn, const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M, int C) {
+  if (Mx < 0 || Mx > kFp8Most || (!row_src && Mx != M))
+    return fail(QB_EINVAL, "%s: x has Mx=%lld rows; expected M=%lld, or row_src (int32 [M])", fn, (long long)Mx,
+                (long long)M);
+  if (M > 0 && Mx > 0 && !x)
+    return fail(QB_EINVAL, "%s: x (bf16 [Mx=%lld][C=%d]) is required", fn, (long long)Mx, C);
+  return QB_OK;
+}
+
+QB_API int qb_bf16_product(const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M, const uint16_t* w, int N,
+                           int C, const int32_t* off, int G, int transposed, uint16_t* y, qb_stream_t stream) {
+  const char* fn = "qb_bf16_product";
+  if (int rc = check_fp8(fn, M, N, C, G)) return rc;
+  if (!off && G != 1) return fail(QB_EINVAL, "%s: G=%d matrices need off (int32 [G + 1])", fn, G);
+  if (transposed != 0 && transposed != 1) return fail(QB_EINVAL, "%s: transposed=%d, expected 0 or 1", fn, transposed);
+  if (int rc = check_rows(fn, x, Mx, row_src, M, C)) return rc;
+  if (M == 0) return ok();
+  if (!w || !y)
+    return fail(QB_EINVAL, "%s: w (bf16 [G=%d][%d][%d]) and y (bf16 [M=%lld][N=%d]) are required", fn, G,
+                transposed ? C : N, transposed ? N : C, (long long)M, N);
+  if (!aligned_all(2, {x, w, y})) return fail(QB_EINVAL, "%s: bf16 arrays must be 2-byte aligned", fn);
+  if (int rc = check_elem_align(fn, {off, row_src})) return rc;
+  return hip_status(
+      qbk::launch_bf16_product(x, int(Mx), row_src, int(M), w, N, C, off, G, transposed != 0, y, stream), fn);
+}
+
+QB_API int64_t qb_bf16_weight_grad_workspace_bytes(int64_t M, int N, int C, int G) {
+  if (int rc = check_fp8("qb_bf16_weight_grad_workspace_bytes", M, N, C, G)) return rc;
+  const int splits = qbk::bf16_grad_splits(M, N, C, G);
+  return splits > 1 ? int64_t(4) * splits * G * N * C : 0;
+}
+
+QB_API int qb_bf16_weight_grad(const uint16_t* dy, const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M,
+                               int N, int C, const int32_t* off, int G, float* dw, void* ws, int64_t ws_bytes,
+                               qb_stream_t stream) {
+  const char* fn = "qb_bf16_weight_grad";
+  if (int rc = check_fp8(fn, M, N, C, G)) return rc;
+  if (!off && G != 1) return fail(QB_EINVAL, "%s: G=%d matrices need off (int32 [G + 1])", fn, G);
+  if (int rc = check_rows(fn, x, Mx, row_src, M, C)) return rc;
+  if (!dw || (M > 0 && !dy))
+    return fail(QB_EINVAL, "%s: dy (bf16 [M=%lld][N=%d]) and dw (float [G=%d][N][C=%d]) are required", fn, (long long)M, N,
+                G, C);
+  const int64_t need = qb_bf16_weight_grad_workspace_bytes(M, N, C, G);
+  if (ws && ws_bytes < need)
+    return fail(QB_EINVAL, "%s: ws_bytes=%lld, this shape needs %lld (qb_bf16_weight_grad_workspace_bytes)", fn,
+                (long long)ws_bytes, (long long)need);
+  if (!aligned16(ws)) return fail(QB_EINVAL, "%s: ws must be 16-byte aligned", fn);
+  if (!aligned_all(2, {dy, x})) return fail(QB_EINVAL, "%s: bf16 arrays must be 2-byte aligned", fn);
+  if (int rc = check_elem_align(fn, {off, row_src, dw})) return rc;
+  return hip_status(qbk::launch_bf16_weight_grad(dy, x, int(Mx), M > 0 ? row_src : nullptr, int(M), N, C,
+                                                 M > 0 ? off : nullptr, G, dw, static_cast<float*>(ws), stream),
+                    fn);
+}
+
 QB_API const char* qb_status_string(int status) {
   switch (status) {
     case QB_OK: return "QB_OK";

@@ -147,7 +147,8 @@ int64_t sld(int64_t n) { return (n + 511) / 512 * 4; }
 // The library's entry points, set by `connect`.
 #define QB_ENTRIES(X) \
   X(qb_balance_forward) X(qb_balance_backward) X(qb_dispatch) X(qb_combine) X(qb_combine_backward) \
-  X(qb_fp8_quantize) X(qb_fp8_quantize_cols) X(qb_fp8_quantize_weight) X(qb_fp8_product) X(qb_fp8_weight_grad)
+  X(qb_fp8_quantize) X(qb_fp8_quantize_cols) X(qb_fp8_quantize_weight) X(qb_fp8_product) X(qb_fp8_weight_grad) \
+  X(qb_bf16_product) X(qb_bf16_weight_grad)
 struct Library {
 #define X(f) decltype(&::f) f;
   QB_ENTRIES(X)
@@ -320,6 +321,53 @@ int weight_grad(PyObject* const* a) {
                  stack<float>(a[4], F32, "dw", g.off != nullptr, g.G, N, C), stream_of(a[6])});
 }
 
+// row_src int32 [M], or None: the rows as they are
+struct Rows {
+  const int32_t* src;
+  int64_t M;
+};
+Rows rows_of(PyObject* o, int64_t Mx) {
+  const at::Tensor* t = tensor_or_none(o, I32, "row_src");
+  if (!t) return {nullptr, Mx};
+  if (t->dim() != 1) throw Bad{"row_src has shape " + shape_name(t->sizes()) + ", expected 1 dimensions"};
+  return {address<const int32_t>(*t), t->numel()};
+}
+
+// x, w, y, off, row_src, transposed, stream
+int bf16_product(PyObject* const* a) {
+  const at::Tensor& x = tensor(a[0], BF16, "x", 2);
+  const Offsets g = offsets(a[3]);
+  const Rows rows = rows_of(a[4], x.size(0));
+  const int transposed = PyObject_IsTrue(a[5]);
+  if (transposed < 0) throw Raised{};
+  const bool st = g.off != nullptr;
+  const int64_t C = x.size(1);
+  const at::Tensor& w = tensor(a[1], BF16, "w", st ? 3 : 2);
+  const int64_t N = w.size(transposed ? -1 : -2);
+  return std::apply(
+      lib.qb_bf16_product,
+      std::tuple{address<const uint16_t>(x), x.size(0), rows.src, rows.M,
+                 stack<const uint16_t>(a[1], BF16, "w", st, g.G, transposed ? C : N, transposed ? N : C),
+                 narrow(N, "w"), narrow(C, "x"), g.off, g.G, transposed,
+                 req<uint16_t>(a[2], BF16, "y", {rows.M, N}), stream_of(a[6])});
+}
+
+// dy, x, dw, off, row_src, ws, stream
+int bf16_weight_grad(PyObject* const* a) {
+  const at::Tensor& dy = tensor(a[0], BF16, "dy", 2);
+  const at::Tensor& x = tensor(a[1], BF16, "x", 2);
+  const Offsets g = offsets(a[3]);
+  const Rows rows = rows_of(a[4], x.size(0));
+  const Workspace ws = workspace(a[5]);
+  const int64_t N = dy.size(1), C = x.size(1);
+  check_shape(dy, "dy", {rows.M, N});
+  return std::apply(
+      lib.qb_bf16_weight_grad,
+      std::tuple{address<const uint16_t>(dy), address<const uint16_t>(x), x.size(0), rows.src, rows.M, narrow(N, "dy"),
+                 narrow(C, "x"), g.off, g.G, stack<float>(a[2], F32, "dw", g.off != nullptr, g.G, N, C), ws.p, ws.n,
+                 stream_of(a[6])});
+}
+
 // No C++ exception leaves a call.
 template <int (*F)(PyObject* const*), int N>
 PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -367,6 +415,8 @@ PyMethodDef methods[] = {
     QB_CALL(quantize_weight, 6),
     QB_CALL(product, 8),
     QB_CALL(weight_grad, 7),
+    QB_CALL(bf16_product, 7),
+    QB_CALL(bf16_weight_grad, 7),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_qb_binding", "Calls of libqb's expert layer.", -1, methods,

@@ -199,4 +199,20 @@ int launch_fp8_product(const uint8_t* xq, const uint8_t* xs, const uint8_t* w, c
 int launch_fp8_weight_grad(const uint8_t* dyt, const uint8_t* dyts, const uint8_t* xt, const uint8_t* xts, int N,
                            int C, int64_t ldm, const int32_t* off, int G, float* dw, hipStream_t st);
 
+// bf16 products.  A gradient of few tiles is split along its rows, while each
+// part keeps 256 of them, into at most 512 parts of tiles of 128 x 128 in all
+// (32 MiB of partial sums).
+inline int bf16_grad_splits(int64_t M, int64_t N, int64_t C, int G) {
+  const int64_t tiles = G * ((N + 127) / 128) * ((C + 127) / 128);
+  int64_t s = tiles > 0 && tiles < 256 ? 512 / tiles : 1;
+  s = s < 16 ? s : 16;
+  const int64_t rows = M / G / 256;
+  s = s < rows ? s : rows;
+  return s > 1 ? int(s) : 1;
+}
+int launch_bf16_product(const uint16_t* x, int Mx, const int32_t* src, int M, const uint16_t* w, int N, int C,
+                        const int32_t* off, int G, bool transposed, uint16_t* y, hipStream_t st);
+int launch_bf16_weight_grad(const uint16_t* dy, const uint16_t* x, int Mx, const int32_t* src, int M, int N, int C,
+                            const int32_t* off, int G, float* dw, float* ws, hipStream_t st);
+
 }  // namespace qbk

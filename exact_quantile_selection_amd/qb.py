@@ -89,6 +89,8 @@ def lib() -> C.CDLL:
             "qb_fp8_quantize_weight": [vp, i32, i32, i32, vp, vp, vp, vp, vp],
             "qb_fp8_product": [vp, vp, vp, vp, i64, i32, i32, vp, i32, i32, vp, vp],
             "qb_fp8_weight_grad": [vp, vp, vp, vp, i64, i32, i32, vp, i32, vp, vp],
+            "qb_bf16_product": [vp, i64, vp, i64, vp, i32, i32, vp, i32, i32, vp, vp],
+            "qb_bf16_weight_grad": [vp, vp, i64, vp, i64, i32, i32, vp, i32, vp, vp, i64, vp],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -101,7 +103,9 @@ def lib() -> C.CDLL:
         L.qb_balance_workspace_bytes.argtypes = [i64, i32, i32]
         L.qb_dispatch_rows.argtypes = [i64, i32, i32, i32]
         L.qb_dispatch_workspace_bytes.argtypes = [i64, i32, i32]
-        for name in ("qb_balance_workspace_bytes", "qb_dispatch_rows", "qb_dispatch_workspace_bytes"):
+        L.qb_bf16_weight_grad_workspace_bytes.argtypes = [i64, i32, i32, i32]
+        for name in ("qb_balance_workspace_bytes", "qb_dispatch_rows", "qb_dispatch_workspace_bytes",
+                     "qb_bf16_weight_grad_workspace_bytes"):
             getattr(L, name).restype = C.c_int64
         L.qb_status_string.argtypes = [C.c_int]
         L.qb_status_string.restype = C.c_char_p
@@ -114,7 +118,7 @@ def lib() -> C.CDLL:
 # the expert layer's entry points, in the order in which the compiled binding takes their addresses
 _EXPERT_LAYER = ("qb_balance_forward", "qb_balance_backward", "qb_dispatch", "qb_combine", "qb_combine_backward",
                  "qb_fp8_quantize", "qb_fp8_quantize_cols", "qb_fp8_quantize_weight", "qb_fp8_product",
-                 "qb_fp8_weight_grad")
+                 "qb_fp8_weight_grad", "qb_bf16_product", "qb_bf16_weight_grad")
 
 
 def _calls():
@@ -602,6 +606,25 @@ def qb_fp8_weight_grad(dyt, dyts, xt, xts, dw, off=None, stream=None):
     """dw float [N, C] (or [G, N, C] with off, multiples of 128) = sum over
     the rows of dy times x, both quantised by qb_fp8_quantize_cols."""
     _check(_calls().weight_grad(dyt, dyts, xt, xts, dw, off, stream))
+
+
+def qb_bf16_product(x, w, y, off=None, row_src=None, transposed=False, stream=None):
+    """y bf16 [M, N] = x bf16 [Mx, C] times w [N, C] transposed (w [C, N] as it
+    is with transposed=True: the gradient of x from dy and the forward's w);
+    with off int32 [G + 1] rows off[e] .. off[e + 1] - 1 take w[e] of a stack.
+    row_src int32 [M]: row m of x is x[row_src[m]] (zeros where outside)."""
+    _check(_calls().bf16_product(x, w, y, off, row_src, transposed, stream))
+
+
+def qb_bf16_weight_grad_workspace_bytes(M, N, C, G=1):
+    return _bytes(lib().qb_bf16_weight_grad_workspace_bytes(M, N, C, G))
+
+
+def qb_bf16_weight_grad(dy, x, dw, off=None, row_src=None, ws=None, stream=None):
+    """dw float [N, C] (or [G, N, C] with off, any offsets) = sum over the rows
+    of dy bf16 [M, N] times x bf16, whose rows row_src numbers as for
+    qb_bf16_product; ws (uint8) lets few, long sums be added up in parts."""
+    _check(_calls().bf16_weight_grad(dy, x, dw, off, row_src, ws, stream))
 
 
 # ---------------------------------------------------------------------------

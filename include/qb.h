@@ -612,6 +612,38 @@ QB_API int qb_fp8_product(const uint8_t* xq, const uint8_t* xs, const uint8_t* w
 QB_API int qb_fp8_weight_grad(const uint8_t* dyt, const uint8_t* dyts, const uint8_t* xt, const uint8_t* xts,
                               int64_t M, int N, int C, const int32_t* off, int G, float* dw, qb_stream_t stream);
 
+/*
+ * The experts' products in bfloat16, sums in 32 bits, over ragged stretches of
+ * rows, for layers whose matrices are not held in fewer bits, and for the
+ * matrices' gradient of those that are.
+ *
+ * qb_bf16_product: y[m][n] = sum_c x[m][c] w[n][c], rounded once.  w bf16
+ * [G][N][C], or with transposed = 1 [G][C][N] (w[n][c] is then w[c][n]: the
+ * gradient of x is the same call on dy and the forward's own w).  y bf16
+ * [M][N].  off and G as for qb_fp8_product: rows outside every expert are not
+ * written.
+ * qb_bf16_weight_grad: dw[e][n][c] = sum over e's rows of dy[m][n] x[m][c], dw
+ * float [G][N][C], overwritten (0 for an expert without rows); off's entries
+ * may be any, and without off the sum runs over all M rows.  ws nullable: with
+ * at least qb_bf16_weight_grad_workspace_bytes (32 MiB at most; 16-byte
+ * aligned, its contents do not matter) a gradient of few, long sums is added
+ * up in parts, whose order is fixed; the parts change the rounding of 32 bits.
+ *
+ * row_src nullable int32 [M]: row m of x is x[row_src[m]], x bf16 [Mx][C];
+ * where row_src[m] is outside [0, Mx) it is zeros in the product, and the row
+ * adds nothing to the gradient, whatever dy holds there.  Without it M = Mx.
+ *
+ * bf16 arrays by their element aligned; calls whose rows are multiples of 16
+ * bytes and whose arrays are 16-byte aligned are the fastest.  0 <= M, Mx <=
+ * 2^22 rows; 1 <= N, C <= 2^22; 1 <= G <= 256.
+ */
+QB_API int qb_bf16_product(const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M, const uint16_t* w, int N,
+                           int C, const int32_t* off, int G, int transposed, uint16_t* y, qb_stream_t stream);
+QB_API int64_t qb_bf16_weight_grad_workspace_bytes(int64_t M, int N, int C, int G);
+QB_API int qb_bf16_weight_grad(const uint16_t* dy, const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M,
+                               int N, int C, const int32_t* off, int G, float* dw, void* ws, int64_t ws_bytes,
+                               qb_stream_t stream);
+
 /* Short name of a status code (static storage). */
 QB_API const char* qb_status_string(int status);
 
