@@ -980,6 +980,77 @@ QB_API int qb_bf16_weight_grad(const uint16_t* dy, const uint16_t* x, int64_t Mx
                     fn);
 }
 
+QB_API int qb_fp4_quantize(const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M, int C, uint8_t* xq,
+                           uint8_t* xs, qb_stream_t stream) {
+  const char* fn = "qb_fp4_quantize";
+  if (int rc = check_fp8(fn, M, 1, C, 1)) return rc;
+  if (int rc = check_rows(fn, x, Mx, row_src, M, C)) return rc;
+  if (M == 0) return ok();
+  if (!xq || !xs)
+    return fail(QB_EINVAL, "%s: xq and xs, the e2m1 matrix of M=%lld rows and its scales, are required", fn, (long long)M);
+  if (!aligned_all(2, {x})) return fail(QB_EINVAL, "%s: x must be 2-byte aligned", fn);
+  if (!aligned16(xq) || !aligned8(xs))
+    return fail(QB_EINVAL, "%s: e2m1 matrices must be 16-byte and scales 8-byte aligned", fn);
+  if (int rc = check_elem_align(fn, {row_src})) return rc;
+  return hip_status(qbk::launch_fp4_quantize(x, Mx, row_src, M, C, xq, xs, stream), fn);
+}
+
+QB_API int qb_fp4_quantize_weight(const float* w, int G, int N, int C, uint8_t* wq, uint8_t* ws, uint8_t* wt,
+                                  uint8_t* wts, qb_stream_t stream) {
+  const char* fn = "qb_fp4_quantize_weight";
+  if (int rc = check_fp8(fn, 0, N, C, G)) return rc;
+  if (!w || !wq || !ws || !wt != !wts)
+    return fail(QB_EINVAL,
+                "%s: w (float [G=%d][N=%d][C=%d]), wq and ws are required, and wt and wts both or neither", fn, G, N, C);
+  if (!aligned16(wq) || !aligned8(ws) || (wt && (!aligned16(wt) || !aligned8(wts))))
+    return fail(QB_EINVAL, "%s: e2m1 matrices must be 16-byte and scales 8-byte aligned", fn);
+  if (int rc = check_elem_align(fn, {w})) return rc;
+  return hip_status(qbk::launch_fp4_quantize_weight(w, G, N, C, wq, ws, wt, wts, stream), fn);
+}
+
+QB_API int qb_fp4_product(const uint8_t* xq, const uint8_t* xs, const uint8_t* w, const uint8_t* w_scale, int64_t M,
+                          int N, int C, const int32_t* off, int G, uint16_t* y, qb_stream_t stream) {
+  const char* fn = "qb_fp4_product";
+  if (int rc = check_fp8(fn, M, N, C, G)) return rc;
+  if (!off && G != 1) return fail(QB_EINVAL, "%s: G=%d matrices need off (int32 [G + 1])", fn, G);
+  if (M == 0) return ok();
+  if (!xq || !xs || !w || !w_scale || !y)
+    return fail(QB_EINVAL, "%s: xq, xs, w, w_scale and y (bf16 [M=%lld][N=%d]) are required", fn, (long long)M, N);
+  if (!aligned16(xq) || !aligned16(w) || !aligned8(xs) || !aligned8(w_scale))
+    return fail(QB_EINVAL, "%s: e2m1 matrices must be 16-byte and scales 8-byte aligned", fn);
+  if (!aligned_all(2, {y})) return fail(QB_EINVAL, "%s: y must be 2-byte aligned", fn);
+  if (int rc = check_elem_align(fn, {off})) return rc;
+  return hip_status(qbk::launch_fp4_product(xq, xs, w, w_scale, int(M), N, C, off, G, y, stream), fn);
+}
+
+static int check_orthogonalize(const char* fn, int G, int N, int C) {
+  if (G < 1 || G > 65535 || N < 1 || N > (1 << 16) || C < 1 || C > (1 << 16))
+    return fail(QB_EINVAL, "%s: G=%d, N=%d, C=%d; expected 1 <= G <= 65535 and 1 <= N, C <= 65536", fn, G, N, C);
+  return QB_OK;
+}
+
+QB_API int64_t qb_orthogonalize_workspace_bytes(int G, int N, int C) {
+  if (int rc = check_orthogonalize("qb_orthogonalize_workspace_bytes", G, N, C)) return rc;
+  return qbk::ortho_ws_layout(G, N, C).bytes;
+}
+
+QB_API int qb_orthogonalize(const float* x, int G, int N, int C, int steps, float a, float b, float c, uint16_t* o,
+                            void* ws, int64_t ws_bytes, qb_stream_t stream) {
+  const char* fn = "qb_orthogonalize";
+  if (int rc = check_orthogonalize(fn, G, N, C)) return rc;
+  if (steps < 1 || steps > 64) return fail(QB_EINVAL, "%s: steps=%d, expected 1 to 64", fn, steps);
+  if (!x || !o)
+    return fail(QB_EINVAL, "%s: x (float [G=%d][N=%d][C=%d]) and o (bf16, its shape) are required", fn, G, N, C);
+  const int64_t need = qbk::ortho_ws_layout(G, N, C).bytes;
+  if (!ws || ws_bytes < need)
+    return fail(QB_EINVAL, "%s: ws_bytes=%lld, this shape needs %lld (qb_orthogonalize_workspace_bytes)", fn,
+                ws ? (long long)ws_bytes : 0LL, (long long)need);
+  if (!aligned16(ws)) return fail(QB_EINVAL, "%s: ws must be 16-byte aligned", fn);
+  if (!aligned_all(2, {o})) return fail(QB_EINVAL, "%s: o must be 2-byte aligned", fn);
+  if (int rc = check_elem_align(fn, {x})) return rc;
+  return hip_status(qbk::launch_orthogonalize(x, G, N, C, steps, a, b, c, o, static_cast<uint8_t*>(ws), stream), fn);
+}
+
 QB_API const char* qb_status_string(int status) {
   switch (status) {
     case QB_OK: return "QB_OK";

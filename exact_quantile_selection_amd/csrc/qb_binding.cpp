@@ -143,12 +143,14 @@ Seqs sequences(PyObject* off, PyObject* valid, int64_t N) {
 
 int64_t ld(int64_t n) { return (n + 127) / 128 * 128; }
 int64_t sld(int64_t n) { return (n + 511) / 512 * 4; }
+int64_t ld4(int64_t n) { return (n + 255) / 256 * 128; }
+int64_t sld4(int64_t n) { return (n + 255) / 256 * 8; }
 
 // The library's entry points, set by `connect`.
 #define QB_ENTRIES(X) \
   X(qb_balance_forward) X(qb_balance_backward) X(qb_dispatch) X(qb_combine) X(qb_combine_backward) \
   X(qb_fp8_quantize) X(qb_fp8_quantize_cols) X(qb_fp8_quantize_weight) X(qb_fp8_product) X(qb_fp8_weight_grad) \
-  X(qb_bf16_product) X(qb_bf16_weight_grad)
+  X(qb_bf16_product) X(qb_bf16_weight_grad) X(qb_fp4_quantize) X(qb_fp4_quantize_weight) X(qb_fp4_product)
 struct Library {
 #define X(f) decltype(&::f) f;
   QB_ENTRIES(X)
@@ -368,6 +370,51 @@ int bf16_weight_grad(PyObject* const* a) {
                  stream_of(a[6])});
 }
 
+// x, xq, xs, row_src, stream
+int fp4_quantize(PyObject* const* a) {
+  const at::Tensor& x = tensor(a[0], BF16, "x", 2);
+  const Rows rows = rows_of(a[3], x.size(0));
+  const int64_t C = x.size(1);
+  return std::apply(
+      lib.qb_fp4_quantize,
+      std::tuple{address<const uint16_t>(x), x.size(0), rows.src, rows.M, narrow(C, "x"),
+                 req<uint8_t>(a[1], U8, "xq", {rows.M, ld4(C)}), req<uint8_t>(a[2], U8, "xs", {rows.M, sld4(C)}),
+                 stream_of(a[4])});
+}
+
+// w, wq, ws, wt, wts, stream
+int fp4_quantize_weight(PyObject* const* a) {
+  const at::Tensor* w = tensor_or_none(a[0], F32, "w");
+  if (!w) throw Bad{"w is required"};
+  if (w->dim() != 2 && w->dim() != 3) throw Bad{"w must be [N, C] or [G, N, C], got " + shape_name(w->sizes())};
+  const bool st = w->dim() == 3;
+  const int64_t G = st ? w->size(0) : 1, N = w->size(-2), C = w->size(-1);
+  uint8_t* wt = a[3] == Py_None ? nullptr : stack<uint8_t>(a[3], U8, "wt", st, G, C, ld4(N));
+  uint8_t* wts = a[4] == Py_None ? nullptr : stack<uint8_t>(a[4], U8, "wts", st, G, C, sld4(N));
+  return std::apply(
+      lib.qb_fp4_quantize_weight,
+      std::tuple{address<const float>(*w), narrow(G, "w"), narrow(N, "w"), narrow(C, "w"),
+                 stack<uint8_t>(a[1], U8, "wq", st, G, N, ld4(C)), stack<uint8_t>(a[2], U8, "ws", st, G, N, sld4(C)),
+                 wt, wts, stream_of(a[5])});
+}
+
+// xq, xs, w, w_scale, y, off, stream
+int fp4_product(PyObject* const* a) {
+  const at::Tensor& xq = tensor(a[0], U8, "xq", 2);
+  const Offsets g = offsets(a[5]);
+  const bool st = g.off != nullptr;
+  const int64_t M = xq.size(0), l = xq.size(1), C = 2 * l;
+  check_shape(xq, "xq", {M, ld4(C)});
+  const at::Tensor& w = tensor(a[2], U8, "w", st ? 3 : 2);
+  const int64_t N = w.size(-2);
+  return std::apply(
+      lib.qb_fp4_product,
+      std::tuple{address<const uint8_t>(xq), req<const uint8_t>(a[1], U8, "xs", {M, sld4(C)}),
+                 stack<const uint8_t>(a[2], U8, "w", st, g.G, N, l),
+                 stack<const uint8_t>(a[3], U8, "w_scale", st, g.G, N, sld4(C)), M, narrow(N, "w"), narrow(C, "xq"),
+                 g.off, g.G, req<uint16_t>(a[4], BF16, "y", {M, N}), stream_of(a[6])});
+}
+
 // No C++ exception leaves a call.
 template <int (*F)(PyObject* const*), int N>
 PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -417,6 +464,9 @@ PyMethodDef methods[] = {
     QB_CALL(weight_grad, 7),
     QB_CALL(bf16_product, 7),
     QB_CALL(bf16_weight_grad, 7),
+    QB_CALL(fp4_quantize, 5),
+    QB_CALL(fp4_quantize_weight, 6),
+    QB_CALL(fp4_product, 7),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_qb_binding", "Calls of libqb's expert layer.", -1, methods,

@@ -59,9 +59,16 @@ struct Gemm16 {
   int64_t part_a, part_b, mat_out, ldo, part_out;
   const uint16_t* add;       // what the result is added to (kSqr: S, kStep: X), in out's layout
   float by_sum, by_add;      // out = by_sum * sum + by_add * add
+  // 4-bit operands: exponent bytes, 8 for each 128 bytes of a row (mat_bs: between B's matrices)
+  const uint8_t *As, *Bs;
+  int64_t sld, mat_bs;
   uint16_t* last;            // kStep: the final result, bf16 [G][M][N], instead of out
   float by_last;
 };
+
+// 4-bit values (e2m1), two a byte, with a power of two for each 32 of them:
+// qb_fp4.hip.  A row's 128 bytes a stage are 256 values and 8 exponents.
+struct Fp4 {};
 
 template <class T>
 __device__ __forceinline__ v4f mma16(v8s a, v8s b, v4f c) {
@@ -70,6 +77,17 @@ __device__ __forceinline__ v4f mma16(v8s a, v8s b, v4f c) {
   else
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
                                                    0);
+}
+
+// The 128 4-bit products of a pair of rows, each lane's 32 with the exponents in
+// byte `half` of its words.  Sums are held in 32 bits: measured with single
+// values in all four lanes of a row, nothing within 2^-23 of the largest is lost.
+__device__ __forceinline__ v4f mma4(v8s a, v8s b, v4f c, int as, int bs, int half) {
+  const v4i x = __builtin_bit_cast(v4i, a), y = __builtin_bit_cast(v4i, b);
+  const v8i u = __builtin_shufflevector(x, x, 0, 1, 2, 3, -1, -1, -1, -1);
+  const v8i v = __builtin_shufflevector(y, y, 0, 1, 2, 3, -1, -1, -1, -1);
+  return half == 0 ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(u, v, c, 4, 4, 0, as, 0, bs)
+                   : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(u, v, c, 4, 4, 1, as, 1, bs);
 }
 
 // A value in two fp16 parts: the nearest, and the nearest to what is left.
@@ -120,6 +138,9 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm16(const Gemm16 g) {
   constexpr int KT = 64;  // of K a stage
   constexpr int A_BYTES = BM * KT * 2, B_BYTES = BN * KT * 2;
   constexpr int A_PW = A_BYTES / 1024 / W, B_PW = B_BYTES / 1024 / W;  // 1 KiB loads a wave and stage
+  constexpr bool FOUR = std::is_same_v<T, Fp4>;
+  constexpr int ROWS = BM + BN, S_PW = FOUR ? (ROWS / 32 + W - 1) / W : 0;  // loads of 32 rows' 8 exponents a wave
+  constexpr int S_BYTES = FOUR ? ROWS * 8 : 0;
   constexpr bool RAGGED = KIND == kRows || KIND == kGrad, SYM = KIND == kSym || KIND == kSqr;
   constexpr bool WIDE = KIND == kRows && !B_KS;
   constexpr int JT = TN < 4 ? TN : 4;  // WIDE: column tiles that share a stretch of 16 JT columns
@@ -131,15 +152,16 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm16(const Gemm16 g) {
   auto key_k = [](int k, int bx) {
     return bx >= 128 ? (k & 3) | ((k >> 1) & 4) : ((k >> 1) & 1) | ((k >> 2) & 2);
   };
-  __shared__ __align__(1024) uint8_t lds[S * (A_BYTES + B_BYTES) + (RAGGED ? 1024 * 3 + 16 : 16)];
+  __shared__ __align__(1024) uint8_t lds[S * (A_BYTES + B_BYTES + S_BYTES) + (RAGGED ? 1024 * 3 + 16 : 16)];
   uint8_t* const lds_b = lds + S * A_BYTES;
+  uint8_t* const lds_s = lds + S * (A_BYTES + B_BYTES);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const int tn_all = (g.N + BN - 1) / BN, tm_all = (g.M + BM - 1) / BM;
   int tiles = g.tiles;
 
   // the experts' first and last rows and their tiles of rows before each
-  int* const first_of = reinterpret_cast<int*>(lds + S * (A_BYTES + B_BYTES));
+  int* const first_of = reinterpret_cast<int*>(lds + S * (A_BYTES + B_BYTES + S_BYTES));
   int *const end_of = first_of + 256, *const before_of = end_of + 256;  // 256, 256 and 257 of them
   if (RAGGED && g.off) {
     if (wave == 0) {
@@ -242,7 +264,7 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm16(const Gemm16 g) {
           const int r = kc_r(u, A_PW), row = lp.m0 + r < lp.m_end ? lp.m0 + r : lp.m_end - 1;
           a_row[u] = row;
         }
-        if (KIND == kRows && g.src) {
+        if (KIND == kRows && !FOUR && g.src) {
 #pragma unroll
           for (int u = 0; u < A_PW; ++u) a_row[u] = g.src[a_row[u]];
           // waited for here, once a tile, and not before the loads of every stage
@@ -303,7 +325,7 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm16(const Gemm16 g) {
       return base + int64_t(uint64_t(uint32_t(row)) * uint32_t(g.lda)) + c;
     } else {
       const int r = kc_r(u, A_PW), q = (lane & 7) ^ key_a(r), row = a_row[u < A_ROWS ? u : 0];
-      const bool in = KIND != kRows || !g.src || uint32_t(row) < uint32_t(g.Mx);
+      const bool in = KIND != kRows || FOUR || !g.src || uint32_t(row) < uint32_t(g.Mx);
       k += q * 8;
       n = in ? g.K - k : 0;
       return base + int64_t(uint64_t(uint32_t(row)) * uint32_t(g.lda)) + k;
@@ -359,6 +381,22 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm16(const Gemm16 g) {
         held[u] = ld_inside(p, n);
       }
     }
+    if constexpr (FOUR) {
+#pragma unroll
+      for (int j = 0; j < S_PW; ++j) {
+        const int first = (wave * S_PW + j) % (ROWS / 32) * 32, r = first + (lane >> 1);
+        const uint8_t* p;
+        if (first < BM) {
+          const int row = lp.m0 + r < lp.m_end ? lp.m0 + r : lp.m_end - 1;
+          p = g.As + int64_t(row) * g.sld;
+        } else {
+          const int row = lp.n0 + r - BM < g.N ? lp.n0 + r - BM : g.N - 1;
+          p = g.Bs + int64_t(lp.e) * g.mat_bs + int64_t(row) * g.sld;
+        }
+        __builtin_amdgcn_global_load_lds((glb_vptr)(p + ls * 8 + (lane & 1) * 4),
+                                         (lds_vptr)(lds_s + st * S_BYTES + first * 8), 4, 0, 0);
+      }
+    }
     next_stage();
   };
   auto put = [&](int st) {  // !DIRECT: what issue() read
@@ -370,8 +408,11 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm16(const Gemm16 g) {
 
   v4f acc[TM][TN];
   const int r = lane & 15, g4 = lane >> 4;
+  // (4 bits: a lane's two halves are side by side, so that their exponents are)
+  constexpr int HALF = FOUR ? 16 : 64;
+  const int s4 = FOUR ? 2 * g4 : g4;
   const int frag_a = A_KS ? (8 * g4 + (r >> 2)) * (BM * 2) + (((wm * TM) ^ key_k(8 * g4 + (r >> 2), BM)) * 32) + (r & 3) * 8
-                          : (wm * TM * 16 + r) * 128 + ((g4 ^ key_a(r)) * 16);
+                          : (wm * TM * 16 + r) * 128 + ((s4 ^ key_a(r)) * 16);
   const int br = WIDE ? (r >> 2) * (4 * JT) + (r & 3) : r;  // KC: its row of column tile 0, and what tile j adds
   auto b_row = [](int j) { return WIDE ? j / JT * (16 * JT) + j % JT * 4 : j * 16; };
   auto frag_b = [&](int j) {
@@ -379,7 +420,7 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm16(const Gemm16 g) {
       return ((8 * g4 + (r >> 2)) * (BN * 2) + (((wn * TN) ^ key_k(8 * g4 + (r >> 2), BN)) * 32) + (r & 3) * 8) ^ (j * 32);
     } else {
       const int row = br + b_row(j);
-      return (wn * TN * 16 + row) * 128 + ((g4 ^ key_b(row)) * 16);
+      return (wn * TN * 16 + row) * 128 + ((s4 ^ key_b(row)) * 16);
     }
   };
   // half h of the stage's K: 8 values of the lane's row or column
@@ -394,17 +435,26 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm16(const Gemm16 g) {
     if constexpr (A_KS)
       return read_ks(p + (frag_a ^ (i * 32)), BM * 2, h);
     else
-      return *reinterpret_cast<const v8s*>(p + i * 16 * 128 + (frag_a ^ (h * 64)));
+      return *reinterpret_cast<const v8s*>(p + i * 16 * 128 + (frag_a ^ (h * HALF)));
   };
   auto read_b = [&](int st, int j, int h) -> v8s {
     const uint8_t* p = lds_b + st * B_BYTES;
     if constexpr (B_KS)
       return read_ks(p + frag_b(j), BN * 2, h);
     else
-      return *reinterpret_cast<const v8s*>(p + (frag_b(j) ^ (h * 64)));
+      return *reinterpret_cast<const v8s*>(p + (frag_b(j) ^ (h * HALF)));
   };
   // stage st's products, while the next loads go to stage `into` after the first row tile's
   auto multiply = [&](int st, bool load, int into) {
+    int as[FOUR ? TM : 1], bs[FOUR ? TN : 1];  // two exponents each, one a half
+    if constexpr (FOUR) {
+      const uint8_t* ss = lds_s + st * S_BYTES + g4 * 2;
+#pragma unroll
+      for (int i = 0; i < TM; ++i) as[i] = *reinterpret_cast<const uint16_t*>(ss + ((wm * TM + i) * 16 + r) * 8);
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        bs[j] = *reinterpret_cast<const uint16_t*>(ss + (BM + wn * TN * 16 + br + b_row(j)) * 8);
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       v8s b[TN], a[2];
@@ -415,7 +465,12 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm16(const Gemm16 g) {
       for (int i = 0; i < TM; ++i) {
         if (i + 1 < TM) a[(i + 1) & 1] = read_a(st, i + 1, h);
 #pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = mma16<T>(b[j], a[i & 1], acc[i][j]);
+        for (int j = 0; j < TN; ++j) {
+          if constexpr (FOUR)
+            acc[i][j] = mma4(b[j], a[i & 1], acc[i][j], bs[j], as[i], h);
+          else
+            acc[i][j] = mma16<T>(b[j], a[i & 1], acc[i][j]);
+        }
         if (h == 0 && i == 0 && load) issue(into);
       }
     }
@@ -558,7 +613,7 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm16(const Gemm16 g) {
   // order of their issue, and a barrier publishes every wave's.
   constexpr int D = DIRECT ? S - 1 : 1;
   // (kGrad's numbers of rows are loads too)
-  constexpr int PER = LOADS, PER_SRC = LOADS + (KIND == kGrad ? B_PW : 0);
+  constexpr int PER = LOADS + S_PW, PER_SRC = LOADS + (KIND == kGrad ? B_PW : 0);
   advance();
   int ist = 0, ahead = 0;
   // the multiplying cursor walks the same tiles as the loading one

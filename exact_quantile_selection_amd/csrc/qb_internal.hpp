@@ -215,4 +215,42 @@ int launch_bf16_product(const uint16_t* x, int Mx, const int32_t* src, int M, co
 int launch_bf16_weight_grad(const uint16_t* dy, const uint16_t* x, int Mx, const int32_t* src, int M, int N, int C,
                             const int32_t* off, int G, float* dw, float* ws, hipStream_t st);
 
+// 4-bit products with a power-of-two scale for each block of 32: bytes of a row of n values, and of its scales.
+constexpr int kQBlock4 = 32;
+inline int64_t fp4_ld(int64_t n) { return (n + 255) / 256 * 128; }
+inline int64_t fp4_sld(int64_t n) { return (n + 255) / 256 * 8; }
+int launch_fp4_quantize(const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M, int C, uint8_t* xq,
+                        uint8_t* xs, hipStream_t st);
+int launch_fp4_quantize_weight(const float* w, int G, int N, int C, uint8_t* wq, uint8_t* ws, uint8_t* wt,
+                               uint8_t* wts, hipStream_t st);
+int launch_fp4_product(const uint8_t* xq, const uint8_t* xs, const uint8_t* w, const uint8_t* ws, int M, int N, int C,
+                       const int32_t* off, int G, uint16_t* y, hipStream_t st);
+
+// The orthogonalised update.  Workspace (byte offsets, 256-aligned): partial
+// sums of squares, x twice (this step's and the next's), S = x x^T or x^T x and
+// P = b S + c S S, each value in two 16-bit parts, rows rounded up to 8 values.
+constexpr int kOrthoSums = 64;  // partial sums of a matrix at most
+struct OrthoWs {
+  bool tall;
+  int64_t R, ldx, ldr;           // rows of S; values between rows of x and of S
+  int64_t x0, x1, s, p, bytes;
+};
+inline OrthoWs ortho_ws_layout(int64_t G, int64_t N, int64_t C) {
+  OrthoWs w;
+  auto up = [](int64_t n, int64_t a) { return (n + a - 1) / a * a; };
+  w.tall = N > C;
+  w.R = w.tall ? C : N;
+  w.ldx = up(C, 8);
+  w.ldr = up(w.R, 8);
+  const int64_t x = up(G * N * w.ldx * 4, 256), s = up(G * w.R * w.ldr * 4, 256);
+  w.x0 = up(G * kOrthoSums * 8, 256);
+  w.x1 = w.x0 + x;
+  w.s = w.x1 + x;
+  w.p = w.s + s;
+  w.bytes = w.p + s;
+  return w;
+}
+int launch_orthogonalize(const float* x, int G, int N, int C, int steps, float a, float b, float c, uint16_t* o,
+                         uint8_t* ws, hipStream_t st);
+
 }  // namespace qbk

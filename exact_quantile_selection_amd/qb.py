@@ -89,6 +89,10 @@ def lib() -> C.CDLL:
             "qb_fp8_quantize_weight": [vp, i32, i32, i32, vp, vp, vp, vp, vp],
             "qb_fp8_product": [vp, vp, vp, vp, i64, i32, i32, vp, i32, i32, vp, vp],
             "qb_fp8_weight_grad": [vp, vp, vp, vp, i64, i32, i32, vp, i32, vp, vp],
+            "qb_fp4_quantize": [vp, i64, vp, i64, i32, vp, vp, vp],
+            "qb_fp4_quantize_weight": [vp, i32, i32, i32, vp, vp, vp, vp, vp],
+            "qb_fp4_product": [vp, vp, vp, vp, i64, i32, i32, vp, i32, vp, vp],
+            "qb_orthogonalize": [vp, i32, i32, i32, i32, f32, f32, f32, vp, vp, i64, vp],
             "qb_bf16_product": [vp, i64, vp, i64, vp, i32, i32, vp, i32, i32, vp, vp],
             "qb_bf16_weight_grad": [vp, vp, i64, vp, i64, i32, i32, vp, i32, vp, vp, i64, vp],
         }
@@ -104,8 +108,9 @@ def lib() -> C.CDLL:
         L.qb_dispatch_rows.argtypes = [i64, i32, i32, i32]
         L.qb_dispatch_workspace_bytes.argtypes = [i64, i32, i32]
         L.qb_bf16_weight_grad_workspace_bytes.argtypes = [i64, i32, i32, i32]
+        L.qb_orthogonalize_workspace_bytes.argtypes = [i32, i32, i32]
         for name in ("qb_balance_workspace_bytes", "qb_dispatch_rows", "qb_dispatch_workspace_bytes",
-                     "qb_bf16_weight_grad_workspace_bytes"):
+                     "qb_bf16_weight_grad_workspace_bytes", "qb_orthogonalize_workspace_bytes"):
             getattr(L, name).restype = C.c_int64
         L.qb_status_string.argtypes = [C.c_int]
         L.qb_status_string.restype = C.c_char_p
@@ -118,7 +123,8 @@ def lib() -> C.CDLL:
 # the expert layer's entry points, in the order in which the compiled binding takes their addresses
 _EXPERT_LAYER = ("qb_balance_forward", "qb_balance_backward", "qb_dispatch", "qb_combine", "qb_combine_backward",
                  "qb_fp8_quantize", "qb_fp8_quantize_cols", "qb_fp8_quantize_weight", "qb_fp8_product",
-                 "qb_fp8_weight_grad", "qb_bf16_product", "qb_bf16_weight_grad")
+                 "qb_fp8_weight_grad", "qb_bf16_product", "qb_bf16_weight_grad",
+                 "qb_fp4_quantize", "qb_fp4_quantize_weight", "qb_fp4_product")
 
 
 def _calls():
@@ -625,6 +631,53 @@ def qb_bf16_weight_grad(dy, x, dw, off=None, row_src=None, ws=None, stream=None)
     of dy bf16 [M, N] times x bf16, whose rows row_src numbers as for
     qb_bf16_product; ws (uint8) lets few, long sums be added up in parts."""
     _check(_calls().bf16_weight_grad(dy, x, dw, off, row_src, ws, stream))
+
+
+def fp4_ld(n):
+    """Bytes of a row of n values in 4 bits."""
+    return -(-n // 256) * 128
+
+
+def fp4_sld(n):
+    """Bytes of its row of scales."""
+    return -(-n // 256) * 8
+
+
+def qb_fp4_quantize(x, xq, xs, row_src=None, stream=None):
+    """x bf16 [Mx, C] -> xq uint8 [M, fp4_ld(C)], two e2m1 values a byte, and
+    xs uint8 [M, fp4_sld(C)], a scale for each 32 columns; row_src as for
+    qb_fp8_quantize."""
+    _check(_calls().fp4_quantize(x, xq, xs, row_src, stream))
+
+
+def qb_fp4_quantize_weight(w, wq, ws, wt=None, wts=None, stream=None):
+    """w float [N, C] or [G, N, C] -> wq [.., N, fp4_ld(C)], ws (blocks along C)
+    and, on request, the transpose with blocks along N, wt [.., C, fp4_ld(N)]
+    and wts."""
+    _check(_calls().fp4_quantize_weight(w, wq, ws, wt, wts, stream))
+
+
+def qb_fp4_product(xq, xs, w, w_scale, y, off=None, stream=None):
+    """y bf16 [M, N] = xq times w [N, ld] transposed, sums in 32 bits; with off
+    int32 [G + 1] rows off[e] .. off[e + 1] - 1 take w[e] of w [G, N, ld]."""
+    _check(_calls().fp4_product(xq, xs, w, w_scale, y, off, stream))
+
+
+def qb_orthogonalize_workspace_bytes(G, N, C):
+    return _bytes(lib().qb_orthogonalize_workspace_bytes(G, N, C))
+
+
+def qb_orthogonalize(x, o, ws, steps=5, poly=(3.4445, -4.7750, 2.0315), stream=None):
+    """o bf16 = x float [N, C] or [G, N, C], each matrix divided by its norm and
+    taken `steps` times through a x + (b S + c S S) x, S = x x^T, (a, b, c) =
+    poly; ws uint8, qb_orthogonalize_workspace_bytes."""
+    if not isinstance(x, torch.Tensor) or x.dim() not in (2, 3):
+        raise ValueError("x must be [N, C] or [G, N, C]")
+    a, b, c = poly
+    G, N, Cn = (1,) * (3 - x.dim()) + tuple(x.shape)
+    _check(lib().qb_orthogonalize(_ptr(x, torch.float32, "x"), G, N, Cn, steps, a, b, c,
+                                  _ptr(o, torch.bfloat16, "o", x.shape), _ptr(ws, torch.uint8, "ws"), ws.numel(),
+                                  _stream(stream)))
 
 
 # ---------------------------------------------------------------------------

@@ -644,6 +644,57 @@ QB_API int qb_bf16_weight_grad(const uint16_t* dy, const uint16_t* x, int64_t Mx
                                int N, int C, const int32_t* off, int G, float* dw, void* ws, int64_t ws_bytes,
                                qb_stream_t stream);
 
+/*
+ * Products in 4-bit floating point (e2m1) with a power-of-two scale for each
+ * block of 32 values along the sum.  A quantised matrix of n columns has rows
+ * of ld(n) = ceil(n / 256) * 128 bytes, two values a byte, the even one in the
+ * low half, zeros past column n, and rows of sld(n) = ceil(n / 256) * 8 scale
+ * bytes: byte j holds e + 127, e the least whole number >= -126 with max |x|
+ * <= 6 * 2^e over columns 32 j .. 32 j + 31 (past the last block any but 255).
+ * Values are x 2^-e rounded to nearest even.  A block that holds a NaN or an
+ * infinity has the scale 255 and stands for NaN.
+ *
+ * qb_fp4_quantize: x bf16 [Mx][C] -> xq [M][ld(C)], xs [M][sld(C)]; row_src
+ * as for qb_fp8_quantize.
+ * qb_fp4_quantize_weight: w float [G][N][C] -> wq [G][N][ld(C)] and ws
+ * [G][N][sld(C)] with blocks along C, and the transpose with blocks along N,
+ * wt [G][C][ld(N)] and wts [G][C][sld(N)] (nullable, both or neither), whose
+ * values are rounded with other scales.
+ * qb_fp4_product: y[m][n] = sum_c x[m][c] w[n][c], y bf16 [M][N], every sum in
+ * 32 bits and rounded once; off and G as for qb_fp8_product.  The gradient of
+ * x is the same call on a quantised dy and the transposed weight, that of w is
+ * qb_bf16_weight_grad.
+ *
+ * Quantised matrices are 16-byte aligned, scale rows 8-byte, bf16 and float
+ * arrays by their element.  0 <= M, Mx <= 2^22 rows; 1 <= N, C <= 2^22; 1 <=
+ * G <= 256.
+ */
+QB_API int qb_fp4_quantize(const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M, int C, uint8_t* xq,
+                           uint8_t* xs, qb_stream_t stream);
+QB_API int qb_fp4_quantize_weight(const float* w, int G, int N, int C, uint8_t* wq, uint8_t* ws, uint8_t* wt,
+                                  uint8_t* wts, qb_stream_t stream);
+QB_API int qb_fp4_product(const uint8_t* xq, const uint8_t* xs, const uint8_t* w, const uint8_t* w_scale, int64_t M,
+                          int N, int C, const int32_t* off, int G, uint16_t* y, qb_stream_t stream);
+
+/*
+ * The orthogonalised update of a stack of matrices, for their optimizer:
+ * x <- x / |x| (the root of its squares' sum), then `steps` times x <- a x + (b
+ * S + c S S) x with S = x x^T, o = x rounded to bf16.  With a, b, c = 3.4445,
+ * -4.7750, 2.0315 five steps take every singular value above 1/100 to between
+ * 0.7 and 1.2, so that o is nearly the orthogonal factor of x.  A zero matrix
+ * gives zero, one that holds a NaN or an infinity gives NaN throughout.
+ *   x float [G][N][C], o bf16 [G][N][C]; 1 <= G <= 65535, 1 <= N, C <= 65536;
+ *   1 <= steps <= 64.  ws: at least qb_orthogonalize_workspace_bytes, 16-byte
+ *   aligned, its contents do not matter.
+ * Inside, values carry 11 to 22 bits and every sum is held in 32: o is within
+ * 2e-3 of |o| of the formula's, most of it o's own rounding.  Entries of x
+ * beyond 16, and of S and b S + c S S beyond 256, become infinite: polynomials
+ * that keep singular values below 4 stay clear of both.
+ */
+QB_API int64_t qb_orthogonalize_workspace_bytes(int G, int N, int C);
+QB_API int qb_orthogonalize(const float* x, int G, int N, int C, int steps, float a, float b, float c, uint16_t* o,
+                            void* ws, int64_t ws_bytes, qb_stream_t stream);
+
 /* Short name of a status code (static storage). */
 QB_API const char* qb_status_string(int status);
 
