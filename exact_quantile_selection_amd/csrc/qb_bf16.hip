@@ -139,7 +139,7 @@ __global__ __launch_bounds__(256) void k_bf16_join(const float* __restrict__ par
 
 // ---------------------------------------------------------------------------
 
-template <int KIND, bool A_KS, bool B_KS, int B, int WM, int WN, int S, bool DIRECT>
+template <int KIND, bool A_KS, bool B_KS, int B, int S, bool DIRECT>
 static int tiled(Gemm16 g, hipStream_t st) {
   const int64_t tn = (g.N + B - 1) / B;
   int64_t tm = (g.M + B - 1) / B;
@@ -149,8 +149,8 @@ static int tiled(Gemm16 g, hipStream_t st) {
   g.tiles = int(tiles);
   // as many workgroups as run at once (a 256 x 256 tile's ring fills a CU's LDS, the others' half of it)
   const int64_t most = int64_t(device_cu_count()) * (B == 256 ? 1 : 2);
-  hipLaunchKernelGGL((k_gemm16<__bf16, KIND, A_KS, B_KS, B, B, WM, WN, S, DIRECT>), dim3(unsigned(std::min(tiles, most))),
-                     dim3(WM * WN * kWave), 0, st, g);
+  hipLaunchKernelGGL((k_gemm16<__bf16, KIND, A_KS, B_KS, B, S, DIRECT>), dim3(unsigned(std::min(tiles, most))),
+                     dim3(B == 256 ? 512 : 256), 0, st, g);
   return int(hipGetLastError());
 }
 
@@ -158,11 +158,11 @@ template <int KIND, bool A_KS, bool B_KS>
 static int gemm(const Gemm16& g, int64_t t256, int64_t t128, int64_t t64, double uneven, bool direct, hipStream_t st) {
   const int64_t cu = device_cu_count();
   if (t64 <= 2 * cu)
-    return direct ? tiled<KIND, A_KS, B_KS, 64, 2, 2, 4, true>(g, st) : tiled<KIND, A_KS, B_KS, 64, 2, 2, 2, false>(g, st);
+    return direct ? tiled<KIND, A_KS, B_KS, 64, 4, true>(g, st) : tiled<KIND, A_KS, B_KS, 64, 4, false>(g, st);
   const double rounds256 = double((t256 + cu - 1) / cu), rounds128 = double((t128 + 2 * cu - 1) / (2 * cu));
   if (direct && t256 > 0 && 3.3 * (rounds256 + uneven) < 2 * rounds128)
-    return tiled<KIND, A_KS, B_KS, 256, 2, 4, 2, true>(g, st);
-  return direct ? tiled<KIND, A_KS, B_KS, 128, 2, 2, 2, true>(g, st) : tiled<KIND, A_KS, B_KS, 128, 2, 2, 2, false>(g, st);
+    return tiled<KIND, A_KS, B_KS, 256, 2, true>(g, st);
+  return direct ? tiled<KIND, A_KS, B_KS, 128, 2, true>(g, st) : tiled<KIND, A_KS, B_KS, 128, 2, false>(g, st);
 }
 
 template <int MT, int KW>

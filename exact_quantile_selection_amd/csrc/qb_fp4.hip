@@ -256,7 +256,7 @@ __global__ __launch_bounds__(512) void k_fp4_thin(const uint8_t* __restrict__ A,
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int i = 0; i < MT; ++i) acc[i] = mma4(b[u][h], a[u][i][h], acc[i], bs[u], as[u][i], h);
+          for (int i = 0; i < MT; ++i) acc[i] = mma4(b[u][h], a[u][i][h], acc[i], bs[u] >> (8 * h), as[u][i] >> (8 * h));
       }
   }
   if constexpr (KW > 1) {
@@ -294,14 +294,14 @@ static int64_t row_tiles(const Gemm16& g, int BM) {
   return g.off ? g.M / BM + std::min(g.G, g.M) : (g.M + BM - 1) / BM;
 }
 
-template <int B, int WM, int WN, int S>
+template <int B, int S>
 static int tiled(Gemm16 g, hipStream_t st) {
   const int64_t tiles = row_tiles(g, B) * ((g.N + B - 1) / B);
   if (tiles > INT32_MAX) return int(hipErrorInvalidValue);
   g.tiles = int(tiles);
   const int64_t most = int64_t(device_cu_count()) * (B == 256 ? 1 : 2);
-  hipLaunchKernelGGL((k_gemm16<Fp4, kRows, false, false, B, B, WM, WN, S, true>), dim3(unsigned(std::min(tiles, most))),
-                     dim3(WM * WN * kWave), 0, st, g);
+  hipLaunchKernelGGL((k_gemm16<Fp4, kRows, false, false, B, S, true>), dim3(unsigned(std::min(tiles, most))),
+                     dim3(B == 256 ? 512 : 256), 0, st, g);
   return int(hipGetLastError());
 }
 
@@ -352,10 +352,10 @@ int launch_fp4_product(const uint8_t* xq, const uint8_t* xs, const uint8_t* w, c
   const int64_t cu = device_cu_count();
   if (rows <= 32 && (off || tiles(64) <= cu)) return rows <= 16 ? few<1>(g, st) : few<2>(g, st);
   const int64_t t256 = rows <= 128 && off ? 0 : tiles(256);
-  if ((off ? tiles(64) * 2 / 3 : tiles(64)) <= 2 * cu) return tiled<64, 2, 2, 4>(g, st);
+  if ((off ? tiles(64) * 2 / 3 : tiles(64)) <= 2 * cu) return tiled<64, 4>(g, st);
   const double rounds256 = double((t256 + cu - 1) / cu), rounds128 = double((tiles(128) + 2 * cu - 1) / (2 * cu));
-  if (t256 > 0 && 3.3 * (rounds256 + (off ? 0.1 : 0.0)) < 2 * rounds128) return tiled<256, 2, 4, 2>(g, st);
-  return tiled<128, 2, 2, 2>(g, st);
+  if (t256 > 0 && 3.3 * (rounds256 + (off ? 0.1 : 0.0)) < 2 * rounds128) return tiled<256, 2>(g, st);
+  return tiled<128, 2>(g, st);
 }
 
 }  // namespace qbk

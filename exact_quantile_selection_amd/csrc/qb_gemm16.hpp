@@ -80,14 +80,13 @@ __device__ __forceinline__ v4f mma16(v8s a, v8s b, v4f c) {
 }
 
 // The 128 4-bit products of a pair of rows, each lane's 32 with the exponents in
-// byte `half` of its words.  Sums are held in 32 bits: measured with single
+// its words' lowest bytes.  Sums are held in 32 bits: measured with single
 // values in all four lanes of a row, nothing within 2^-23 of the largest is lost.
-__device__ __forceinline__ v4f mma4(v8s a, v8s b, v4f c, int as, int bs, int half) {
+__device__ __forceinline__ v4f mma4(v8s a, v8s b, v4f c, int as, int bs) {
   const v4i x = __builtin_bit_cast(v4i, a), y = __builtin_bit_cast(v4i, b);
   const v8i u = __builtin_shufflevector(x, x, 0, 1, 2, 3, -1, -1, -1, -1);
   const v8i v = __builtin_shufflevector(y, y, 0, 1, 2, 3, -1, -1, -1, -1);
-  return half == 0 ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(u, v, c, 4, 4, 0, as, 0, bs)
-                   : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(u, v, c, 4, 4, 1, as, 1, bs);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(u, v, c, 4, 4, 0, as, 0, bs);
 }
 
 // A value in two fp16 parts: the nearest, and the nearest to what is left.
@@ -116,57 +115,95 @@ __device__ __forceinline__ uint4 ld_inside(const uint16_t* p, int n) {
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// 16 bytes a lane from memory to the 1 KiB of LDS at `to` (the wave's).  The
-// compiler waits for every load that it knows to go to LDS before it reads
-// LDS by a transposing read, whatever the addresses; of these it does not know,
-// and the kernel's own waits order them (an operand lands a stage before it is
-// read).  There is no result register, so nothing is reused too early, and m0
-// has no other use in a kernel that calls this.
+// 16 or 4 bytes a lane from memory to the LDS at `to` (the wave's), lane by
+// lane.  The compiler waits for every load that it knows to go to LDS before it
+// reads LDS by a transposing read, whatever the addresses; of these it does not
+// know, and the kernel's own waits order them (an operand lands a stage before
+// it is read).  There is no result register, so nothing is reused too early,
+// and m0 has no other use in a kernel that calls this.
+template <int BYTES>
 __device__ __forceinline__ void load_to_lds(const void* from, uint8_t* to) {
   const uint32_t at = uint32_t(uintptr_t((__attribute__((address_space(3))) uint8_t*)to));
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(from) : "memory");
+  if constexpr (BYTES == 16)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(from) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(at), "v"(from) : "memory");
+}
+// The same from a base that the wave shares and an offset of the lane's.
+template <int BYTES>
+__device__ __forceinline__ void load_to_lds(const void* base, uint32_t off, uint8_t* to) {
+  const uint32_t at = uint32_t(uintptr_t((__attribute__((address_space(3))) uint8_t*)to));
+  if constexpr (BYTES == 16)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");
 }
 
-// BM x BN tiles, waves WM x WN, a ring of S stages.  DIRECT: rows are multiples
+// A pointer that all lanes hold, told to the compiler: it then lies in scalar registers.
+__device__ __forceinline__ const uint8_t* same_for_all(const void* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(v)), hi = __builtin_amdgcn_readfirstlane(uint32_t(v >> 32));
+  return reinterpret_cast<const uint8_t*>(uint64_t(hi) << 32 | lo);
+}
+
+// Waits until at most k (of up to K) stages of PER loads, and EXTRA stores, are
+// outstanding, and every LDS read is back.
+template <int K, int PER, int EXTRA>
+__device__ __forceinline__ void wait_stages(int k) {
+  if constexpr (K > 0) {
+    if (k < K) return wait_stages<K - 1, PER, EXTRA>(k);
+  }
+  __builtin_amdgcn_s_waitcnt(vm_count(K * PER + EXTRA < 63 ? K * PER + EXTRA : 63));
+}
+
+#define QB_INLINE __attribute__((always_inline))
+
+// B x B tiles by 2 x 4 waves (2 x 2 for the smaller ones), a ring of S stages.  DIRECT: rows are multiples
 // of 16 bytes, and the loads go to LDS; else they pass through registers, 2
 // bytes being the only alignment asked for.  PA, PB: which part of each operand
 // each of PARTS passes over K multiplies, a bit a pass.
-template <class T, int KIND, bool A_KS, bool B_KS, int BM, int BN, int WM, int WN, int S, bool DIRECT, int PARTS = 1,
-          int PA = 0, int PB = 0>
-__global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm16(const Gemm16 g) {
-  constexpr int W = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
-  constexpr int KT = 64;  // of K a stage
-  constexpr int A_BYTES = BM * KT * 2, B_BYTES = BN * KT * 2;
-  constexpr int A_PW = A_BYTES / 1024 / W, B_PW = B_BYTES / 1024 / W;  // 1 KiB loads a wave and stage
+//
+// A stage is two steps of 32 of K.  While a wave multiplies a step, whose
+// operands are in registers, it reads the next one's, A's row tile by row tile
+// into the registers that are done with; early in a stage's second step it waits
+// at a barrier for the next stage's loads, and every wave has read all of this
+// one, whose place in the ring takes new loads in the shadow of the products
+// that are left.  The loads run on over the end of a tile.
+template <class T, int KIND, bool A_KS, bool B_KS, int B, int S, bool DIRECT, int PARTS = 1, int PA = 0, int PB = 0>
+__global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16 g) {
+  constexpr int WN = B == 256 ? 4 : 2, W = 2 * WN, TM = B / 32, TN = B / WN / 16;
+  constexpr int KT = 64;  // of K a stage: 128 bytes of a KC row
+  constexpr int BYTES = B * KT * 2, PW = BYTES / 1024 / W;  // of an operand's stage; its 1 KiB loads a wave
   constexpr bool FOUR = std::is_same_v<T, Fp4>;
-  constexpr int ROWS = BM + BN, S_PW = FOUR ? (ROWS / 32 + W - 1) / W : 0;  // loads of 32 rows' 8 exponents a wave
-  constexpr int S_BYTES = FOUR ? ROWS * 8 : 0;
+  constexpr int S_PW = FOUR ? 2 * B / 32 / W : 0;  // loads of 32 rows' 8 exponents a wave
+  constexpr int S_BYTES = FOUR ? 2 * B * 8 : 0;
   constexpr bool RAGGED = KIND == kRows || KIND == kGrad, SYM = KIND == kSym || KIND == kSqr;
+  constexpr bool BY_ROW = KIND == kRows && !FOUR;  // A's rows may be numbered by src
   constexpr bool WIDE = KIND == kRows && !B_KS;
   constexpr int JT = TN < 4 ? TN : 4;  // WIDE: column tiles that share a stretch of 16 JT columns
-  static_assert(A_PW * W * 1024 == A_BYTES && B_PW * W * 1024 == B_BYTES, "tile split");
-  static_assert(TN % JT == 0 && JT >= 2 && (!SYM || BM == BN) && (KIND != kGrad || BM == BN), "tile shape");
   // a row's number in the swizzle of its slots
   auto key_a = [](int row) { return (row >> 1) & 7; };
   auto key_b = [](int row) { return WIDE ? ((row >> 1) & 1) | ((row >> (JT == 4 ? 3 : 2)) & 6) : (row >> 1) & 7; };
-  auto key_k = [](int k, int bx) {
-    return bx >= 128 ? (k & 3) | ((k >> 1) & 4) : ((k >> 1) & 1) | ((k >> 2) & 2);
-  };
-  __shared__ __align__(1024) uint8_t lds[S * (A_BYTES + B_BYTES + S_BYTES) + (RAGGED ? 1024 * 3 + 16 : 16)];
-  uint8_t* const lds_b = lds + S * A_BYTES;
-  uint8_t* const lds_s = lds + S * (A_BYTES + B_BYTES);
+  auto key_k = [](int k) { return B >= 128 ? (k & 3) | ((k >> 1) & 4) : ((k >> 1) & 1) | ((k >> 2) & 2); };
+  constexpr int RING = S * (2 * BYTES + S_BYTES);
+  // numbers of rows: of the last 8 tiles' (kRows), of two batches of stages for each wave (kGrad)
+  constexpr int SRC_BYTES = !DIRECT ? 0 : BY_ROW ? 8 * B * 4 : KIND == kGrad ? W * 512 : 0;
+  __shared__ __align__(1024) uint8_t lds[RING + SRC_BYTES + (RAGGED ? 1024 * 3 + 16 : 16)];
+  uint8_t* const lds_b = lds + S * BYTES;
+  uint8_t* const lds_s = lds + S * 2 * BYTES;
+  int* const src_of = reinterpret_cast<int*>(lds + RING);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  const int tn_all = (g.N + BN - 1) / BN, tm_all = (g.M + BM - 1) / BM;
+  const int tn_all = (g.N + B - 1) / B, tm_all = (g.M + B - 1) / B;
   int tiles = g.tiles;
 
   // the experts' first and last rows and their tiles of rows before each
-  int* const first_of = reinterpret_cast<int*>(lds + S * (A_BYTES + B_BYTES + S_BYTES));
+  int* const first_of = reinterpret_cast<int*>(lds + RING + SRC_BYTES);
   int *const end_of = first_of + 256, *const before_of = end_of + 256;  // 256, 256 and 257 of them
   if (RAGGED && g.off) {
     if (wave == 0) {
       int lo[4], hi[4], n[4], before;
-      const int total = group_tiles(g.off, g.G, KIND == kGrad ? g.K : g.M, BM, lane, lo, hi, n, before);
+      const int total = group_tiles(g.off, g.G, KIND == kGrad ? g.K : g.M, B, lane, lo, hi, n, before);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         first_of[4 * lane + j] = lo[j];
@@ -178,7 +215,8 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm16(const Gemm16 g) {
     }
     __syncthreads();
     // (offsets out of order could make more than there are)
-    if constexpr (KIND == kRows) tiles = (before_of[256] < tiles / tn_all ? before_of[256] : tiles / tn_all) * tn_all;
+    if constexpr (KIND == kRows)
+      tiles = std::min(__builtin_amdgcn_readfirstlane(before_of[256]), tiles / tn_all) * tn_all;
   }
 
   // A tile: rows m0 .. m_end - 1 and columns from n0 of a result; K from k0 to
@@ -186,7 +224,7 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm16(const Gemm16 g) {
   struct Place {
     int m0, m_end, n0, k0, k1, e, part;
   };
-  auto place = [&](int t) {
+  auto place = [&](int t) QB_INLINE {
     Place p{0, g.M, 0, 0, g.K, 0, 0};
     int tm, tn;
     if constexpr (KIND == kGrad) {
@@ -204,7 +242,7 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm16(const Gemm16 g) {
         p.k0 += std::min(p.part * each, stages) * KT;
         p.k1 = std::min(p.k1, p.k0 + each * KT);
       }
-      p.m0 = tm * BM;
+      p.m0 = tm * B;
     } else if constexpr (KIND == kRows) {
       if (g.off) {
         tile_order(t, tiles / tn_all, tn_all, 8, tm, tn);
@@ -213,11 +251,11 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm16(const Gemm16 g) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) begun += __popcll(__ballot(before_of[4 * lane + j] <= tm));
         p.e = begun > 0 ? begun - 1 : 0;
-        p.m0 = __builtin_amdgcn_readfirstlane(first_of[p.e] + (tm - before_of[p.e]) * BM);
+        p.m0 = __builtin_amdgcn_readfirstlane(first_of[p.e] + (tm - before_of[p.e]) * B);
         p.m_end = __builtin_amdgcn_readfirstlane(end_of[p.e]);
       } else {
         tile_order(t, tm_all, tn_all, 8, tm, tn);
-        p.m0 = tm * BM;
+        p.m0 = tm * B;
       }
     } else if constexpr (SYM) {
       // tiles on and below the diagonal, row by row
@@ -228,257 +266,369 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm16(const Gemm16 g) {
       while ((tm + 1) * (tm + 2) / 2 <= t) ++tm;
       while (tm * (tm + 1) / 2 > t) --tm;
       tn = t - tm * (tm + 1) / 2;
-      p.m0 = tm * BM;
+      p.m0 = tm * B;
     } else {
       const int per = tm_all * tn_all;
       p.e = t / per;
       tile_order(t % per, tm_all, tn_all, 8, tm, tn);
-      p.m0 = tm * BM;
+      p.m0 = tm * B;
     }
-    p.n0 = tn * BN;
+    p.n0 = tn * B;
     return p;
   };
-  auto stages_of = [&](const Place& p) {
-    return KIND == kGrad ? (p.k1 - p.k0 + KT - 1) / KT : (g.K + KT - 1) / KT * PARTS;
+  // stages of one pass over K
+  auto pass_of = [&](const Place& p) QB_INLINE {
+    return KIND == kGrad ? (p.k1 - p.k0 + KT - 1) / KT : (g.K + KT - 1) / KT;
+  };
+  auto order = [&](int t) QB_INLINE {
+    const bool in_turn = KIND == kGrad && gridDim.x % 8 == 0;
+    return in_turn ? tile_in_turn<B == 256 ? 16 : 8>(t, tiles) : tile_at(t, int(gridDim.x), tiles);
   };
 
-  // The tile whose loads are issued next, the stage of it, and the numbers of
-  // the rows that this lane loads for it.
-  Place lp{};
-  int ls = 0, ln = 0, lat = int(blockIdx.x);
+  // --- the loads ---
+  // The tile whose loads are issued next; its stages: ls of ln in this pass over
+  // K, lpass of PARTS.
+  Place lp{}, np{};
+  int ls = 0, ln = 0, lpass = 0, lat = int(blockIdx.x), ltile = 0;
   bool more = false;
-  constexpr int A_ROWS = A_KS ? 1 : A_PW;
-  int a_row[A_ROWS], k_row[B_PW];
-  // lane's part in load u: of a KC operand row r and slot q, of a KS one row k and 8 columns from c
-  auto kc_r = [&](int u, int pw) { return ((wave * pw + u) * kWave + lane) >> 3; };
-  auto ks_k = [&](int u, int pw, int bx) { return ((wave * pw + u) * kWave + lane) / (bx / 8); };
-  auto ks_c = [&](int u, int pw, int bx) {
-    const int s = ((wave * pw + u) * kWave + lane) % (bx / 8);
-    return (((s >> 1) ^ key_k(ks_k(u, pw, bx), bx)) * 2 + (s & 1)) * 8;
+  int ctile = -1;  // the number of the tile that is multiplied, as ltile - 1 is of the one that is loaded
+  // lane's part in load u: of a KC operand row r, 8 values from q; of a KS one row k, 8 columns from c
+  auto kc_r = [&](int u) QB_INLINE { return ((wave * PW + u) * kWave + lane) >> 3; };
+  auto q_a = [&](int u) QB_INLINE { return ((lane & 7) ^ key_a(kc_r(u))) * 8; };
+  auto q_b = [&](int u) QB_INLINE { return ((lane & 7) ^ key_b(kc_r(u))) * 8; };
+  auto ks_k = [&](int u) QB_INLINE { return ((wave * PW + u) * kWave + lane) / (B / 8); };
+  auto ks_c = [&](int u) QB_INLINE {
+    const int s = ((wave * PW + u) * kWave + lane) % (B / 8);
+    return (((s >> 1) ^ key_k(ks_k(u))) * 2 + (s & 1)) * 8;
   };
-  auto load_rows = [&]() {  // of stage ls
-    if constexpr (!A_KS) {
-      if (ls == 0) {
+  auto times = [](int row, int64_t ld) QB_INLINE { return int64_t(uint64_t(uint32_t(row)) * uint32_t(ld)); };
+  // Each lane's offsets in bytes from the stage's bases.
+  const uint8_t *a_base = nullptr, *b_base = nullptr;
+  uint32_t a_off[DIRECT ? PW : 1], b_off[DIRECT ? PW : 1];
+  const uint8_t* s_base = nullptr;  // 4 bits: the exponents' of the operand whose this wave loads
+  uint32_t s_off[FOUR ? S_PW : 1];
+  int a_row[!DIRECT && !A_KS ? PW : 1], k_row[KIND == kGrad ? PW : 1];
+  auto wait_all = [&]() QB_INLINE {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(vm_count(0));
+    asm volatile("" ::: "memory");
+  };
+  // kRows: the numbers of tile p's rows, each wave those that it loads.
+  constexpr int RPW = B / W;
+  auto fetch_rows = [&](const Place& p, int tile) QB_INLINE {
+    const int row = p.m0 + wave * RPW + lane;
+    if (lane < RPW)
+      load_to_lds<4>(g.src + (row < p.m_end ? row : p.m_end - 1),
+                     reinterpret_cast<uint8_t*>(src_of + (tile & 7) * B + wave * RPW));
+  };
+  // kGrad: those of the stages from `stage`, as many as 64 numbers are for.
+  constexpr int KPW = KT / W, BATCH = 64 / KPW;
+  int* const batch_of = src_of + wave * 128;
+  auto fetch_batch = [&](int stage) QB_INLINE {
+    const int k = lp.k0 + (stage + lane / KPW) * KT + wave * KPW + lane % KPW;
+    load_to_lds<4>(g.src + (k < lp.k1 ? k : lp.k1 - 1), reinterpret_cast<uint8_t*>(batch_of + (stage / BATCH & 1) * 64));
+  };
+  // Where the first stage of a pass lies.
+  auto set_bases = [&]() QB_INLINE {
+    if constexpr (DIRECT) {
+      const uint16_t *a = g.A, *b = g.B;
+      if constexpr (!RAGGED) a += int64_t(lp.e) * g.mat_a;
+      if constexpr (KIND != kGrad) b += int64_t(lp.e) * g.mat_b;
+      if constexpr (PARTS > 1) {
+        a += ((PA >> lpass) & 1) * g.part_a;
+        b += ((PB >> lpass) & 1) * g.part_b;
+      }
+      if constexpr (A_KS)
+        a += times(lp.k0, g.lda) + lp.m0;
+      else if (!BY_ROW || !g.src)
+        a += times(lp.m0, g.lda);
+      if constexpr (!B_KS)
+        b += times(lp.n0, g.ldb);
+      else
+        b += (KIND == kGrad && g.src ? 0 : times(lp.k0, g.ldb)) + lp.n0;
+      a_base = same_for_all(a);
+      b_base = same_for_all(b);
+      if constexpr (FOUR)
+        s_base = same_for_all(wave < W / 2 ? g.As + times(lp.m0, g.sld)
+                                           : g.Bs + int64_t(lp.e) * g.mat_bs + times(lp.n0, g.sld));
+    }
+  };
+  // Rows and columns past a tile's end are the last ones again, for results
+  // that are not kept; rows that src routes nowhere are row 0, and their results
+  // are written as zeros.
+  auto set_offsets = [&]() QB_INLINE {
+    if constexpr (DIRECT) {
 #pragma unroll
-        for (int u = 0; u < A_PW; ++u) {
-          const int r = kc_r(u, A_PW), row = lp.m0 + r < lp.m_end ? lp.m0 + r : lp.m_end - 1;
-          a_row[u] = row;
+      for (int u = 0; u < PW; ++u) {
+        if constexpr (A_KS) {
+          const int c = ks_c(u), most = (g.M - 1 - lp.m0) & ~7;
+          a_off[u] = 2 * (uint32_t(ks_k(u)) * uint32_t(g.lda) + (c < most ? c : most));
+        } else {
+          const int r = kc_r(u);
+          int row = lp.m0 + r < lp.m_end ? r : lp.m_end - 1 - lp.m0;
+          if (BY_ROW && g.src) {
+            row = src_of[((ltile & 7) * B + r) & (8 * B - 1)];
+            row = uint32_t(row) < uint32_t(g.Mx) ? row : 0;
+          }
+          a_off[u] = 2 * (uint32_t(row) * uint32_t(g.lda) + q_a(u));
         }
-        if (KIND == kRows && !FOUR && g.src) {
-#pragma unroll
-          for (int u = 0; u < A_PW; ++u) a_row[u] = g.src[a_row[u]];
-          // waited for here, once a tile, and not before the loads of every stage
-#pragma unroll
-          for (int u = 0; u < A_PW; ++u) asm volatile("" : "+v"(a_row[u]));
+        if constexpr (B_KS) {
+          const int c = ks_c(u), most = (g.N - 1 - lp.n0) & ~7;
+          b_off[u] = 2 * ((KIND == kGrad && g.src ? 0 : uint32_t(ks_k(u)) * uint32_t(g.ldb)) + (c < most ? c : most));
+        } else {
+          const int r = kc_r(u), row = lp.n0 + r < g.N ? r : g.N - 1 - lp.n0;
+          b_off[u] = 2 * (uint32_t(row) * uint32_t(g.ldb) + q_b(u));
         }
       }
     }
-    if constexpr (KIND == kGrad) {
+  };
+  auto set_scales = [&]() QB_INLINE {
+    if constexpr (FOUR) {
 #pragma unroll
-      for (int u = 0; u < B_PW; ++u) {
-        const int row = lp.k0 + ls * KT + ks_k(u, B_PW, BN);
-        k_row[u] = row < lp.k1 ? row : lp.k1 - 1;
+      for (int j = 0; j < S_PW; ++j) {
+        int r = (wave * S_PW + j) * 32 % B + (lane >> 1);
+        const int most = (wave < W / 2 ? lp.m_end - lp.m0 : g.N - lp.n0) - 1;
+        r = r < most ? r : most;
+        s_off[j] = uint32_t(r) * uint32_t(g.sld) + (lane & 1) * 4;
       }
-      if (g.src) {
+    }
+  };
+  // The numbers of the rows that stage ls reads.
+  auto stage_rows = [&]() QB_INLINE {
+    if constexpr (!DIRECT && !A_KS) {
+      if (ls == 0) {
 #pragma unroll
-        for (int u = 0; u < B_PW; ++u) k_row[u] = g.src[k_row[u]];
+        for (int u = 0; u < PW; ++u) {
+          const int r = kc_r(u), row = lp.m0 + r < lp.m_end ? lp.m0 + r : lp.m_end - 1;
+          a_row[u] = BY_ROW && g.src ? g.src[row] : row;
+        }
+      }
+    }
+    if constexpr (!DIRECT && KIND == kGrad) {
+#pragma unroll
+      for (int u = 0; u < PW; ++u) {
+        const int row = lp.k0 + ls * KT + ks_k(u), in = row < lp.k1 ? row : lp.k1 - 1;
+        k_row[u] = g.src ? g.src[in] : in;
+      }
+    }
+    if constexpr (DIRECT && KIND == kGrad) {
+      // (a batch is fetched a batch before its first stage: older than that stage's loads by more than the ring)
+      if (g.src) {
+        if (ls > 0 && ls % BATCH == 0) fetch_batch(ls + BATCH);
+#pragma unroll
+        for (int u = 0; u < PW; ++u)
+          k_row[u] = batch_of[(ls / BATCH & 1) * 64 + ls % BATCH * KPW + ks_k(u) - wave * KPW];
       }
     }
   };
   // The next tile that has something to multiply; of the others (experts
   // without rows) the gradient is written as zeros.
-  auto advance = [&]() {
+  auto advance = [&]() QB_INLINE {
     more = false;
     for (; lat < tiles; lat += int(gridDim.x)) {
-      const bool in_turn = KIND == kGrad && gridDim.x % 8 == 0;
-      lp = place(in_turn ? tile_in_turn<BM == 256 ? 16 : 8>(lat, tiles) : tile_at(lat, int(gridDim.x), tiles));
-      ln = stages_of(lp);
+      lp = BY_ROW && DIRECT && ltile > 0 && g.src ? np : place(order(lat));
+      ln = pass_of(lp);
       if (ln > 0) {
         more = true;
         lat += int(gridDim.x);
         break;
       }
       if constexpr (KIND == kGrad)
-        zero_tile<BM, BN, W>(static_cast<float*>(g.out), (int64_t(lp.part) * g.G + lp.e) * g.M, lp.m0, g.M, lp.n0, g.N,
-                             tid);
+        zero_tile<B, B, W>(static_cast<float*>(g.out), (int64_t(lp.part) * g.G + lp.e) * g.M, lp.m0, g.M, lp.n0, g.N,
+                           tid);
     }
-    ls = 0;
-    if (more) load_rows();
-  };
-
-  // Where load u of the stage lies, and how many of its 8 values are inside.
-  auto a_at = [&](int u, int& n) -> const uint16_t* {
-    const uint16_t* base = g.A;
-    if constexpr (!RAGGED) base += int64_t(lp.e) * g.mat_a;
-    int k = ls * KT;
-    if constexpr (PARTS > 1) {
-      const int each = (g.K + KT - 1) / KT, p = ls / each;
-      k = (ls - p * each) * KT;
-      base += ((PA >> p) & 1) * g.part_a;
-    }
-    if constexpr (A_KS) {
-      const int kr = ks_k(u, A_PW, BM), c = lp.m0 + ks_c(u, A_PW, BM);
-      const int row = KIND == kGrad ? lp.k0 + k + kr : k + kr;
-      bool in = row < (KIND == kGrad ? lp.k1 : g.K);
-      if constexpr (KIND == kGrad) in = in && (!g.src || uint32_t(k_row[u < B_PW ? u : 0]) < uint32_t(g.Mx));
-      n = in ? g.M - c : 0;
-      return base + int64_t(uint64_t(uint32_t(row)) * uint32_t(g.lda)) + c;
-    } else {
-      const int r = kc_r(u, A_PW), q = (lane & 7) ^ key_a(r), row = a_row[u < A_ROWS ? u : 0];
-      const bool in = KIND != kRows || FOUR || !g.src || uint32_t(row) < uint32_t(g.Mx);
-      k += q * 8;
-      n = in ? g.K - k : 0;
-      return base + int64_t(uint64_t(uint32_t(row)) * uint32_t(g.lda)) + k;
-    }
-  };
-  auto b_at = [&](int u, int& n) -> const uint16_t* {
-    const uint16_t* base = g.B;
-    if constexpr (KIND != kGrad) base += int64_t(lp.e) * g.mat_b;
-    int k = ls * KT;
-    if constexpr (PARTS > 1) {
-      const int each = (g.K + KT - 1) / KT, p = ls / each;
-      k = (ls - p * each) * KT;
-      base += ((PB >> p) & 1) * g.part_b;
-    }
-    if constexpr (B_KS) {
-      const int kr = ks_k(u, B_PW, BN), c = lp.n0 + ks_c(u, B_PW, BN);
-      const int row = KIND == kGrad ? k_row[u] : k + kr;
-      const bool in = KIND == kGrad ? lp.k0 + k + kr < lp.k1 && (!g.src || uint32_t(row) < uint32_t(g.Mx)) : row < g.K;
-      n = in ? g.N - c : 0;
-      return base + int64_t(uint64_t(uint32_t(row)) * uint32_t(g.ldb)) + c;
-    } else {
-      const int r = kc_r(u, B_PW), q = (lane & 7) ^ key_b(r);
-      const int row = lp.n0 + r < g.N ? lp.n0 + r : g.N - 1;
-      k += q * 8;
-      n = g.K - k;
-      return base + int64_t(uint64_t(uint32_t(row)) * uint32_t(g.ldb)) + k;
-    }
-  };
-  constexpr int LOADS = A_PW + B_PW;
-  auto at = [&](int u, int& n) { return u < A_PW ? a_at(u < A_PW ? u : 0, n) : b_at(u < A_PW ? 0 : u - A_PW, n); };
-  auto slot = [&](int u, int st) {
-    return u < A_PW ? lds + st * A_BYTES + (wave * A_PW + u) * 1024 : lds_b + st * B_BYTES + (wave * B_PW + u - A_PW) * 1024;
-  };
-  uint4 held[DIRECT ? 1 : LOADS];
-  auto next_stage = [&]() {
-    if (++ls < ln)
-      load_rows();
-    else
-      advance();
-  };
-  auto issue = [&](int st) {
-#pragma unroll
-    for (int u = 0; u < LOADS; ++u) {
-      int n;
-      const uint16_t* p = at(u, n);
-      if constexpr (DIRECT) {
-        const uint8_t* q = n > 0 ? reinterpret_cast<const uint8_t*>(p) : reinterpret_cast<const uint8_t*>(&kZero16);
-        if constexpr (A_KS || B_KS)
-          load_to_lds(q, slot(u, st));
-        else
-          __builtin_amdgcn_global_load_lds((glb_vptr)q, (lds_vptr)slot(u, st), 16, 0, 0);
-      } else {
-        held[u] = ld_inside(p, n);
+    ls = lpass = 0;
+    if (!more) return;
+    if constexpr (BY_ROW && DIRECT) {
+      if (g.src) {
+        // the first tile's numbers are waited for; another's were fetched with the tile before it, and have landed
+        // with what that multiplied already unless it had less than a ring of stages
+        if (ltile == 0) fetch_rows(lp, 0);
+        if (ltile == 0 || ln < S + 1) wait_all();
       }
     }
+    if constexpr (KIND == kGrad && DIRECT) {
+      if (g.src) {
+        fetch_batch(0);
+        fetch_batch(BATCH);
+        wait_all();
+      }
+    }
+    set_bases();
+    set_offsets();
+    set_scales();
+    stage_rows();
+    if constexpr (BY_ROW && DIRECT) {
+      if (g.src && lat < tiles) {
+        np = place(order(lat));
+        fetch_rows(np, ltile + 1);
+      }
+    }
+    ++ltile;
+  };
+  auto next_stage = [&]() QB_INLINE {
+    if (++ls < ln) {
+      if constexpr (DIRECT) {
+        a_base += A_KS ? KT * 2 * g.lda : KT * 2;
+        b_base += B_KS ? (KIND == kGrad && g.src ? 0 : KT * 2 * g.ldb) : KT * 2;
+        if constexpr (FOUR) s_base += 8;
+      }
+      stage_rows();
+    } else if (lpass + 1 < PARTS) {
+      ls = 0;
+      ++lpass;
+      set_bases();
+    } else {
+      advance();
+    }
+  };
+
+  auto slot_a = [&](int u, int st) QB_INLINE { return lds + st * BYTES + (wave * PW + u) * 1024; };
+  auto slot_b = [&](int u, int st) QB_INLINE { return lds_b + st * BYTES + (wave * PW + u) * 1024; };
+  auto left_of_k = [&]() QB_INLINE { return (KIND == kGrad ? lp.k1 - lp.k0 : g.K) - ls * KT; };
+  // Whether stage ls is whole.
+  auto plain = [&]() QB_INLINE { return DIRECT && more && left_of_k() >= KT; };
+  // kGrad with src: both operands' rows by number, zeros for a row that was routed nowhere
+  auto issue_taken = [&](int u, int st, int left) QB_INLINE {
+    const uint8_t* const zero = reinterpret_cast<const uint8_t*>(&kZero16);
+    const int row = k_row[KIND == kGrad ? u : 0];
+    const bool in = ks_k(u) < left && uint32_t(row) < uint32_t(g.Mx);
+    load_to_lds<16>(in ? a_base + a_off[u] : zero, slot_a(u, st));
+    load_to_lds<16>(in ? b_base + 2 * times(row, g.ldb) + b_off[u] : zero, slot_b(u, st));
+  };
+  auto issue_plain = [&](int u, int st) QB_INLINE {
+    if (KIND == kGrad && DIRECT && g.src) {
+      issue_taken(u, st, KT);
+    } else if constexpr (DIRECT) {
+      load_to_lds<16>(a_base, a_off[u], slot_a(u, st));
+      load_to_lds<16>(b_base, b_off[u], slot_b(u, st));
+    }
+  };
+  auto issue_scales = [&](int st) QB_INLINE {
     if constexpr (FOUR) {
 #pragma unroll
-      for (int j = 0; j < S_PW; ++j) {
-        const int first = (wave * S_PW + j) % (ROWS / 32) * 32, r = first + (lane >> 1);
-        const uint8_t* p;
-        if (first < BM) {
-          const int row = lp.m0 + r < lp.m_end ? lp.m0 + r : lp.m_end - 1;
-          p = g.As + int64_t(row) * g.sld;
-        } else {
-          const int row = lp.n0 + r - BM < g.N ? lp.n0 + r - BM : g.N - 1;
-          p = g.Bs + int64_t(lp.e) * g.mat_bs + int64_t(row) * g.sld;
-        }
-        __builtin_amdgcn_global_load_lds((glb_vptr)(p + ls * 8 + (lane & 1) * 4),
-                                         (lds_vptr)(lds_s + st * S_BYTES + first * 8), 4, 0, 0);
-      }
+      for (int j = 0; j < S_PW; ++j)
+        load_to_lds<4>(s_base, s_off[j], lds_s + st * S_BYTES + (wave * S_PW + j) * 256);
     }
-    next_stage();
   };
-  auto put = [&](int st) {  // !DIRECT: what issue() read
-    if constexpr (!DIRECT) {
+  uint4 held[DIRECT ? 1 : 2 * PW];
+  int held_for = -1;  // !DIRECT: the stage of the ring that they are for
+  // Stage ls of the loading tile to place st of the ring, whatever it is.
+  auto issue = [&](int st) QB_INLINE {
+    const int left = left_of_k();
+    if constexpr (DIRECT) {
+      const uint8_t* const zero = reinterpret_cast<const uint8_t*>(&kZero16);
 #pragma unroll
-      for (int u = 0; u < LOADS; ++u) *reinterpret_cast<uint4*>(slot(u, st) + lane * 16) = held[u];
+      for (int u = 0; u < PW; ++u) {
+        if (KIND == kGrad && g.src) {
+          issue_taken(u, st, left);
+        } else {
+          load_to_lds<16>((A_KS ? ks_k(u) : q_a(u)) < left ? a_base + a_off[u] : zero, slot_a(u, st));
+          load_to_lds<16>((B_KS ? ks_k(u) : q_b(u)) < left ? b_base + b_off[u] : zero, slot_b(u, st));
+        }
+      }
+    } else {
+      const uint16_t *a = g.A, *b = g.B;
+      if constexpr (KIND != kGrad) b += int64_t(lp.e) * g.mat_b;
+      const int k = ls * KT;
+#pragma unroll
+      for (int u = 0; u < PW; ++u) {
+        if constexpr (A_KS) {
+          const int kr = ks_k(u), c = lp.m0 + ks_c(u);
+          bool in = kr < left;
+          if (KIND == kGrad && g.src) in = in && uint32_t(k_row[KIND == kGrad ? u : 0]) < uint32_t(g.Mx);
+          held[u] = ld_inside(a + times(lp.k0 + k + kr, g.lda) + c, in ? g.M - c : 0);
+        } else {
+          const int row = a_row[A_KS ? 0 : u], q = q_a(u);
+          const bool in = !BY_ROW || !g.src || uint32_t(row) < uint32_t(g.Mx);
+          held[u] = ld_inside(a + times(row, g.lda) + k + q, in ? left - q : 0);
+        }
+        if constexpr (B_KS) {
+          const int kr = ks_k(u), c = lp.n0 + ks_c(u), row = KIND == kGrad ? k_row[KIND == kGrad ? u : 0] : k + kr;
+          const bool in = kr < left && (KIND != kGrad || !g.src || uint32_t(row) < uint32_t(g.Mx));
+          held[PW + u] = ld_inside(b + times(row, g.ldb) + c, in ? g.N - c : 0);
+        } else {
+          const int r = kc_r(u), row = lp.n0 + r < g.N ? lp.n0 + r : g.N - 1, q = q_b(u);
+          held[PW + u] = ld_inside(b + times(row, g.ldb) + k + q, left - q);
+        }
+      }
+      held_for = st;
+    }
+    issue_scales(st);
+  };
+  auto put = [&]() QB_INLINE {  // !DIRECT: what issue() read
+    if constexpr (!DIRECT) {
+      if (held_for >= 0) {
+#pragma unroll
+        for (int u = 0; u < PW; ++u) {
+          *reinterpret_cast<uint4*>(slot_a(u, held_for) + lane * 16) = held[u];
+          *reinterpret_cast<uint4*>(slot_b(u, held_for) + lane * 16) = held[PW + u];
+        }
+      }
+      held_for = -1;
     }
   };
 
+  // --- the products ---
   v4f acc[TM][TN];
   const int r = lane & 15, g4 = lane >> 4;
-  // (4 bits: a lane's two halves are side by side, so that their exponents are)
-  constexpr int HALF = FOUR ? 16 : 64;
-  const int s4 = FOUR ? 2 * g4 : g4;
-  const int frag_a = A_KS ? (8 * g4 + (r >> 2)) * (BM * 2) + (((wm * TM) ^ key_k(8 * g4 + (r >> 2), BM)) * 32) + (r & 3) * 8
-                          : (wm * TM * 16 + r) * 128 + ((s4 ^ key_a(r)) * 16);
+  // The lane's 16 bytes of step 0 of row tile 0; step 1's lie 4 slots on.
+  const int frag_a = A_KS ? (8 * g4 + (r >> 2)) * (B * 2) + (((wm * TM) ^ key_k(8 * g4 + (r >> 2))) * 32) + (r & 3) * 8
+                          : (wm * TM * 16 + r) * 128 + ((g4 ^ key_a(r)) * 16);
   const int br = WIDE ? (r >> 2) * (4 * JT) + (r & 3) : r;  // KC: its row of column tile 0, and what tile j adds
   auto b_row = [](int j) { return WIDE ? j / JT * (16 * JT) + j % JT * 4 : j * 16; };
-  auto frag_b = [&](int j) {
-    if constexpr (B_KS) {
-      return ((8 * g4 + (r >> 2)) * (BN * 2) + (((wn * TN) ^ key_k(8 * g4 + (r >> 2), BN)) * 32) + (r & 3) * 8) ^ (j * 32);
-    } else {
-      const int row = br + b_row(j);
-      return (wn * TN * 16 + row) * 128 + ((s4 ^ key_b(row)) * 16);
-    }
-  };
-  // half h of the stage's K: 8 values of the lane's row or column
-  auto read_ks = [&](const uint8_t* p, int pitch, int h) {
+  // (B's rows of one lane have one number in the swizzle)
+  const int frag_b = B_KS ? (8 * g4 + (r >> 2)) * (B * 2) + (((wn * TN) ^ key_k(8 * g4 + (r >> 2))) * 32) + (r & 3) * 8
+                          : (wn * TN * 16 + br) * 128 + ((g4 ^ key_b(br)) * 16);
+  auto read_ks = [&](const uint8_t* p, int h) QB_INLINE {
     const auto q = (__attribute__((address_space(3))) uint8_t*)p;
-    const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(q + (32 * h) * pitch));
-    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(q + (32 * h + 4) * pitch));
+    const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(q + 32 * h * (B * 2)));
+    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(q + (32 * h + 4) * (B * 2)));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
-  auto read_a = [&](int st, int i, int h) -> v8s {
-    const uint8_t* p = lds + st * A_BYTES;
-    if constexpr (A_KS)
-      return read_ks(p + (frag_a ^ (i * 32)), BM * 2, h);
-    else
-      return *reinterpret_cast<const v8s*>(p + i * 16 * 128 + (frag_a ^ (h * HALF)));
-  };
-  auto read_b = [&](int st, int j, int h) -> v8s {
-    const uint8_t* p = lds_b + st * B_BYTES;
+  // a step's operands, and B's of two steps; their exponents
+  v8s a[TM], b[2][TN];
+  int as[FOUR ? TM : 1], bs[2][FOUR ? TN : 1];
+  // step h's part of column tile j, or of row tile i, of the stage in place st of the ring
+  auto read_b = [&](int j, int st, auto h) QB_INLINE {
+    constexpr int H = decltype(h)::value;
+    const uint8_t* p = lds_b + st * BYTES;
     if constexpr (B_KS)
-      return read_ks(p + frag_b(j), BN * 2, h);
+      b[H][j] = read_ks(p + (frag_b ^ (j * 32)), H);
     else
-      return *reinterpret_cast<const v8s*>(p + (frag_b(j) ^ (h * HALF)));
+      b[H][j] = *reinterpret_cast<const v8s*>(p + b_row(j) * 128 + (frag_b ^ (H * 64)));
+    if constexpr (FOUR) bs[H][j] = lds_s[st * S_BYTES + (B + wn * TN * 16 + br + b_row(j)) * 8 + g4 + 4 * H];
   };
-  // stage st's products, while the next loads go to stage `into` after the first row tile's
-  auto multiply = [&](int st, bool load, int into) {
-    int as[FOUR ? TM : 1], bs[FOUR ? TN : 1];  // two exponents each, one a half
+  auto read_a = [&](int i, int st, auto h) QB_INLINE {
+    constexpr int H = decltype(h)::value;
+    const uint8_t* p = lds + st * BYTES;
+    if constexpr (A_KS)
+      a[i] = read_ks(p + (frag_a ^ (i * 32)), H);
+    else
+      a[i] = *reinterpret_cast<const v8s*>(p + i * 16 * 128 + (frag_a ^ (H * 64)));
+    if constexpr (FOUR) as[i] = lds_s[st * S_BYTES + ((wm * TM + i) * 16 + r) * 8 + g4 + 4 * H];
+  };
+  auto multiply = [&](int i, auto h) QB_INLINE {
+    constexpr int H = decltype(h)::value;
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      if constexpr (FOUR)
+        acc[i][j] = mma4(b[H][j], a[i], acc[i][j], bs[H][j], as[i]);
+      else
+        acc[i][j] = mma16<T>(b[H][j], a[i], acc[i][j]);
+    }
     if constexpr (FOUR) {
-      const uint8_t* ss = lds_s + st * S_BYTES + g4 * 2;
+      // the products stay here: the compiler would gather a stage's behind its reads, out of registers
 #pragma unroll
-      for (int i = 0; i < TM; ++i) as[i] = *reinterpret_cast<const uint16_t*>(ss + ((wm * TM + i) * 16 + r) * 8);
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-        bs[j] = *reinterpret_cast<const uint16_t*>(ss + (BM + wn * TN * 16 + br + b_row(j)) * 8);
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      v8s b[TN], a[2];
-#pragma unroll
-      for (int j = 0; j < TN; ++j) b[j] = read_b(st, j, h);
-      a[0] = read_a(st, 0, h);
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        if (i + 1 < TM) a[(i + 1) & 1] = read_a(st, i + 1, h);
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-          if constexpr (FOUR)
-            acc[i][j] = mma4(b[j], a[i & 1], acc[i][j], bs[j], as[i], h);
-          else
-            acc[i][j] = mma16<T>(b[j], a[i & 1], acc[i][j]);
-        }
-        if (h == 0 && i == 0 && load) issue(into);
-      }
+      for (int j = 0; j < TN; ++j) asm volatile("" : "+v"(acc[i][j]));
     }
   };
+  constexpr std::integral_constant<int, 0> first{};
+  constexpr std::integral_constant<int, 1> second{};
 
   // element c of acc[i][j]: row 16 i + r, column 16 j + 4 g4 + c (WIDE: 4 JT g4 + 4 j + c of its JT column tiles)
   constexpr int STORES = TM * (WIDE ? TN / 2 : TN);
-  auto store_some = [&](const Place& p, auto whole) {
+  auto store_some = [&](const Place& p, auto whole) QB_INLINE {
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       const int row = p.m0 + (wm * TM + i) * 16 + r;
@@ -503,6 +653,11 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm16(const Gemm16 g) {
       } else if constexpr (KIND == kRows) {
         if (!whole() && row >= p.m_end) continue;
         uint16_t* o = static_cast<uint16_t*>(g.out) + int64_t(row) * g.N;
+        if (BY_ROW && DIRECT && g.src &&
+            uint32_t(src_of[((ctile & 7) * B + (wm * TM + i) * 16 + r) & (8 * B - 1)]) >= uint32_t(g.Mx)) {
+#pragma unroll
+          for (int j = 0; j < TN; ++j) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+        }
         if constexpr (WIDE) {
 #pragma unroll
           for (int h = 0; h < TN / 2; ++h) {  // 8 columns each
@@ -595,8 +750,8 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm16(const Gemm16 g) {
       }
     }
   };
-  auto store = [&](const Place& p) {
-    const bool whole = p.m0 + BM <= p.m_end && p.n0 + BN <= g.N;
+  auto store = [&](const Place& p) QB_INLINE {
+    const bool whole = p.m0 + B <= p.m_end && p.n0 + B <= g.N;
     if constexpr (RAGGED) {
       if (whole)
         store_some(p, std::true_type{});
@@ -609,80 +764,111 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm16(const Gemm16 g) {
     }
   };
 
-  // D stages ahead of the products; the loads of a wave are waited for in the
-  // order of their issue, and a barrier publishes every wave's.
-  constexpr int D = DIRECT ? S - 1 : 1;
-  // (kGrad's numbers of rows are loads too)
-  constexpr int PER = LOADS + S_PW, PER_SRC = LOADS + (KIND == kGrad ? B_PW : 0);
-  advance();
-  int ist = 0, ahead = 0;
+  // The loads of a wave are waited for in the order of their issue, and a
+  // barrier publishes every wave's.  `ahead`: stages issued and not multiplied yet,
+  // the current one among them; `behind`: that many stages more have loads that
+  // are older than the last tile's stores.
+  constexpr int PER = 2 * PW + S_PW;
+  int ahead = 0, behind = 0;
   // the multiplying cursor walks the same tiles as the loading one
   Place now{};
-  int cs = 0, cn = 0, cat = int(blockIdx.x);
-  auto begin = [&]() {
+  int cat = int(blockIdx.x);
+  auto begin = [&]() QB_INLINE {
     for (; cat < tiles; cat += int(gridDim.x)) {
-      const bool in_turn = KIND == kGrad && gridDim.x % 8 == 0;
-      now = place(in_turn ? tile_in_turn<BM == 256 ? 16 : 8>(cat, tiles) : tile_at(cat, int(gridDim.x), tiles));
-      cn = stages_of(now);
-      if (cn > 0) {
+      now = place(order(cat));
+      const int n = pass_of(now) * PARTS;
+      if (n > 0) {
         cat += int(gridDim.x);
-        cs = 0;
-        return true;
+        ++ctile;
+        return n;
       }
     }
-    return false;
+    return 0;
   };
-#pragma unroll
-  for (int d = 0; d < D; ++d) {
-    if (more) {
-      issue(ist);
-      put(ist);
-      ist = ist + 1 < S ? ist + 1 : 0;
-      ++ahead;
-    }
-  }
-  int st = 0;
-  bool behind = false;  // the last tile's stores are younger than the loads that are waited for
-  while (begin()) {
+  auto clear = [&]() QB_INLINE {
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
-    for (; cs < cn; ++cs) {
-      if constexpr (DIRECT && D > 1) {
-        if (ahead < D)
-          __builtin_amdgcn_s_waitcnt(vm_count(0));
-        else if (KIND == kGrad && g.src)
-          __builtin_amdgcn_s_waitcnt(vm_count(std::min(63, (D - 1) * PER_SRC)));
-        else
-          __builtin_amdgcn_s_waitcnt(vm_count(std::min(63, (D - 1) * PER)));
-      } else if (DIRECT && behind) {
-        __builtin_amdgcn_s_waitcnt(vm_count(std::min(63, STORES)));
-      } else if (DIRECT) {
-        __builtin_amdgcn_s_waitcnt(vm_count(0));
-      } else {
-        __builtin_amdgcn_s_waitcnt(0xC07F);  // LDS alone: the loads went through registers
-      }
-      behind = false;
-      asm volatile("" ::: "memory");
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-      if constexpr (KIND == kGrad && D == 1) {
-        // the numbers of rows that the next loads go by arrived with this stage: the compiler's wait for them belongs here
+  };
+  advance();
+#pragma unroll 1
+  for (int d = 0; d < S; ++d) {
+    if (!more) break;
+    issue(d);
+    put();
+    next_stage();
+    ++ahead;
+  }
+  int left = begin(), st = 0;
+  if (left > 0) {
+    asm volatile("" ::: "memory");
+    if constexpr (DIRECT)
+      wait_stages<S - 1, PER, 0>(ahead - 1);
+    else
+      __builtin_amdgcn_s_waitcnt(0xC07F);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 #pragma unroll
-        for (int u = 0; u < B_PW; ++u) asm volatile("" : "+v"(k_row[u]));
-      }
-      const bool load = more;
-      multiply(st, load, ist);
+    for (int j = 0; j < TN; ++j) read_b(j, 0, first);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) read_a(i, 0, first);
+    clear();
+  }
+  // the second step's products but for the first row's, the next stage's first reads and, if `load`, a stage's loads
+  auto second_step = [&](int next, bool load) QB_INLINE {
+    read_a(0, next, first);
+#pragma unroll
+    for (int i = 1; i < TM; ++i) {
       if (load) {
-        put(ist);
-        ist = ist + 1 < S ? ist + 1 : 0;
-      } else {
-        --ahead;
+#pragma unroll
+        for (int u = (i - 1) * PW / (TM - 1); u < i * PW / (TM - 1); ++u) issue_plain(u, st);
       }
-      st = st + 1 < S ? st + 1 : 0;
+#pragma unroll
+      for (int j = (i - 1) * TN / (TM - 1); j < i * TN / (TM - 1); ++j) read_b(j, next, first);
+      multiply(i, second);
+      read_a(i, next, first);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    behind = store(now);
+  };
+  while (left > 0) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+#pragma unroll
+      for (int j = i * TN / TM; j < (i + 1) * TN / TM; ++j) read_b(j, st, second);
+      multiply(i, first);
+      read_a(i, st, second);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    multiply(0, second);
+    put();  // (the place was read before the last barrier)
+    // this wave's reads of this stage, its loads of the next
+    asm volatile("" ::: "memory");
+    if constexpr (!DIRECT)
+      __builtin_amdgcn_s_waitcnt(0xC07F);
+    else if (behind > 0)
+      wait_stages<S - 2, PER, STORES>(ahead - 2);
+    else
+      wait_stages<S - 2, PER, 0>(ahead - 2);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    behind -= behind > 0;
+    // (behind the last stage the reads find an old one, which nothing multiplies)
+    const int next = st + 1 < S ? st + 1 : 0;
+    const bool load = plain();
+    if (!load && more) issue(st);
+    second_step(next, load);
+    if (load) issue_scales(st);
+    if (more)
+      next_stage();
+    else
+      --ahead;
+    st = next;
+    if (--left == 0) {
+      behind = store(now) ? S - 1 : 0;
+      left = begin();
+      clear();
+    }
   }
   __builtin_amdgcn_s_waitcnt(vm_count(0));  // no load may land after the LDS has changed hands
 }

@@ -77,13 +77,13 @@ __global__ __launch_bounds__(256) void k_ortho_scale(const float* __restrict__ x
 
 // ---------------------------------------------------------------------------
 
-template <int KIND, bool A_KS, bool B_KS, int PARTS, int PA, int PB, int B, int WM, int WN, int S>
+template <int KIND, bool A_KS, bool B_KS, int PARTS, int PA, int PB, int B, int S>
 static int tiled(Gemm16 g, int64_t tiles, hipStream_t st) {
   if (tiles > INT32_MAX) return int(hipErrorInvalidValue);
   g.tiles = int(tiles);
   const int64_t most = int64_t(device_cu_count()) * (B == 256 ? 1 : 2);
-  hipLaunchKernelGGL((k_gemm16<_Float16, KIND, A_KS, B_KS, B, B, WM, WN, S, true, PARTS, PA, PB>),
-                     dim3(unsigned(std::min(tiles, most))), dim3(WM * WN * kWave), 0, st, g);
+  hipLaunchKernelGGL((k_gemm16<_Float16, KIND, A_KS, B_KS, B, S, true, PARTS, PA, PB>),
+                     dim3(unsigned(std::min(tiles, most))), dim3(B == 256 ? 512 : 256), 0, st, g);
   return int(hipGetLastError());
 }
 
@@ -95,10 +95,10 @@ static int product(const Gemm16& g, hipStream_t st) {
     return g.G * (KIND == kStep ? tm * tn : tm * (tm + 1) / 2);
   };
   const int64_t t256 = tiles(256), t128 = tiles(128), t64 = tiles(64);
-  if (t64 <= 2 * cu) return tiled<KIND, A_KS, B_KS, PARTS, PA, PB, 64, 2, 2, 4>(g, t64, st);
+  if (t64 <= 2 * cu) return tiled<KIND, A_KS, B_KS, PARTS, PA, PB, 64, 4>(g, t64, st);
   const double rounds256 = double((t256 + cu - 1) / cu), rounds128 = double((t128 + 2 * cu - 1) / (2 * cu));
-  if (3.3 * rounds256 < 2 * rounds128) return tiled<KIND, A_KS, B_KS, PARTS, PA, PB, 256, 2, 4, 2>(g, t256, st);
-  return tiled<KIND, A_KS, B_KS, PARTS, PA, PB, 128, 2, 2, 2>(g, t128, st);
+  if (3.3 * rounds256 < 2 * rounds128) return tiled<KIND, A_KS, B_KS, PARTS, PA, PB, 256, 2>(g, t256, st);
+  return tiled<KIND, A_KS, B_KS, PARTS, PA, PB, 128, 2>(g, t128, st);
 }
 
 int launch_orthogonalize(const float* x, int G, int N, int C, int steps, float a, float b, float c, uint16_t* o,
