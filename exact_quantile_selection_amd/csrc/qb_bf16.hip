@@ -189,7 +189,10 @@ static int few(const Gemm16& g, hipStream_t st) {
   }
 }
 
+// Rows of 16-byte multiples at 16-byte addresses, within 32-bit offsets of their array's start where they are taken by
+// number.
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+static bool by_offset(const int32_t* src, int64_t Mx, int64_t C) { return !src || (Mx > 0 && Mx * C * 2 <= (int64_t(1) << 32)); }
 
 int launch_bf16_product(const uint16_t* x, int Mx, const int32_t* src, int M, const uint16_t* w, int N, int C,
                         const int32_t* off, int G, bool transposed, uint16_t* y, hipStream_t st) {
@@ -214,7 +217,7 @@ int launch_bf16_product(const uint16_t* x, int Mx, const int32_t* src, int M, co
   };
   const int64_t cu = device_cu_count();
   if (!transposed && rows <= 32 && (off || tiles(64) <= cu)) return rows <= 16 ? few<1>(g, st) : few<2>(g, st);
-  const bool direct = C % 8 == 0 && (!transposed || N % 8 == 0) && aligned16(x) && aligned16(w);
+  const bool direct = C % 8 == 0 && (!transposed || N % 8 == 0) && aligned16(x) && aligned16(w) && by_offset(src, Mx, C);
   const int64_t t256 = rows <= 128 && off ? 0 : tiles(256);
   const int64_t t64 = !off ? tiles(64) : tiles(64) * 2 / 3;
   const double uneven = off ? 0.1 : 0.0;
@@ -239,7 +242,7 @@ int launch_bf16_weight_grad(const uint16_t* dy, const uint16_t* x, int Mx, const
   g.splits = ws ? bf16_grad_splits(M, N, C, G) : 1;
   g.out = g.splits > 1 ? ws : dw;
   auto tiles = [&](int b) { return int64_t(G) * g.splits * ((N + b - 1) / b) * ((C + b - 1) / b); };
-  const bool direct = N % 8 == 0 && C % 8 == 0 && aligned16(dy) && aligned16(x);
+  const bool direct = N % 8 == 0 && C % 8 == 0 && aligned16(dy) && aligned16(x) && by_offset(src, Mx, C);
   if (int rc = gemm<kGrad, true, true>(g, tiles(256), tiles(128), tiles(64), off ? 0.25 : 0.0, direct, st)) return rc;
   if (g.splits > 1) {
     const int64_t n = int64_t(G) * N * C;

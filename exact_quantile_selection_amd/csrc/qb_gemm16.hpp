@@ -59,6 +59,7 @@ struct Gemm16 {
   int64_t part_a, part_b, mat_out, ldo, part_out;
   const uint16_t* add;       // what the result is added to (kSqr: S, kStep: X), in out's layout
   float by_sum, by_add;      // out = by_sum * sum + by_add * add
+  int add_parts, out_parts;  // parts of a value that are read there and written: 1 or 2
   // 4-bit operands: exponent bytes, 8 for each 128 bytes of a row (mat_bs: between B's matrices)
   const uint8_t *As, *Bs;
   int64_t sld, mat_bs;
@@ -179,26 +180,24 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
   constexpr int S_BYTES = FOUR ? 2 * B * 8 : 0;
   constexpr bool RAGGED = KIND == kRows || KIND == kGrad, SYM = KIND == kSym || KIND == kSqr;
   constexpr bool BY_ROW = KIND == kRows && !FOUR;  // A's rows may be numbered by src
-  constexpr bool WIDE = KIND == kRows && !B_KS;
-  constexpr int JT = TN < 4 ? TN : 4;  // WIDE: column tiles that share a stretch of 16 JT columns
   // a row's number in the swizzle of its slots
-  auto key_a = [](int row) { return (row >> 1) & 7; };
-  auto key_b = [](int row) { return WIDE ? ((row >> 1) & 1) | ((row >> (JT == 4 ? 3 : 2)) & 6) : (row >> 1) & 7; };
+  auto key_r = [](int row) { return (row >> 1) & 7; };
   auto key_k = [](int k) { return B >= 128 ? (k & 3) | ((k >> 1) & 4) : ((k >> 1) & 1) | ((k >> 2) & 2); };
   constexpr int RING = S * (2 * BYTES + S_BYTES);
   // numbers of rows: of the last 8 tiles' (kRows), of two batches of stages for each wave (kGrad)
   constexpr int SRC_BYTES = !DIRECT ? 0 : BY_ROW ? 8 * B * 4 : KIND == kGrad ? W * 512 : 0;
-  __shared__ __align__(1024) uint8_t lds[RING + SRC_BYTES + (RAGGED ? 1024 * 3 + 16 : 16)];
+  __shared__ __align__(1024) uint8_t lds[RING + SRC_BYTES + W * 256 + (RAGGED ? 1024 * 3 + 16 : 16)];
   uint8_t* const lds_b = lds + S * BYTES;
   uint8_t* const lds_s = lds + S * 2 * BYTES;
   int* const src_of = reinterpret_cast<int*>(lds + RING);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
+  int* const kept_of = reinterpret_cast<int*>(lds + RING + SRC_BYTES) + wave * 64;  // the last 8 tiles' places, a copy a wave
   const int tn_all = (g.N + B - 1) / B, tm_all = (g.M + B - 1) / B;
   int tiles = g.tiles;
 
   // the experts' first and last rows and their tiles of rows before each
-  int* const first_of = reinterpret_cast<int*>(lds + RING + SRC_BYTES);
+  int* const first_of = reinterpret_cast<int*>(lds + RING + SRC_BYTES + W * 256);
   int *const end_of = first_of + 256, *const before_of = end_of + 256;  // 256, 256 and 257 of them
   if (RAGGED && g.off) {
     if (wave == 0) {
@@ -294,8 +293,7 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
   int ctile = -1;  // the number of the tile that is multiplied, as ltile - 1 is of the one that is loaded
   // lane's part in load u: of a KC operand row r, 8 values from q; of a KS one row k, 8 columns from c
   auto kc_r = [&](int u) QB_INLINE { return ((wave * PW + u) * kWave + lane) >> 3; };
-  auto q_a = [&](int u) QB_INLINE { return ((lane & 7) ^ key_a(kc_r(u))) * 8; };
-  auto q_b = [&](int u) QB_INLINE { return ((lane & 7) ^ key_b(kc_r(u))) * 8; };
+  auto kc_q = [&](int u) QB_INLINE { return ((lane & 7) ^ key_r(kc_r(u))) * 8; };
   auto ks_k = [&](int u) QB_INLINE { return ((wave * PW + u) * kWave + lane) / (B / 8); };
   auto ks_c = [&](int u) QB_INLINE {
     const int s = ((wave * PW + u) * kWave + lane) % (B / 8);
@@ -308,6 +306,8 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
   const uint8_t* s_base = nullptr;  // 4 bits: the exponents' of the operand whose this wave loads
   uint32_t s_off[FOUR ? S_PW : 1];
   int a_row[!DIRECT && !A_KS ? PW : 1], k_row[KIND == kGrad ? PW : 1];
+  uint32_t k_off[KIND == kGrad && DIRECT ? PW : 1];  // kGrad with src: B's offsets of this stage's rows
+  bool some_out = false;                            // and whether one of the wave's rows was routed nowhere
   auto wait_all = [&]() QB_INLINE {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(vm_count(0));
@@ -370,14 +370,14 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
             row = src_of[((ltile & 7) * B + r) & (8 * B - 1)];
             row = uint32_t(row) < uint32_t(g.Mx) ? row : 0;
           }
-          a_off[u] = 2 * (uint32_t(row) * uint32_t(g.lda) + q_a(u));
+          a_off[u] = 2 * (uint32_t(row) * uint32_t(g.lda) + kc_q(u));
         }
         if constexpr (B_KS) {
           const int c = ks_c(u), most = (g.N - 1 - lp.n0) & ~7;
           b_off[u] = 2 * ((KIND == kGrad && g.src ? 0 : uint32_t(ks_k(u)) * uint32_t(g.ldb)) + (c < most ? c : most));
         } else {
           const int r = kc_r(u), row = lp.n0 + r < g.N ? r : g.N - 1 - lp.n0;
-          b_off[u] = 2 * (uint32_t(row) * uint32_t(g.ldb) + q_b(u));
+          b_off[u] = 2 * (uint32_t(row) * uint32_t(g.ldb) + kc_q(u));
         }
       }
     }
@@ -418,6 +418,13 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
 #pragma unroll
         for (int u = 0; u < PW; ++u)
           k_row[u] = batch_of[(ls / BATCH & 1) * 64 + ls % BATCH * KPW + ks_k(u) - wave * KPW];
+        bool out = false;
+#pragma unroll
+        for (int u = 0; u < PW; ++u) {
+          out = out || uint32_t(k_row[u]) >= uint32_t(g.Mx);
+          k_off[u] = uint32_t(k_row[u]) * uint32_t(2 * g.ldb) + b_off[u];
+        }
+        some_out = __ballot(out) != 0;
       }
     }
   };
@@ -454,6 +461,10 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
         wait_all();
       }
     }
+    if (lane == 0) {
+      int* kept = kept_of + (ltile & 7) * 8;
+      kept[0] = lp.m0, kept[1] = lp.m_end, kept[2] = lp.n0, kept[3] = lp.e, kept[4] = lp.part, kept[5] = ln * PARTS;
+    }
     set_bases();
     set_offsets();
     set_scales();
@@ -486,22 +497,24 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
   auto slot_a = [&](int u, int st) QB_INLINE { return lds + st * BYTES + (wave * PW + u) * 1024; };
   auto slot_b = [&](int u, int st) QB_INLINE { return lds_b + st * BYTES + (wave * PW + u) * 1024; };
   auto left_of_k = [&]() QB_INLINE { return (KIND == kGrad ? lp.k1 - lp.k0 : g.K) - ls * KT; };
-  // Whether stage ls is whole.
-  auto plain = [&]() QB_INLINE { return DIRECT && more && left_of_k() >= KT; };
+  // Whether stage ls is whole and (kGrad) all its rows are there.
+  auto plain = [&]() QB_INLINE { return DIRECT && more && left_of_k() >= KT && !(KIND == kGrad && some_out); };
   // kGrad with src: both operands' rows by number, zeros for a row that was routed nowhere
   auto issue_taken = [&](int u, int st, int left) QB_INLINE {
     const uint8_t* const zero = reinterpret_cast<const uint8_t*>(&kZero16);
     const int row = k_row[KIND == kGrad ? u : 0];
     const bool in = ks_k(u) < left && uint32_t(row) < uint32_t(g.Mx);
     load_to_lds<16>(in ? a_base + a_off[u] : zero, slot_a(u, st));
-    load_to_lds<16>(in ? b_base + 2 * times(row, g.ldb) + b_off[u] : zero, slot_b(u, st));
+    load_to_lds<16>(in ? b_base + k_off[KIND == kGrad ? u : 0] : zero, slot_b(u, st));
   };
-  auto issue_plain = [&](int u, int st) QB_INLINE {
-    if (KIND == kGrad && DIRECT && g.src) {
-      issue_taken(u, st, KT);
-    } else if constexpr (DIRECT) {
-      load_to_lds<16>(a_base, a_off[u], slot_a(u, st));
-      load_to_lds<16>(b_base, b_off[u], slot_b(u, st));
+  // one of a whole stage's loads, A's and B's in turn
+  auto issue_plain = [&](int v, int st) QB_INLINE {
+    if constexpr (DIRECT) {
+      const int u = v >> 1;
+      if (v & 1)
+        load_to_lds<16>(b_base, KIND == kGrad && g.src ? k_off[KIND == kGrad ? u : 0] : b_off[u], slot_b(u, st));
+      else
+        load_to_lds<16>(a_base, a_off[u], slot_a(u, st));
     }
   };
   auto issue_scales = [&](int st) QB_INLINE {
@@ -523,8 +536,8 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
         if (KIND == kGrad && g.src) {
           issue_taken(u, st, left);
         } else {
-          load_to_lds<16>((A_KS ? ks_k(u) : q_a(u)) < left ? a_base + a_off[u] : zero, slot_a(u, st));
-          load_to_lds<16>((B_KS ? ks_k(u) : q_b(u)) < left ? b_base + b_off[u] : zero, slot_b(u, st));
+          load_to_lds<16>((A_KS ? ks_k(u) : kc_q(u)) < left ? a_base + a_off[u] : zero, slot_a(u, st));
+          load_to_lds<16>((B_KS ? ks_k(u) : kc_q(u)) < left ? b_base + b_off[u] : zero, slot_b(u, st));
         }
       }
     } else {
@@ -539,7 +552,7 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
           if (KIND == kGrad && g.src) in = in && uint32_t(k_row[KIND == kGrad ? u : 0]) < uint32_t(g.Mx);
           held[u] = ld_inside(a + times(lp.k0 + k + kr, g.lda) + c, in ? g.M - c : 0);
         } else {
-          const int row = a_row[A_KS ? 0 : u], q = q_a(u);
+          const int row = a_row[A_KS ? 0 : u], q = kc_q(u);
           const bool in = !BY_ROW || !g.src || uint32_t(row) < uint32_t(g.Mx);
           held[u] = ld_inside(a + times(row, g.lda) + k + q, in ? left - q : 0);
         }
@@ -548,7 +561,7 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
           const bool in = kr < left && (KIND != kGrad || !g.src || uint32_t(row) < uint32_t(g.Mx));
           held[PW + u] = ld_inside(b + times(row, g.ldb) + c, in ? g.N - c : 0);
         } else {
-          const int r = kc_r(u), row = lp.n0 + r < g.N ? lp.n0 + r : g.N - 1, q = q_b(u);
+          const int r = kc_r(u), row = lp.n0 + r < g.N ? lp.n0 + r : g.N - 1, q = kc_q(u);
           held[PW + u] = ld_inside(b + times(row, g.ldb) + k + q, left - q);
         }
       }
@@ -574,12 +587,9 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
   const int r = lane & 15, g4 = lane >> 4;
   // The lane's 16 bytes of step 0 of row tile 0; step 1's lie 4 slots on.
   const int frag_a = A_KS ? (8 * g4 + (r >> 2)) * (B * 2) + (((wm * TM) ^ key_k(8 * g4 + (r >> 2))) * 32) + (r & 3) * 8
-                          : (wm * TM * 16 + r) * 128 + ((g4 ^ key_a(r)) * 16);
-  const int br = WIDE ? (r >> 2) * (4 * JT) + (r & 3) : r;  // KC: its row of column tile 0, and what tile j adds
-  auto b_row = [](int j) { return WIDE ? j / JT * (16 * JT) + j % JT * 4 : j * 16; };
-  // (B's rows of one lane have one number in the swizzle)
+                          : (wm * TM * 16 + r) * 128 + ((g4 ^ key_r(r)) * 16);
   const int frag_b = B_KS ? (8 * g4 + (r >> 2)) * (B * 2) + (((wn * TN) ^ key_k(8 * g4 + (r >> 2))) * 32) + (r & 3) * 8
-                          : (wn * TN * 16 + br) * 128 + ((g4 ^ key_b(br)) * 16);
+                          : (wn * TN * 16 + r) * 128 + ((g4 ^ key_r(r)) * 16);
   auto read_ks = [&](const uint8_t* p, int h) QB_INLINE {
     const auto q = (__attribute__((address_space(3))) uint8_t*)p;
     const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(q + 32 * h * (B * 2)));
@@ -596,8 +606,8 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
     if constexpr (B_KS)
       b[H][j] = read_ks(p + (frag_b ^ (j * 32)), H);
     else
-      b[H][j] = *reinterpret_cast<const v8s*>(p + b_row(j) * 128 + (frag_b ^ (H * 64)));
-    if constexpr (FOUR) bs[H][j] = lds_s[st * S_BYTES + (B + wn * TN * 16 + br + b_row(j)) * 8 + g4 + 4 * H];
+      b[H][j] = *reinterpret_cast<const v8s*>(p + j * 16 * 128 + (frag_b ^ (H * 64)));
+    if constexpr (FOUR) bs[H][j] = lds_s[st * S_BYTES + (B + (wn * TN + j) * 16 + r) * 8 + g4 + 4 * H];
   };
   auto read_a = [&](int i, int st, auto h) QB_INLINE {
     constexpr int H = decltype(h)::value;
@@ -626,8 +636,33 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
   constexpr std::integral_constant<int, 0> first{};
   constexpr std::integral_constant<int, 1> second{};
 
-  // element c of acc[i][j]: row 16 i + r, column 16 j + 4 g4 + c (WIDE: 4 JT g4 + 4 j + c of its JT column tiles)
-  constexpr int STORES = TM * (WIDE ? TN / 2 : TN);
+  // Element c of acc[i][j] is row 16 i + r, column 16 j + 4 g4 + c.  For 16-bit results the four lanes of a row
+  // exchange what they hold of JT column tiles, so that each has 4 JT columns side by side: of tile g4 (JT = 4), or half
+  // of tile g4 & 1 (JT = 2).
+  constexpr int JT = TN < 4 ? TN : 4;
+  auto exchange = [&](uint32_t(&w)[JT]) QB_INLINE {
+    auto swap32 = [](uint32_t& x, uint32_t& y) {
+      const auto t = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+      x = t[0], y = t[1];
+    };
+    auto swap16 = [](uint32_t& x, uint32_t& y) {
+      const auto t = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+      x = t[0], y = t[1];
+    };
+    if constexpr (JT == 4) {
+      swap32(w[0], w[2]);
+      swap32(w[1], w[3]);
+      swap16(w[0], w[1]);
+      swap16(w[2], w[3]);
+    } else {
+      swap16(w[0], w[1]);
+    }
+  };
+  // where the lane's stretch of 4 JT columns of column tiles from j begins
+  auto stretch = [&](const Place& p, int j) QB_INLINE {
+    return p.n0 + (wn * TN + j) * 16 + (JT == 4 ? g4 * 16 : (g4 & 1) * 16 + (g4 >> 1) * 8);
+  };
+  constexpr int STORES = KIND == kGrad ? TM * TN : TM * TN / 2;
   auto store_some = [&](const Place& p, auto whole) QB_INLINE {
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
@@ -651,21 +686,26 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
           }
         }
       } else if constexpr (KIND == kRows) {
-        if (!whole() && row >= p.m_end) continue;
+        const bool dead = BY_ROW && DIRECT && g.src &&
+                          uint32_t(src_of[((ctile & 7) * B + (wm * TM + i) * 16 + r) & (8 * B - 1)]) >= uint32_t(g.Mx);
         uint16_t* o = static_cast<uint16_t*>(g.out) + int64_t(row) * g.N;
-        if (BY_ROW && DIRECT && g.src &&
-            uint32_t(src_of[((ctile & 7) * B + (wm * TM + i) * 16 + r) & (8 * B - 1)]) >= uint32_t(g.Mx)) {
 #pragma unroll
-          for (int j = 0; j < TN; ++j) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
-        }
-        if constexpr (WIDE) {
+        for (int j0 = 0; j0 < TN; j0 += JT) {
+          uint32_t w[2][JT];
 #pragma unroll
-          for (int h = 0; h < TN / 2; ++h) {  // 8 columns each
-            const int col = p.n0 + (wn * TN + 2 * h / JT * JT) * 16 + g4 * (4 * JT) + 8 * (h % (JT / 2));
+          for (int k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int j = 0; j < JT; ++j) w[k][j] = bf16x2_rne(acc[i][j0 + j][2 * k], acc[i][j0 + j][2 * k + 1]);
+            exchange(w[k]);
+          }
+          if (!whole() && row >= p.m_end) continue;
+          const int col0 = stretch(p, j0);
+#pragma unroll
+          for (int h = 0; h < JT / 2; ++h) {  // 8 columns each
+            const int col = col0 + 8 * h;
             Half8 t;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              t.v[k] = bf16x2_rne(acc[i][2 * h + k / 2][2 * (k & 1)], acc[i][2 * h + k / 2][2 * (k & 1) + 1]);
+            for (int k = 0; k < 4; ++k) t.v[k] = dead ? 0 : w[k & 1][2 * h + (k >> 1)];
             if (whole() || col + 7 < g.N) {
               *reinterpret_cast<Half8*>(o + col) = t;
             } else {
@@ -674,76 +714,75 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
                 if (col + c < g.N) o[col + c] = uint16_t(t.v[c >> 1] >> (16 * (c & 1)));
             }
           }
-        } else {
-#pragma unroll
-          for (int j = 0; j < TN; ++j) {
-            const int col = p.n0 + (wn * TN + j) * 16 + g4 * 4;
-            Half4 t;
-            t.v[0] = bf16x2_rne(acc[i][j][0], acc[i][j][1]);
-            t.v[1] = bf16x2_rne(acc[i][j][2], acc[i][j][3]);
-            if (whole() || col + 3 < g.N) {
-              *reinterpret_cast<Half4*>(o + col) = t;
-            } else {
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                if (col + c < g.N) o[col + c] = uint16_t(t.v[c >> 1] >> (16 * (c & 1)));
-            }
-          }
         }
       } else {
         // rows of ldo values, a multiple of 8, of which those past N are kept zero
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-          const int col = p.n0 + (wn * TN + j) * 16 + g4 * 4;
-          const int64_t at0 = int64_t(p.e) * g.mat_out + int64_t(row) * g.ldo + col;
-          const bool here = row < g.M && col < g.ldo;
-          float v[4];
-          uint16_t hi[4], lo[4];
-          uint2 ah = make_uint2(0, 0), al = make_uint2(0, 0);
-          if (KIND != kSym && here) {
-            ah = *reinterpret_cast<const uint2*>(g.add + at0);
-            al = *reinterpret_cast<const uint2*>(g.add + at0 + g.part_out);
-          }
+        for (int j0 = 0; j0 < TN; j0 += JT) {
+          uint32_t w[4][JT];  // the lane's columns: w[c][x] is column 4 x + c of its stretch
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const uint32_t h2 = c < 2 ? ah.x : ah.y, l2 = c < 2 ? al.x : al.y;
-            v[c] = g.by_sum * acc[i][j][c];
-            if constexpr (KIND != kSym)
-              v[c] += g.by_add * joined16(uint16_t(h2 >> (16 * (c & 1))), uint16_t(l2 >> (16 * (c & 1))));
-            v[c] = row < g.M && col + c < g.N ? v[c] : 0.f;
-            split16(v[c], hi[c], lo[c]);
-          }
-          if (KIND == kStep && g.last) {
-            if (here) {
-              uint16_t* o = g.last + (int64_t(p.e) * g.M + row) * g.N + col;
-              const uint32_t x0 = bf16x2_rne(v[0] * g.by_last, v[1] * g.by_last),
-                             x1 = bf16x2_rne(v[2] * g.by_last, v[3] * g.by_last);
-              if (col + 3 < g.N) {
-                Half4 t;
-                t.v[0] = x0;
-                t.v[1] = x1;
-                *reinterpret_cast<Half4*>(o) = t;
-              } else {
-                for (int c = 0; c < 4; ++c)
-                  if (col + c < g.N) o[c] = uint16_t((c < 2 ? x0 : x1) >> (16 * (c & 1)));
-              }
-            }
-          } else {
-            uint16_t* o = static_cast<uint16_t*>(g.out);
-            if (here) {
-              *reinterpret_cast<uint2*>(o + at0) = make_uint2(hi[0] | uint32_t(hi[1]) << 16, hi[2] | uint32_t(hi[3]) << 16);
-              *reinterpret_cast<uint2*>(o + at0 + g.part_out) =
-                  make_uint2(lo[0] | uint32_t(lo[1]) << 16, lo[2] | uint32_t(lo[3]) << 16);
-            }
-            if (SYM && p.m0 != p.n0 && row < g.ldo) {
-              // the same value across the diagonal
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
-                if (col + c < g.N) {
-                  const int64_t at1 = int64_t(p.e) * g.mat_out + int64_t(col + c) * g.ldo + row;
-                  o[at1] = hi[c];
-                  o[at1 + g.part_out] = lo[c];
+            for (int j = 0; j < JT; ++j) {
+              const float e = acc[i][j0 + j][c];  // (a bit cast of the element itself would take the vector's first)
+              w[c][j] = __builtin_bit_cast(uint32_t, e);
+            }
+            exchange(w[c]);
+          }
+          const int col0 = stretch(p, j0);
+#pragma unroll
+          for (int h = 0; h < JT / 2; ++h) {  // 8 columns each
+            const int col = col0 + 8 * h;
+            const int64_t at0 = int64_t(p.e) * g.mat_out + int64_t(row) * g.ldo + col;
+            const bool here = row < g.M && col < g.ldo;
+            uint4 ah = make_uint4(0, 0, 0, 0), al = ah;
+            if (KIND != kSym && here) {
+              ah = *reinterpret_cast<const uint4*>(g.add + at0);
+              if (g.add_parts > 1) al = *reinterpret_cast<const uint4*>(g.add + at0 + g.part_out);
+            }
+            const uint32_t h4[4] = {ah.x, ah.y, ah.z, ah.w}, l4[4] = {al.x, al.y, al.z, al.w};
+            float v[8];
+            uint16_t hi[8], lo[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              v[c] = g.by_sum * __builtin_bit_cast(float, w[c & 3][2 * h + (c >> 2)]);
+              if constexpr (KIND != kSym)
+                v[c] += g.by_add * joined16(uint16_t(h4[c >> 1] >> (16 * (c & 1))), uint16_t(l4[c >> 1] >> (16 * (c & 1))));
+              v[c] = row < g.M && col + c < g.N ? v[c] : 0.f;
+              split16(v[c], hi[c], lo[c]);
+            }
+            auto two = [](const uint16_t(&x)[8], int k) { return x[2 * k] | uint32_t(x[2 * k + 1]) << 16; };
+            if (KIND == kStep && g.last) {
+              if (here) {
+                uint16_t* o = g.last + (int64_t(p.e) * g.M + row) * g.N + col;
+                Half8 t;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) t.v[k] = bf16x2_rne(v[2 * k] * g.by_last, v[2 * k + 1] * g.by_last);
+                if (col + 7 < g.N) {
+                  *reinterpret_cast<Half8*>(o) = t;
+                } else {
+#pragma unroll
+                  for (int c = 0; c < 8; ++c)
+                    if (col + c < g.N) o[c] = uint16_t(t.v[c >> 1] >> (16 * (c & 1)));
                 }
+              }
+            } else {
+              uint16_t* o = static_cast<uint16_t*>(g.out);
+              if (here) {
+                *reinterpret_cast<uint4*>(o + at0) = make_uint4(two(hi, 0), two(hi, 1), two(hi, 2), two(hi, 3));
+                if (g.out_parts > 1)
+                  *reinterpret_cast<uint4*>(o + at0 + g.part_out) = make_uint4(two(lo, 0), two(lo, 1), two(lo, 2), two(lo, 3));
+              }
+              if (SYM && p.m0 != p.n0 && row < g.ldo) {
+                // the same value across the diagonal
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                  if (col + c < g.N) {
+                    const int64_t at1 = int64_t(p.e) * g.mat_out + int64_t(col + c) * g.ldo + row;
+                    o[at1] = hi[c];
+                    if (g.out_parts > 1) o[at1 + g.part_out] = lo[c];
+                  }
+              }
             }
           }
         }
@@ -770,20 +809,14 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
   // are older than the last tile's stores.
   constexpr int PER = 2 * PW + S_PW;
   int ahead = 0, behind = 0;
-  // the multiplying cursor walks the same tiles as the loading one
+  // the tile that is multiplied: what was kept of it when its loads began
   Place now{};
-  int cat = int(blockIdx.x);
   auto begin = [&]() QB_INLINE {
-    for (; cat < tiles; cat += int(gridDim.x)) {
-      now = place(order(cat));
-      const int n = pass_of(now) * PARTS;
-      if (n > 0) {
-        cat += int(gridDim.x);
-        ++ctile;
-        return n;
-      }
-    }
-    return 0;
+    if (++ctile == ltile) return 0;
+    const int* kept = kept_of + (ctile & 7) * 8;
+    auto at = [&](int i) QB_INLINE { return __builtin_amdgcn_readfirstlane(kept[i]); };
+    now = Place{at(0), at(1), at(2), 0, 0, at(3), at(4)};
+    return at(5);
   };
   auto clear = [&]() QB_INLINE {
 #pragma unroll
@@ -822,7 +855,7 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
     for (int i = 1; i < TM; ++i) {
       if (load) {
 #pragma unroll
-        for (int u = (i - 1) * PW / (TM - 1); u < i * PW / (TM - 1); ++u) issue_plain(u, st);
+        for (int v = (i - 1) * 2 * PW / (TM - 1); v < i * 2 * PW / (TM - 1); ++v) issue_plain(v, st);
       }
 #pragma unroll
       for (int j = (i - 1) * TN / (TM - 1); j < i * TN / (TM - 1); ++j) read_b(j, next, first);
