@@ -184,8 +184,7 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
   auto key_r = [](int row) { return (row >> 1) & 7; };
   auto key_k = [](int k) { return B >= 128 ? (k & 3) | ((k >> 1) & 4) : ((k >> 1) & 1) | ((k >> 2) & 2); };
   constexpr int RING = S * (2 * BYTES + S_BYTES);
-  // numbers of rows: of the last 8 tiles' (kRows), of two batches of stages for each wave (kGrad)
-  constexpr int SRC_BYTES = !DIRECT ? 0 : BY_ROW ? 8 * B * 4 : KIND == kGrad ? W * 512 : 0;
+  constexpr int SRC_BYTES = BY_ROW && DIRECT ? 8 * B * 4 : 0;  // numbers of the last 8 tiles' rows
   __shared__ __align__(1024) uint8_t lds[RING + SRC_BYTES + W * 256 + (RAGGED ? 1024 * 3 + 16 : 16)];
   uint8_t* const lds_b = lds + S * BYTES;
   uint8_t* const lds_s = lds + S * 2 * BYTES;
@@ -321,13 +320,10 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
       load_to_lds<4>(g.src + (row < p.m_end ? row : p.m_end - 1),
                      reinterpret_cast<uint8_t*>(src_of + (tile & 7) * B + wave * RPW));
   };
-  // kGrad: those of the stages from `stage`, as many as 64 numbers are for.
-  constexpr int KPW = KT / W, BATCH = 64 / KPW;
-  int* const batch_of = src_of + wave * 128;
-  auto fetch_batch = [&](int stage) QB_INLINE {
-    const int k = lp.k0 + (stage + lane / KPW) * KT + wave * KPW + lane % KPW;
-    load_to_lds<4>(g.src + (k < lp.k1 ? k : lp.k1 - 1), reinterpret_cast<uint8_t*>(batch_of + (stage / BATCH & 1) * 64));
-  };
+  // kGrad: a stage's rows, of which each wave loads KPW that follow one another, and each of its loads RPL of them;
+  // their numbers are read into scalar registers (by a counter of their own: they keep no vector load waiting).
+  constexpr int KPW = KT / W, RPL = KPW / PW;
+  int rows[KIND == kGrad && DIRECT ? KPW : 1];
   // Where the first stage of a pass lies.
   auto set_bases = [&]() QB_INLINE {
     if constexpr (DIRECT) {
@@ -367,7 +363,7 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
           const int r = kc_r(u);
           int row = lp.m0 + r < lp.m_end ? r : lp.m_end - 1 - lp.m0;
           if (BY_ROW && g.src) {
-            row = src_of[((ltile & 7) * B + r) & (8 * B - 1)];
+            row = src_of[(((ltile - 1) & 7) * B + r) & (8 * B - 1)];
             row = uint32_t(row) < uint32_t(g.Mx) ? row : 0;
           }
           a_off[u] = 2 * (uint32_t(row) * uint32_t(g.lda) + kc_q(u));
@@ -412,15 +408,29 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
       }
     }
     if constexpr (DIRECT && KIND == kGrad) {
-      // (a batch is fetched a batch before its first stage: older than that stage's loads by more than the ring)
       if (g.src) {
-        if (ls > 0 && ls % BATCH == 0) fetch_batch(ls + BATCH);
+        const auto src = (const __attribute__((address_space(4))) int32_t*)g.src;
+        const int k = __builtin_amdgcn_readfirstlane(lp.k0 + ls * KT + wave * KPW);
+        if (k + KPW <= lp.k1) {
 #pragma unroll
-        for (int u = 0; u < PW; ++u)
-          k_row[u] = batch_of[(ls / BATCH & 1) * 64 + ls % BATCH * KPW + ks_k(u) - wave * KPW];
+          for (int i = 0; i < KPW; ++i) rows[i] = src[k + i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < KPW; ++i) rows[i] = src[std::min(k + i, lp.k1 - 1)];
+        }
+      }
+    }
+  };
+  // and, once those reads are back, where the rows lie
+  auto take_rows = [&]() QB_INLINE {
+    if constexpr (DIRECT && KIND == kGrad) {
+      if (g.src) {
         bool out = false;
 #pragma unroll
         for (int u = 0; u < PW; ++u) {
+          k_row[u] = rows[u * RPL];
+#pragma unroll
+          for (int i = 1; i < RPL; ++i) k_row[u] = lane / (kWave / RPL) == i ? rows[u * RPL + i] : k_row[u];
           out = out || uint32_t(k_row[u]) >= uint32_t(g.Mx);
           k_off[u] = uint32_t(k_row[u]) * uint32_t(2 * g.ldb) + b_off[u];
         }
@@ -454,15 +464,9 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
         if (ltile == 0 || ln < S + 1) wait_all();
       }
     }
-    if constexpr (KIND == kGrad && DIRECT) {
-      if (g.src) {
-        fetch_batch(0);
-        fetch_batch(BATCH);
-        wait_all();
-      }
-    }
+    ++ltile;
     if (lane == 0) {
-      int* kept = kept_of + (ltile & 7) * 8;
+      int* kept = kept_of + ((ltile - 1) & 7) * 8;
       kept[0] = lp.m0, kept[1] = lp.m_end, kept[2] = lp.n0, kept[3] = lp.e, kept[4] = lp.part, kept[5] = ln * PARTS;
     }
     set_bases();
@@ -472,10 +476,9 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
     if constexpr (BY_ROW && DIRECT) {
       if (g.src && lat < tiles) {
         np = place(order(lat));
-        fetch_rows(np, ltile + 1);
+        fetch_rows(np, ltile);
       }
     }
-    ++ltile;
   };
   auto next_stage = [&]() QB_INLINE {
     if (++ls < ln) {
@@ -828,6 +831,7 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
 #pragma unroll 1
   for (int d = 0; d < S; ++d) {
     if (!more) break;
+    take_rows();
     issue(d);
     put();
     next_stage();
@@ -886,6 +890,7 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     behind -= behind > 0;
+    take_rows();
     // (behind the last stage the reads find an old one, which nothing multiplies)
     const int next = st + 1 < S ? st + 1 : 0;
     const bool load = plain();
