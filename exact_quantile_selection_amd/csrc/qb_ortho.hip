@@ -15,13 +15,17 @@
 // to the rest (22 bits), times 2^12 for x and 2^8 for S and P (entries of x
 // below 16 and of S and P below 256 fit; with the usual polynomials they stay
 // below 1.3 and 3).  What a product reads of them was chosen by what it costs
-// the result (relative to |result|, random 512 x 1024, five steps; the result's
-// own rounding to bf16 is 1.7e-3): x in one part for S 4.6e-4, S in one part for
-// S S 2.3e-3, P in one part 1.0e-3, x in one part for P x 9e-4, x in one part
-// where it is added 1.4e-3.  So S S takes both parts of both (three passes: the
-// product of the low parts is below 2^-22), P x both of P, the sum both of x,
-// and S and P x one of x: 1.1e-3 in all.  bf16 in one part, as such steps are
-// often run, is 2.1e-2 off.
+// the result (simulated; relative to |result|, random 512 x 1024, five steps; the
+// result's own rounding to bf16 is 1.7e-3): x in one part for S 4.6e-4, S in one
+// part for S S 2.3e-3, P in one part 1.0e-3, x in one part for P x 9e-4, x in one
+// part where it is added 1.4e-3.  What the last two steps round weighs most (the
+// ones before are 6e-4 off with all of that but the last in one part).  So the
+// sum always takes both parts of x, S and P x one part of x; S S both parts of
+// both (three passes: the product of the low parts is below 2^-22) and P x both
+// of P, but for the first three steps of matrices of 256 rows and more (roundings
+// of smaller ones add up less evenly: 2e-3 and more so), unless they are among
+// the last two, which take one: 1.1e-3 in all.  bf16 in one part, as such steps
+// are often run, is 2.1e-2 off.
 #include "qb_gemm16.hpp"
 
 namespace qbk {
@@ -32,10 +36,22 @@ constexpr float kScaleX = 4096.f, kScaleS = 256.f;
 __global__ __launch_bounds__(256) void k_ortho_sums(const float* __restrict__ x, int64_t n, double* __restrict__ sums) {
   __shared__ double part[4];
   const float* p = x + int64_t(blockIdx.y) * n;
-  const int64_t each = (n + gridDim.x - 1) / gridDim.x, first = each * blockIdx.x;
+  const int64_t each = ((n + gridDim.x - 1) / gridDim.x + 3) / 4 * 4, first = each * blockIdx.x;
   const int64_t last = first + each < n ? first + each : n;
   double t = 0;
-  for (int64_t i = first + threadIdx.x; i < last; i += 256) t += double(p[i]) * double(p[i]);
+  constexpr int U = 4;
+  int64_t i = first + threadIdx.x * 4;
+  for (; i + (U - 1) * 1024 + 3 < last; i += U * 1024) {
+    Float4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = *reinterpret_cast<const Float4*>(p + i + u * 1024);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) t += double(v[u].v[c]) * double(v[u].v[c]);
+  }
+  for (; i < last; i += 1024)
+    for (int64_t k = i; k < i + 4 && k < last; ++k) t += double(p[k]) * double(p[k]);
 #pragma unroll
   for (int d = 1; d < kWave; d <<= 1) t += __shfl_xor(t, d);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = t;
@@ -58,15 +74,21 @@ __global__ __launch_bounds__(256) void k_ortho_scale(const float* __restrict__ x
   const int64_t row = i / per;
   const int col = int(i % per) * 8;
   const float* p = x + (g * N + row) * C + col;
+  float v[8];
+  if (col + 7 < C) {
+    const Float4 v0 = *reinterpret_cast<const Float4*>(p), v1 = *reinterpret_cast<const Float4*>(p + 4);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = v0.v[c], v[4 + c] = v1.v[c];
+  } else {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] = col + c < C ? p[c] : 0.f;
+  }
   uint32_t hi[4], lo[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     uint16_t h[2], l[2];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const float v = col + 2 * k + c < C ? float(double(p[2 * k + c]) * f) : 0.f;
-      split16(v, h[c], l[c]);
-    }
+    for (int c = 0; c < 2; ++c) split16(col + 2 * k + c < C ? float(double(v[2 * k + c]) * f) : 0.f, h[c], l[c]);
     hi[k] = h[0] | uint32_t(h[1]) << 16;
     lo[k] = l[0] | uint32_t(l[1]) << 16;
   }
@@ -109,8 +131,8 @@ int launch_orthogonalize(const float* x, int G, int N, int C, int steps, float a
   uint16_t *s = reinterpret_cast<uint16_t*>(ws + w.s), *p = reinterpret_cast<uint16_t*>(ws + w.p);
   const int64_t n = int64_t(N) * C, mat_x = N * w.ldx, mat_s = w.R * w.ldr;
   const int64_t part_x = G * mat_x, part_s = G * mat_s;
-  // a workgroup for 16,384 values, as many as a matrix has room for
-  const int sums_of = int(std::max<int64_t>(1, std::min<int64_t>(kOrthoSums, n / 16384)));
+  // a workgroup for 4096 values, as many as a matrix has room for
+  const int sums_of = int(std::max<int64_t>(1, std::min<int64_t>(kOrthoSums, n / 4096)));
   hipLaunchKernelGGL(k_ortho_sums, dim3(unsigned(sums_of), unsigned(G)), dim3(256), 0, st, x, n, sums);
   hipLaunchKernelGGL(k_ortho_scale, dim3(unsigned((N * (w.ldx / 8) + 255) / 256), unsigned(G)), dim3(256), 0, st, x, N, C,
                      w.ldx, sums_of, sums, part_x, xs[0]);
@@ -144,7 +166,9 @@ int launch_orthogonalize(const float* x, int G, int N, int C, int steps, float a
     g.out = p;
     g.by_sum = c / kScaleS;
     g.by_add = b;
-    rc = product<kSqr, false, false, 3, 0b100, 0b010>(g, st);
+    const bool rough = w.R >= 256 && i < 3 && i + 2 < steps;
+    g.out_parts = rough ? 1 : 2;
+    rc = rough ? product<kSqr, false, false, 1, 0, 0>(g, st) : product<kSqr, false, false, 3, 0b100, 0b010>(g, st);
     if (rc) return rc;
     // a x + P x, or a x + x P
     g.M = N;
@@ -157,6 +181,7 @@ int launch_orthogonalize(const float* x, int G, int N, int C, int steps, float a
     g.part_out = part_x;
     g.by_sum = 1.f / kScaleS;
     g.by_add = a;
+    g.out_parts = 2;
     g.last = i + 1 == steps ? o : nullptr;
     g.by_last = 1.f / kScaleX;
     if (w.tall) {
@@ -167,13 +192,13 @@ int launch_orthogonalize(const float* x, int G, int N, int C, int steps, float a
       g.ldb = w.ldr;
       g.mat_b = mat_s;
       g.part_b = part_s;
-      rc = product<kStep, false, false, 2, 0, 0b10>(g, st);
+      rc = rough ? product<kStep, false, false, 1, 0, 0>(g, st) : product<kStep, false, false, 2, 0, 0b10>(g, st);
     } else {
       g.A = p;
       g.B = now;
       g.ldb = w.ldx;
       g.mat_b = mat_x;
-      rc = product<kStep, false, true, 2, 0b10, 0>(g, st);
+      rc = rough ? product<kStep, false, true, 1, 0, 0>(g, st) : product<kStep, false, true, 2, 0b10, 0>(g, st);
     }
     if (rc) return rc;
   }

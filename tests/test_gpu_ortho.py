@@ -35,10 +35,12 @@ def formula(x, steps=5, poly=POLY, one=lambda t, s: t, two=lambda t, s: t):
         x = x / n
     tall = x.shape[0] > x.shape[1]
     x = two(x.T.contiguous() if tall else x, 4096.0)
-    for _ in range(steps):
+    for i in range(steps):
+        rough = min(x.shape) >= 256 and i < 3 and i + 2 < steps
         r = one(x, 4096.0)
         s = two(r @ r.T, 256.0)
-        p = two(b * s + c * (s @ s), 256.0)
+        q = one(s, 256.0) if rough else s
+        p = (one if rough else two)(b * s + c * (q @ q), 256.0)
         x = two(a * x + p @ r, 4096.0)
     return x.T if tall else x
 
