@@ -14,10 +14,16 @@ namespace qbk {
 // ---------------------------------------------------------------------------
 // the product of few rows
 
-// 16 values of K from p, of which n lie inside the row.
-__device__ __forceinline__ void ld_16(const uint16_t* p, int n, v8s (&v)[2]) {
-  v[0] = __builtin_bit_cast(v8s, ld_inside(p, n));
-  v[1] = __builtin_bit_cast(v8s, ld_inside(p + 8, n - 8));
+// 16 of a row's K values from `at`, in two parts (see ld_inside).
+template <bool SHORT, bool WHOLE>
+__device__ __forceinline__ void ld_16(const uint16_t* row, int at, int K, uint4 (&v)[2]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    v[h] = SHORT ? ld_short(row, at + 8 * h, K) : WHOLE ? ld_half8(row + at + 8 * h) : ld_inside(row, at + 8 * h, K);
+}
+template <bool SHORT>
+__device__ __forceinline__ v8s part_of(const uint4 (&v)[2], int h, int at, int K) {
+  return __builtin_bit_cast(v8s, SHORT ? v[h] : in_place(v[h], missing(at + 8 * h, K)));
 }
 
 // Bound by the weight's bytes: a workgroup of 8 waves takes 16 MT rows and
@@ -25,7 +31,7 @@ __device__ __forceinline__ void ld_16(const uint16_t* p, int n, v8s (&v)[2]) {
 // the whole weight is in flight at once, and join their sums through LDS in
 // order.  Both operands go from memory to registers: lane l takes 32
 // contiguous bytes of row l % 16, four lanes a line.
-template <int MT, int KW>
+template <int MT, int KW, bool SHORT>
 __global__ __launch_bounds__(512) void k_bf16_thin(const uint16_t* __restrict__ A, int Mx,
                                                    const int32_t* __restrict__ src, const uint16_t* __restrict__ Bm,
                                                    int64_t M, int N, int K, const int32_t* __restrict__ off, int G,
@@ -56,7 +62,7 @@ __global__ __launch_bounds__(512) void k_bf16_thin(const uint16_t* __restrict__ 
   const int KB = (K + 63) / 64;
   const int ncol = n0 + wn * 16;
   const int brow = ncol + r < N ? ncol + r : N - 1;
-  const uint16_t* bp = Bm + int64_t(brow) * K + g4 * 16;
+  const uint16_t* bp = Bm + int64_t(brow) * K;
   const uint16_t* ap[MT];
   bool live[MT];
 #pragma unroll
@@ -65,27 +71,35 @@ __global__ __launch_bounds__(512) void k_bf16_thin(const uint16_t* __restrict__ 
     row = row < m_end ? row : m_end - 1;
     if (src) row = src[row];
     live[i] = !src || (row >= 0 && row < Mx);
-    ap[i] = A + (live[i] ? row : 0) * K + g4 * 16;
+    ap[i] = A + (live[i] ? row : 0) * K;
   }
   v4f acc[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) acc[i] = (v4f){0.f, 0.f, 0.f, 0.f};
-  for (int kb = wk; kb < KB; kb += KW * U) {
-    v8s b[U][2], a[U][MT][2];
+  auto step = [&](int kb, auto whole) {
+    constexpr bool WHOLE = decltype(whole)::value;
+    uint4 b[U][2], a[U][MT][2];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = (kb + u * KW) * 64, n = K - g4 * 16 - k;  // (past the end: zeros)
-      ld_16(bp + k, n, b[u]);
+      const int at = (kb + u * KW) * 64 + g4 * 16;
+      ld_16<SHORT, WHOLE>(bp, at, K, b[u]);
 #pragma unroll
-      for (int i = 0; i < MT; ++i) ld_16(ap[i] + k, live[i] ? n : 0, a[u][i]);
+      for (int i = 0; i < MT; ++i) ld_16<SHORT, WHOLE>(ap[i], at, K, a[u][i]);
     }
+    __builtin_amdgcn_sched_barrier(0);  // (all of them before the first product)
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+      const int at = (kb + u * KW) * 64 + g4 * 16;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < MT; ++i) acc[i] = mma16<__bf16>(b[u][h], a[u][i][h], acc[i]);
-  }
+        for (int i = 0; i < MT; ++i)
+          acc[i] = mma16<__bf16>(part_of<SHORT || WHOLE>(b[u], h, at, K), part_of<SHORT || WHOLE>(a[u][i], h, at, K), acc[i]);
+    }
+  };
+  int kb = wk;
+  for (; (kb + (U - 1) * KW) * 64 + 64 <= K; kb += KW * U) step(kb, std::true_type{});
+  for (; kb < KB; kb += KW * U) step(kb, std::false_type{});  // (past the end: zeros)
   if constexpr (KW > 1) {
 #pragma unroll
     for (int i = 0; i < MT; ++i) *reinterpret_cast<v4f*>(&red[wave][i][lane][0]) = acc[i];
@@ -102,9 +116,9 @@ __global__ __launch_bounds__(512) void k_bf16_thin(const uint16_t* __restrict__ 
     const int col = ncol + g4 * 4;
     if (row >= m_end) continue;
     uint16_t* o = out + row * N + col;
-    Half4 t;
-    t.v[0] = bf16x2_rne(acc[i][0], acc[i][1]);
-    t.v[1] = bf16x2_rne(acc[i][2], acc[i][3]);
+    Half4 t;  // (a row that was routed nowhere was multiplied as row 0)
+    t.v[0] = live[i] ? bf16x2_rne(acc[i][0], acc[i][1]) : 0;
+    t.v[1] = live[i] ? bf16x2_rne(acc[i][2], acc[i][3]) : 0;
     if (col + 3 < N) {
       *reinterpret_cast<Half4*>(o) = t;
     } else {
@@ -170,8 +184,12 @@ static int thin(const Gemm16& g, int64_t row_tiles, hipStream_t st) {
   constexpr int BN = 16 * (8 / KW);
   const int64_t blocks = row_tiles * ((g.N + BN - 1) / BN);
   if (blocks > INT32_MAX) return int(hipErrorInvalidValue);
-  hipLaunchKernelGGL((k_bf16_thin<MT, KW>), dim3(unsigned(blocks)), dim3(512), 0, st, g.A, g.Mx, g.src, g.B, g.M, g.N, g.K,
-                     g.off, g.G, static_cast<uint16_t*>(g.out));
+  if (g.K >= 8)
+    hipLaunchKernelGGL((k_bf16_thin<MT, KW, false>), dim3(unsigned(blocks)), dim3(512), 0, st, g.A, g.Mx, g.src, g.B, g.M,
+                       g.N, g.K, g.off, g.G, static_cast<uint16_t*>(g.out));
+  else
+    hipLaunchKernelGGL((k_bf16_thin<MT, KW, true>), dim3(unsigned(blocks)), dim3(512), 0, st, g.A, g.Mx, g.src, g.B, g.M,
+                       g.N, g.K, g.off, g.G, static_cast<uint16_t*>(g.out));
   return int(hipGetLastError());
 }
 
@@ -197,7 +215,8 @@ static bool by_offset(const int32_t* src, int64_t Mx, int64_t C) { return !src |
 int launch_bf16_product(const uint16_t* x, int Mx, const int32_t* src, int M, const uint16_t* w, int N, int C,
                         const int32_t* off, int G, bool transposed, uint16_t* y, hipStream_t st) {
   Gemm16 g{};
-  g.A = x;
+  // (x without a row: every row is zeros, and something that may be read stands for them)
+  g.A = Mx > 0 ? x : w;
   g.B = w;
   g.lda = C;
   g.ldb = transposed ? N : C;
@@ -229,7 +248,7 @@ int launch_bf16_weight_grad(const uint16_t* dy, const uint16_t* x, int Mx, const
                             const int32_t* off, int G, float* dw, float* ws, hipStream_t st) {
   Gemm16 g{};
   g.A = dy;
-  g.B = x;
+  g.B = Mx > 0 ? x : reinterpret_cast<const uint16_t*>(dw);
   g.lda = N;
   g.ldb = C;
   g.M = N;

@@ -37,7 +37,7 @@ __device__ __forceinline__ uint32_t to_e2m1x4(float a, float b, float c, float d
 }
 
 // A wave takes 512 columns of U rows, 4 lanes a block.  Bound by its 2 bytes in.
-template <int U>
+template <int U, bool SHORT>
 __global__ __launch_bounds__(256) void k_fp4_quantize(const uint16_t* __restrict__ x, int64_t Mx,
                                                       const int32_t* __restrict__ row_src, int64_t M, int C, int64_t ld,
                                                       int64_t sld, uint8_t* __restrict__ xq, uint8_t* __restrict__ xs) {
@@ -45,6 +45,7 @@ __global__ __launch_bounds__(256) void k_fp4_quantize(const uint16_t* __restrict
   const int64_t r0 = (int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6)) * U;
   const int c0 = int(blockIdx.y) * 512 + lane * 8;
   uint4 v[U];
+  bool out[U];  // a row of zeros
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t r = r0 + u;
@@ -53,11 +54,14 @@ __global__ __launch_bounds__(256) void k_fp4_quantize(const uint16_t* __restrict
       src = row_src[r];
       if (src >= Mx) src = -1;
     }
-    v[u] = src >= 0 && c0 < C ? ld_inside(x + src * C + c0, C - c0) : make_uint4(0, 0, 0, 0);
+    const uint16_t* row = x + (src >= 0 ? src : 0) * C;
+    v[u] = SHORT ? ld_short(row, c0, src >= 0 ? C : 0) : ld_inside(row, c0, C);
+    out[u] = src < 0;
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t r = r0 + u;
+    if (!SHORT && (out[u] || c0 + 8 > C)) v[u] = in_place(v[u], out[u] ? 8 : missing(c0, C));
     const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
     uint32_t top = 0;
 #pragma unroll
@@ -87,10 +91,15 @@ int launch_fp4_quantize(const uint16_t* x, int64_t Mx, const int32_t* row_src, i
   // four rows a wave once that still gives every CU its waves
   const bool four = M * chunks >= 16 * 1024;
   const dim3 grid{unsigned(four ? (M + 15) / 16 : (M + 3) / 4), chunks, 1u};
-  if (four)
-    hipLaunchKernelGGL(k_fp4_quantize<4>, grid, dim3(256), 0, st, x, Mx, row_src, M, C, fp4_ld(C), fp4_sld(C), xq, xs);
+  if (C < 8 || Mx == 0)
+    hipLaunchKernelGGL((k_fp4_quantize<1, true>), dim3(unsigned((M + 3) / 4), chunks), dim3(256), 0, st, x, Mx, row_src, M,
+                       C, fp4_ld(C), fp4_sld(C), xq, xs);
+  else if (four)
+    hipLaunchKernelGGL((k_fp4_quantize<4, false>), grid, dim3(256), 0, st, x, Mx, row_src, M, C, fp4_ld(C), fp4_sld(C), xq,
+                       xs);
   else
-    hipLaunchKernelGGL(k_fp4_quantize<1>, grid, dim3(256), 0, st, x, Mx, row_src, M, C, fp4_ld(C), fp4_sld(C), xq, xs);
+    hipLaunchKernelGGL((k_fp4_quantize<1, false>), grid, dim3(256), 0, st, x, Mx, row_src, M, C, fp4_ld(C), fp4_sld(C), xq,
+                       xs);
   return int(hipGetLastError());
 }
 

@@ -100,20 +100,37 @@ __device__ __forceinline__ float joined16(uint16_t hi, uint16_t lo) {
   return float(__builtin_bit_cast(_Float16, hi)) + float(__builtin_bit_cast(_Float16, lo));
 }
 
-// 8 values from p of which n lie inside the operand, the others zero.
-__device__ __forceinline__ uint4 ld_inside(const uint16_t* p, int n) {
-  if (n >= 8) {
-    typedef uint32_t half8 __attribute__((ext_vector_type(4), aligned(2)));
-    const half8 t = *reinterpret_cast<const half8*>(p);
-    return make_uint4(t[0], t[1], t[2], t[3]);
-  }
-  uint32_t v[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = 2 * i < n ? p[2 * i] : 0, hi = 2 * i + 1 < n ? p[2 * i + 1] : 0;
-    v[i] = lo | (hi << 16);
-  }
-  return make_uint4(v[0], v[1], v[2], v[3]);
+// The 8 values from `at` of a row of `length` (8 at least), zeros past its end,
+// in two parts so that nothing waits between them: one load of 16 bytes, which
+// begins earlier where fewer than 8 values are left, and the shift that puts
+// those in their place, `missing` of them.
+__device__ __forceinline__ int missing(int at, int length) {
+  const int n = at + 8 - length;
+  return n < 0 ? 0 : n > 8 ? 8 : n;
+}
+__device__ __forceinline__ uint4 ld_half8(const void* p) {
+  typedef uint32_t half8 __attribute__((ext_vector_type(4), aligned(2)));
+  const half8 t = *(const __attribute__((address_space(1))) half8*)p;
+  return make_uint4(t[0], t[1], t[2], t[3]);
+}
+__device__ __forceinline__ uint4 ld_inside(const uint16_t* row, int at, int length) {
+  return ld_half8(row + (at < length - 8 ? at : length - 8));
+}
+__device__ __forceinline__ uint4 in_place(uint4 v, int missing) {
+  if (missing & 8) v = make_uint4(0, 0, 0, 0);
+  if (missing & 4) v = make_uint4(v.z, v.w, 0, 0);
+  if (missing & 2) v = make_uint4(v.y, v.z, v.w, 0);
+  if (missing & 1) v = make_uint4(v.x >> 16 | v.y << 16, v.y >> 16 | v.z << 16, v.z >> 16 | v.w << 16, v.w >> 16);
+  return v;
+}
+// The same value by value, for rows of fewer than 8.
+__device__ __forceinline__ uint4 ld_short(const uint16_t* from, int at, int length) {
+  const auto row = (const __attribute__((address_space(1))) uint16_t*)from;
+  auto two = [&](int i) {
+    const uint32_t lo = at + i < length ? row[at + i] : 0, hi = at + i + 1 < length ? row[at + i + 1] : 0;
+    return lo | hi << 16;
+  };
+  return make_uint4(two(0), two(2), two(4), two(6));
 }
 
 // 16 or 4 bytes a lane from memory to the LDS at `to` (the wave's), lane by
@@ -184,7 +201,7 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
   auto key_r = [](int row) { return (row >> 1) & 7; };
   auto key_k = [](int k) { return B >= 128 ? (k & 3) | ((k >> 1) & 4) : ((k >> 1) & 1) | ((k >> 2) & 2); };
   constexpr int RING = S * (2 * BYTES + S_BYTES);
-  constexpr int SRC_BYTES = BY_ROW && DIRECT ? 8 * B * 4 : 0;  // numbers of the last 8 tiles' rows
+  constexpr int SRC_BYTES = BY_ROW ? 8 * B * 4 : 0;  // numbers of the last 8 tiles' rows
   __shared__ __align__(1024) uint8_t lds[RING + SRC_BYTES + W * 256 + (RAGGED ? 1024 * 3 + 16 : 16)];
   uint8_t* const lds_b = lds + S * BYTES;
   uint8_t* const lds_s = lds + S * 2 * BYTES;
@@ -301,11 +318,13 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
   auto times = [](int row, int64_t ld) QB_INLINE { return int64_t(uint64_t(uint32_t(row)) * uint32_t(ld)); };
   // Each lane's offsets in bytes from the stage's bases.
   const uint8_t *a_base = nullptr, *b_base = nullptr;
-  uint32_t a_off[DIRECT ? PW : 1], b_off[DIRECT ? PW : 1];
+  uint32_t a_off[PW], b_off[PW];
   const uint8_t* s_base = nullptr;  // 4 bits: the exponents' of the operand whose this wave loads
   uint32_t s_off[FOUR ? S_PW : 1];
-  int a_row[!DIRECT && !A_KS ? PW : 1], k_row[KIND == kGrad ? PW : 1];
-  uint32_t k_off[KIND == kGrad && DIRECT ? PW : 1];  // kGrad with src: B's offsets of this stage's rows
+  int a_row[BY_ROW && !DIRECT ? PW : 1];    // !DIRECT: A's rows, which may lie beyond 32 bits of their base
+  uint32_t off_end = 0;                     // !DIRECT: how many of a load's columns lie past their rows' end, 4 bits each
+  int k_row[KIND == kGrad ? PW : 1];
+  uint32_t k_off[KIND == kGrad ? PW : 1];  // kGrad with src: B's offsets of this stage's rows
   bool some_out = false;                            // and whether one of the wave's rows was routed nowhere
   auto wait_all = [&]() QB_INLINE {
     asm volatile("" ::: "memory");
@@ -323,58 +342,61 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
   // kGrad: a stage's rows, of which each wave loads KPW that follow one another, and each of its loads RPL of them;
   // their numbers are read into scalar registers (by a counter of their own: they keep no vector load waiting).
   constexpr int KPW = KT / W, RPL = KPW / PW;
-  int rows[KIND == kGrad && DIRECT ? KPW : 1];
+  int rows[KIND == kGrad ? KPW : 1];
   // Where the first stage of a pass lies.
   auto set_bases = [&]() QB_INLINE {
-    if constexpr (DIRECT) {
-      const uint16_t *a = g.A, *b = g.B;
-      if constexpr (!RAGGED) a += int64_t(lp.e) * g.mat_a;
-      if constexpr (KIND != kGrad) b += int64_t(lp.e) * g.mat_b;
-      if constexpr (PARTS > 1) {
-        a += ((PA >> lpass) & 1) * g.part_a;
-        b += ((PB >> lpass) & 1) * g.part_b;
-      }
-      if constexpr (A_KS)
-        a += times(lp.k0, g.lda) + lp.m0;
-      else if (!BY_ROW || !g.src)
-        a += times(lp.m0, g.lda);
-      if constexpr (!B_KS)
-        b += times(lp.n0, g.ldb);
-      else
-        b += (KIND == kGrad && g.src ? 0 : times(lp.k0, g.ldb)) + lp.n0;
-      a_base = same_for_all(a);
-      b_base = same_for_all(b);
-      if constexpr (FOUR)
-        s_base = same_for_all(wave < W / 2 ? g.As + times(lp.m0, g.sld)
-                                           : g.Bs + int64_t(lp.e) * g.mat_bs + times(lp.n0, g.sld));
+    const uint16_t *a = g.A, *b = g.B;
+    if constexpr (!RAGGED) a += int64_t(lp.e) * g.mat_a;
+    if constexpr (KIND != kGrad) b += int64_t(lp.e) * g.mat_b;
+    if constexpr (PARTS > 1) {
+      a += ((PA >> lpass) & 1) * g.part_a;
+      b += ((PB >> lpass) & 1) * g.part_b;
     }
+    if constexpr (A_KS)
+      a += times(lp.k0, g.lda);
+    else if (!BY_ROW || !g.src)
+      a += times(lp.m0, g.lda);
+    if constexpr (!B_KS)
+      b += times(lp.n0, g.ldb);
+    else if (KIND != kGrad || !g.src)
+      b += times(lp.k0, g.ldb);
+    a_base = same_for_all(a);
+    b_base = same_for_all(b);
+    if constexpr (FOUR)
+      s_base = same_for_all(wave < W / 2 ? g.As + times(lp.m0, g.sld)
+                                         : g.Bs + int64_t(lp.e) * g.mat_bs + times(lp.n0, g.sld));
   };
   // Rows and columns past a tile's end are the last ones again, for results
   // that are not kept; rows that src routes nowhere are row 0, and their results
   // are written as zeros.
   auto set_offsets = [&]() QB_INLINE {
-    if constexpr (DIRECT) {
+    off_end = 0;
 #pragma unroll
-      for (int u = 0; u < PW; ++u) {
-        if constexpr (A_KS) {
-          const int c = ks_c(u), most = (g.M - 1 - lp.m0) & ~7;
-          a_off[u] = 2 * (uint32_t(ks_k(u)) * uint32_t(g.lda) + (c < most ? c : most));
-        } else {
-          const int r = kc_r(u);
-          int row = lp.m0 + r < lp.m_end ? r : lp.m_end - 1 - lp.m0;
-          if (BY_ROW && g.src) {
-            row = src_of[(((ltile - 1) & 7) * B + r) & (8 * B - 1)];
-            row = uint32_t(row) < uint32_t(g.Mx) ? row : 0;
-          }
-          a_off[u] = 2 * (uint32_t(row) * uint32_t(g.lda) + kc_q(u));
+    for (int u = 0; u < PW; ++u) {
+      // a column, the last 8 of a row at most (DIRECT: rows are multiples of 8)
+      auto column = [&](int c, int length, int load) QB_INLINE {
+        const int most = DIRECT ? (length - 1) & ~7 : length < 8 ? 0 : length - 8;
+        if (!DIRECT) off_end |= uint32_t(missing(c, length)) << (4 * load);
+        return c < most ? c : most;
+      };
+      if constexpr (A_KS) {
+        a_off[u] = 2 * (uint32_t(ks_k(u)) * uint32_t(g.lda) + column(lp.m0 + ks_c(u), g.M, u));
+      } else {
+        const int r = kc_r(u);
+        int row = lp.m0 + r < lp.m_end ? r : lp.m_end - 1 - lp.m0;
+        if (BY_ROW && g.src) {
+          row = src_of[(((ltile - 1) & 7) * B + r) & (8 * B - 1)];
+          row = uint32_t(row) < uint32_t(g.Mx) ? row : 0;
         }
-        if constexpr (B_KS) {
-          const int c = ks_c(u), most = (g.N - 1 - lp.n0) & ~7;
-          b_off[u] = 2 * ((KIND == kGrad && g.src ? 0 : uint32_t(ks_k(u)) * uint32_t(g.ldb)) + (c < most ? c : most));
-        } else {
-          const int r = kc_r(u), row = lp.n0 + r < g.N ? r : g.N - 1 - lp.n0;
-          b_off[u] = 2 * (uint32_t(row) * uint32_t(g.ldb) + kc_q(u));
-        }
+        if constexpr (BY_ROW && !DIRECT) a_row[u] = row;
+        a_off[u] = 2 * ((BY_ROW && !DIRECT ? 0 : uint32_t(row) * uint32_t(g.lda)) + kc_q(u));
+      }
+      if constexpr (B_KS) {
+        b_off[u] = 2 * ((KIND == kGrad && g.src ? 0 : uint32_t(ks_k(u)) * uint32_t(g.ldb)) +
+                        column(lp.n0 + ks_c(u), g.N, PW + u));
+      } else {
+        const int r = kc_r(u), row = lp.n0 + r < g.N ? r : g.N - 1 - lp.n0;
+        b_off[u] = 2 * (uint32_t(row) * uint32_t(g.ldb) + kc_q(u));
       }
     }
   };
@@ -391,23 +413,7 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
   };
   // The numbers of the rows that stage ls reads.
   auto stage_rows = [&]() QB_INLINE {
-    if constexpr (!DIRECT && !A_KS) {
-      if (ls == 0) {
-#pragma unroll
-        for (int u = 0; u < PW; ++u) {
-          const int r = kc_r(u), row = lp.m0 + r < lp.m_end ? lp.m0 + r : lp.m_end - 1;
-          a_row[u] = BY_ROW && g.src ? g.src[row] : row;
-        }
-      }
-    }
-    if constexpr (!DIRECT && KIND == kGrad) {
-#pragma unroll
-      for (int u = 0; u < PW; ++u) {
-        const int row = lp.k0 + ls * KT + ks_k(u), in = row < lp.k1 ? row : lp.k1 - 1;
-        k_row[u] = g.src ? g.src[in] : in;
-      }
-    }
-    if constexpr (DIRECT && KIND == kGrad) {
+    if constexpr (KIND == kGrad) {
       if (g.src) {
         const auto src = (const __attribute__((address_space(4))) int32_t*)g.src;
         const int k = __builtin_amdgcn_readfirstlane(lp.k0 + ls * KT + wave * KPW);
@@ -423,7 +429,7 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
   };
   // and, once those reads are back, where the rows lie
   auto take_rows = [&]() QB_INLINE {
-    if constexpr (DIRECT && KIND == kGrad) {
+    if constexpr (KIND == kGrad) {
       if (g.src) {
         bool out = false;
 #pragma unroll
@@ -443,7 +449,7 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
   auto advance = [&]() QB_INLINE {
     more = false;
     for (; lat < tiles; lat += int(gridDim.x)) {
-      lp = BY_ROW && DIRECT && ltile > 0 && g.src ? np : place(order(lat));
+      lp = BY_ROW && ltile > 0 && g.src ? np : place(order(lat));
       ln = pass_of(lp);
       if (ln > 0) {
         more = true;
@@ -456,7 +462,7 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
     }
     ls = lpass = 0;
     if (!more) return;
-    if constexpr (BY_ROW && DIRECT) {
+    if constexpr (BY_ROW) {
       if (g.src) {
         // the first tile's numbers are waited for; another's were fetched with the tile before it, and have landed
         // with what that multiplied already unless it had less than a ring of stages
@@ -473,7 +479,7 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
     set_offsets();
     set_scales();
     stage_rows();
-    if constexpr (BY_ROW && DIRECT) {
+    if constexpr (BY_ROW) {
       if (g.src && lat < tiles) {
         np = place(order(lat));
         fetch_rows(np, ltile);
@@ -482,11 +488,9 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
   };
   auto next_stage = [&]() QB_INLINE {
     if (++ls < ln) {
-      if constexpr (DIRECT) {
-        a_base += A_KS ? KT * 2 * g.lda : KT * 2;
-        b_base += B_KS ? (KIND == kGrad && g.src ? 0 : KT * 2 * g.ldb) : KT * 2;
-        if constexpr (FOUR) s_base += 8;
-      }
+      a_base += A_KS ? KT * 2 * g.lda : KT * 2;
+      b_base += B_KS ? (KIND == kGrad && g.src ? 0 : KT * 2 * g.ldb) : KT * 2;
+      if constexpr (FOUR) s_base += 8;
       stage_rows();
     } else if (lpass + 1 < PARTS) {
       ls = 0;
@@ -501,23 +505,32 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
   auto slot_b = [&](int u, int st) QB_INLINE { return lds_b + st * BYTES + (wave * PW + u) * 1024; };
   auto left_of_k = [&]() QB_INLINE { return (KIND == kGrad ? lp.k1 - lp.k0 : g.K) - ls * KT; };
   // Whether stage ls is whole and (kGrad) all its rows are there.
-  auto plain = [&]() QB_INLINE { return DIRECT && more && left_of_k() >= KT && !(KIND == kGrad && some_out); };
-  // kGrad with src: both operands' rows by number, zeros for a row that was routed nowhere
-  auto issue_taken = [&](int u, int st, int left) QB_INLINE {
-    const uint8_t* const zero = reinterpret_cast<const uint8_t*>(&kZero16);
-    const int row = k_row[KIND == kGrad ? u : 0];
-    const bool in = ks_k(u) < left && uint32_t(row) < uint32_t(g.Mx);
-    load_to_lds<16>(in ? a_base + a_off[u] : zero, slot_a(u, st));
-    load_to_lds<16>(in ? b_base + k_off[KIND == kGrad ? u : 0] : zero, slot_b(u, st));
+  auto plain = [&]() QB_INLINE {
+    return more && left_of_k() >= KT && !(KIND == kGrad && some_out) && (DIRECT || (g.lda >= 8 && g.ldb >= 8));
+  };
+  // !DIRECT: what a stage's loads read, and how many values of each are missing, 4 bits each
+  uint4 held[DIRECT ? 1 : 2 * PW];
+  uint32_t held_missing = 0;
+  int held_for = -1;  // the place in the ring that they are for
+  auto a_row_at = [&](int u) QB_INLINE { return BY_ROW && !DIRECT ? 2 * times(a_row[BY_ROW && !DIRECT ? u : 0], g.lda) : 0; };
+  auto b_row_at = [&](int u) QB_INLINE {
+    return KIND == kGrad && g.src ? 2 * times(k_row[KIND == kGrad ? u : 0], g.ldb) : 0;
   };
   // one of a whole stage's loads, A's and B's in turn
   auto issue_plain = [&](int v, int st) QB_INLINE {
+    const int u = v >> 1;
     if constexpr (DIRECT) {
-      const int u = v >> 1;
       if (v & 1)
         load_to_lds<16>(b_base, KIND == kGrad && g.src ? k_off[KIND == kGrad ? u : 0] : b_off[u], slot_b(u, st));
       else
         load_to_lds<16>(a_base, a_off[u], slot_a(u, st));
+    } else {
+      if (v & 1)
+        held[PW + u] = ld_half8(b_base + b_row_at(u) + b_off[u]);
+      else
+        held[u] = ld_half8(a_base + a_row_at(u) + a_off[u]);
+      held_missing = off_end;
+      held_for = st;
     }
   };
   auto issue_scales = [&](int st) QB_INLINE {
@@ -527,54 +540,50 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
         load_to_lds<4>(s_base, s_off[j], lds_s + st * S_BYTES + (wave * S_PW + j) * 256);
     }
   };
-  uint4 held[DIRECT ? 1 : 2 * PW];
-  int held_for = -1;  // !DIRECT: the stage of the ring that they are for
-  // Stage ls of the loading tile to place st of the ring, whatever it is.
+  // Stage ls of the loading tile to place st of the ring, whatever it is: zeros past the end of K, and for kGrad in both
+  // operands' rows that src routes nowhere.
   auto issue = [&](int st) QB_INLINE {
     const int left = left_of_k();
-    if constexpr (DIRECT) {
-      const uint8_t* const zero = reinterpret_cast<const uint8_t*>(&kZero16);
+    held_missing = off_end;
+    held_for = st;
 #pragma unroll
-      for (int u = 0; u < PW; ++u) {
-        if (KIND == kGrad && g.src) {
-          issue_taken(u, st, left);
-        } else {
-          load_to_lds<16>((A_KS ? ks_k(u) : kc_q(u)) < left ? a_base + a_off[u] : zero, slot_a(u, st));
-          load_to_lds<16>((B_KS ? ks_k(u) : kc_q(u)) < left ? b_base + b_off[u] : zero, slot_b(u, st));
-        }
+    for (int u = 0; u < PW; ++u) {
+      const bool out = KIND == kGrad && g.src && uint32_t(k_row[KIND == kGrad ? u : 0]) >= uint32_t(g.Mx);
+      const uint8_t *pa = a_base + a_row_at(u) + a_off[u], *pb = b_base + (out ? 0 : b_row_at(u)) + b_off[u];
+      if constexpr (DIRECT) {
+        const uint8_t* const zero = reinterpret_cast<const uint8_t*>(&kZero16);
+        load_to_lds<16>((A_KS ? ks_k(u) : kc_q(u)) < left && !out ? pa : zero, slot_a(u, st));
+        load_to_lds<16>((B_KS ? ks_k(u) : kc_q(u)) < left && !out ? pb : zero, slot_b(u, st));
+      } else {
+        // a KS operand's row, or the last there is (by_src: its own); a KC operand's values, or the row's last 8
+        auto hold = [&](bool ks, const uint8_t* p, int64_t ld, int length, int col, int i, bool by_src) QB_INLINE {
+          const int over = ks ? ks_k(u) - left + 1 : kc_q(u) + 8 - left;
+          if (ks && over > 0 && !by_src) p -= 2 * times(over, ld);
+          if (length < 8) {
+            // (rows of fewer than 8 values: p is a KS operand's row, or q values on in a KC one's)
+            const uint16_t* row = reinterpret_cast<const uint16_t*>(p) - (ks ? 0 : kc_q(u));
+            held[i] = ld_short(row, ks ? col : kc_q(u), out || (ks && over > 0) ? 0 : ks ? length : left);
+            held_missing &= ~(15u << (4 * i));
+            return;
+          }
+          if (!ks && over > 0) p -= 2 * over;
+          held[i] = ld_half8(p);
+          const int none = out || (ks && over > 0) ? 8 : ks || over <= 0 ? 0 : over < 8 ? over : 8;
+          if (none) held_missing = (held_missing & ~(15u << (4 * i))) | uint32_t(none) << (4 * i);
+        };
+        hold(A_KS, pa, g.lda, A_KS ? g.M : g.K, lp.m0 + ks_c(u), u, false);
+        hold(B_KS, pb, g.ldb, B_KS ? g.N : g.K, lp.n0 + ks_c(u), PW + u, KIND == kGrad && g.src);
       }
-    } else {
-      const uint16_t *a = g.A, *b = g.B;
-      if constexpr (KIND != kGrad) b += int64_t(lp.e) * g.mat_b;
-      const int k = ls * KT;
-#pragma unroll
-      for (int u = 0; u < PW; ++u) {
-        if constexpr (A_KS) {
-          const int kr = ks_k(u), c = lp.m0 + ks_c(u);
-          bool in = kr < left;
-          if (KIND == kGrad && g.src) in = in && uint32_t(k_row[KIND == kGrad ? u : 0]) < uint32_t(g.Mx);
-          held[u] = ld_inside(a + times(lp.k0 + k + kr, g.lda) + c, in ? g.M - c : 0);
-        } else {
-          const int row = a_row[A_KS ? 0 : u], q = kc_q(u);
-          const bool in = !BY_ROW || !g.src || uint32_t(row) < uint32_t(g.Mx);
-          held[u] = ld_inside(a + times(row, g.lda) + k + q, in ? left - q : 0);
-        }
-        if constexpr (B_KS) {
-          const int kr = ks_k(u), c = lp.n0 + ks_c(u), row = KIND == kGrad ? k_row[KIND == kGrad ? u : 0] : k + kr;
-          const bool in = kr < left && (KIND != kGrad || !g.src || uint32_t(row) < uint32_t(g.Mx));
-          held[PW + u] = ld_inside(b + times(row, g.ldb) + c, in ? g.N - c : 0);
-        } else {
-          const int r = kc_r(u), row = lp.n0 + r < g.N ? lp.n0 + r : g.N - 1, q = kc_q(u);
-          held[PW + u] = ld_inside(b + times(row, g.ldb) + k + q, left - q);
-        }
-      }
-      held_for = st;
     }
     issue_scales(st);
   };
   auto put = [&]() QB_INLINE {  // !DIRECT: what issue() read
     if constexpr (!DIRECT) {
       if (held_for >= 0) {
+        if (__ballot(held_missing != 0) != 0)
+#pragma unroll
+          for (int i = 0; i < 2 * PW; ++i) held[i] = in_place(held[i], held_missing >> (4 * i) & 15);
+        held_missing = 0;
 #pragma unroll
         for (int u = 0; u < PW; ++u) {
           *reinterpret_cast<uint4*>(slot_a(u, held_for) + lane * 16) = held[u];
@@ -689,7 +698,7 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
           }
         }
       } else if constexpr (KIND == kRows) {
-        const bool dead = BY_ROW && DIRECT && g.src &&
+        const bool dead = BY_ROW && g.src &&
                           uint32_t(src_of[((ctile & 7) * B + (wm * TM + i) * 16 + r) & (8 * B - 1)]) >= uint32_t(g.Mx);
         uint16_t* o = static_cast<uint16_t*>(g.out) + int64_t(row) * g.N;
 #pragma unroll
