@@ -162,7 +162,7 @@ static int tiled(Gemm16 g, hipStream_t st) {
   if (tiles > INT32_MAX) return int(hipErrorInvalidValue);
   g.tiles = int(tiles);
   // as many workgroups as run at once (a 256 x 256 tile's ring fills a CU's LDS, the others' half of it)
-  const int64_t most = int64_t(device_cu_count()) * (B == 256 ? 1 : 2);
+  const int64_t most = int64_t(device_cu_count()) * (B == 256 ? 1 : B == 64 && !DIRECT ? 4 : 2);
   hipLaunchKernelGGL((k_gemm16<__bf16, KIND, A_KS, B_KS, B, S, DIRECT>), dim3(unsigned(std::min(tiles, most))),
                      dim3(B == 256 ? 512 : 256), 0, st, g);
   return int(hipGetLastError());
@@ -171,8 +171,8 @@ static int tiled(Gemm16 g, hipStream_t st) {
 template <int KIND, bool A_KS, bool B_KS>
 static int gemm(const Gemm16& g, int64_t t256, int64_t t128, int64_t t64, double uneven, bool direct, hipStream_t st) {
   const int64_t cu = device_cu_count();
-  if (t64 <= 2 * cu)
-    return direct ? tiled<KIND, A_KS, B_KS, 64, 4, true>(g, st) : tiled<KIND, A_KS, B_KS, 64, 4, false>(g, st);
+  if (t64 <= (direct ? 2 : 4) * cu)
+    return direct ? tiled<KIND, A_KS, B_KS, 64, 4, true>(g, st) : tiled<KIND, A_KS, B_KS, 64, 2, false>(g, st);
   const double rounds256 = double((t256 + cu - 1) / cu), rounds128 = double((t128 + 2 * cu - 1) / (2 * cu));
   if (direct && t256 > 0 && 3.3 * (rounds256 + uneven) < 2 * rounds128)
     return tiled<KIND, A_KS, B_KS, 256, 2, true>(g, st);

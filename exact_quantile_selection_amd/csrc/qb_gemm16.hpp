@@ -59,7 +59,7 @@ struct Gemm16 {
   int64_t part_a, part_b, mat_out, ldo, part_out;
   const uint16_t* add;       // what the result is added to (kSqr: S, kStep: X), in out's layout
   float by_sum, by_add;      // out = by_sum * sum + by_add * add
-  int add_parts, out_parts;  // parts of a value that are read there and written: 1 or 2
+  int out_parts;             // parts of a value that are written: 1 or 2 (both are added)
   // 4-bit operands: exponent bytes, 8 for each 128 bytes of a row (mat_bs: between B's matrices)
   const uint8_t *As, *Bs;
   int64_t sld, mat_bs;
@@ -188,7 +188,7 @@ __device__ __forceinline__ void wait_stages(int k) {
 // one, whose place in the ring takes new loads in the shadow of the products
 // that are left.  The loads run on over the end of a tile.
 template <class T, int KIND, bool A_KS, bool B_KS, int B, int S, bool DIRECT, int PARTS = 1, int PA = 0, int PB = 0>
-__global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16 g) {
+__global__ __launch_bounds__(B == 256 ? 512 : 256, B == 64 && !DIRECT ? 4 : 2) void k_gemm16(const Gemm16 g) {
   constexpr int WN = B == 256 ? 4 : 2, W = 2 * WN, TM = B / 32, TN = B / WN / 16;
   constexpr int KT = 64;  // of K a stage: 128 bytes of a KC row
   constexpr int BYTES = B * KT * 2, PW = BYTES / 1024 / W;  // of an operand's stage; its 1 KiB loads a wave
@@ -202,10 +202,12 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
   auto key_k = [](int k) { return B >= 128 ? (k & 3) | ((k >> 1) & 4) : ((k >> 1) & 1) | ((k >> 2) & 2); };
   constexpr int RING = S * (2 * BYTES + S_BYTES);
   constexpr int SRC_BYTES = BY_ROW ? 8 * B * 4 : 0;  // numbers of the last 8 tiles' rows
-  __shared__ __align__(1024) uint8_t lds[RING + SRC_BYTES + W * 256 + (RAGGED ? 1024 * 3 + 16 : 16)];
+  __shared__ __align__(1024) uint8_t lds[RING + SRC_BYTES + W * 256 + (RAGGED ? 1024 * 3 + 16 : 0) +
+                                         (SYM ? W * (TN < 4 ? 1024 : 2048) : 0)];
   uint8_t* const lds_b = lds + S * BYTES;
   uint8_t* const lds_s = lds + S * 2 * BYTES;
   int* const src_of = reinterpret_cast<int*>(lds + RING);
+  uint8_t* const turned = lds + RING + SRC_BYTES + W * 256;  // SYM: 16 rows of a wave's results
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   int* const kept_of = reinterpret_cast<int*>(lds + RING + SRC_BYTES) + wave * 64;  // the last 8 tiles' places, a copy a wave
@@ -675,7 +677,52 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
     return p.n0 + (wn * TN + j) * 16 + (JT == 4 ? g4 * 16 : (g4 & 1) * 16 + (g4 >> 1) * 8);
   };
   constexpr int STORES = KIND == kGrad ? TM * TN : TM * TN / 2;
+  // kSqr, kStep: the addends of the lane's part of row tile i and the JT column tiles from j0, which are read two such
+  // parts ahead of the one that is written
+  constexpr bool SQUARE = SYM || KIND == kStep, ADDS = KIND == kSqr || KIND == kStep;
+  constexpr int STRIPS = TN / JT;
+  uint4 addend[ADDS ? 3 : 1][JT / 2][2];
+  // A strip's place in out's layout, the same for all lanes, and the lane's in bytes from there.  Made anew for each
+  // tile: the compiler would keep a register for each strip through the products.
+  uint32_t lane_at = 0;
+  auto strip_at = [&](const uint16_t* array, const Place& p, int strip) QB_INLINE {
+    const int64_t row = p.m0 + (wm * TM + strip / STRIPS) * 16, col = p.n0 + (wn * TN + strip % STRIPS * JT) * 16;
+    return same_for_all(array + int64_t(p.e) * g.mat_out + row * g.ldo + col);
+  };
+  auto ld_16_of = [](const uint8_t* base, uint32_t off) QB_INLINE {
+    typedef uint32_t w4 __attribute__((ext_vector_type(4)));
+    const w4 t = *(const __attribute__((address_space(1))) w4*)((const __attribute__((address_space(1))) uint8_t*)base + off);
+    return make_uint4(t[0], t[1], t[2], t[3]);
+  };
+  auto st_16_of = [](uint8_t* base, uint32_t off, uint4 v) QB_INLINE {
+    typedef uint32_t w4 __attribute__((ext_vector_type(4)));
+    *(__attribute__((address_space(1))) w4*)((__attribute__((address_space(1))) uint8_t*)base + off) = (w4){v.x, v.y, v.z, v.w};
+  };
+  auto read_addends = [&](const Place& p, int strip, auto whole) QB_INLINE {
+    if constexpr (ADDS) {
+      const int row = p.m0 + (wm * TM + strip / STRIPS) * 16 + r, col0 = stretch(p, strip % STRIPS * JT);
+      const uint8_t* const from = strip_at(g.add, p, strip);
+#pragma unroll
+      for (int h = 0; h < JT / 2; ++h) {
+        const int col = col0 + 8 * h;
+        uint4(&v)[2] = addend[strip % 3][h];
+        v[0] = v[1] = make_uint4(0, 0, 0, 0);
+        if (whole() || (row < g.M && col < g.ldo)) {
+          v[0] = ld_16_of(from, lane_at + 16 * h);
+          v[1] = ld_16_of(from + 2 * g.part_out, lane_at + 16 * h);
+        }
+      }
+    }
+  };
   auto store_some = [&](const Place& p, auto whole) QB_INLINE {
+    if constexpr (SQUARE) {
+      lane_at = 2 * (uint32_t(r) * uint32_t(g.ldo) + (JT == 4 ? g4 * 16 : (g4 & 1) * 16 + (g4 >> 1) * 8));
+      asm volatile("" : "+v"(lane_at));
+    }
+    if constexpr (ADDS) {
+      read_addends(p, 0, whole);
+      if (TM * STRIPS > 1) read_addends(p, 1, whole);
+    }
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       const int row = p.m0 + (wm * TM + i) * 16 + r;
@@ -731,6 +778,8 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
         // rows of ldo values, a multiple of 8, of which those past N are kept zero
 #pragma unroll
         for (int j0 = 0; j0 < TN; j0 += JT) {
+          const int strip = i * STRIPS + j0 / JT;
+          if (strip + 2 < TM * STRIPS) read_addends(p, strip + 2, whole);
           uint32_t w[4][JT];  // the lane's columns: w[c][x] is column 4 x + c of its stretch
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -742,35 +791,33 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
             exchange(w[c]);
           }
           const int col0 = stretch(p, j0);
+          uint4 parts[2][JT / 2];
 #pragma unroll
           for (int h = 0; h < JT / 2; ++h) {  // 8 columns each
             const int col = col0 + 8 * h;
-            const int64_t at0 = int64_t(p.e) * g.mat_out + int64_t(row) * g.ldo + col;
-            const bool here = row < g.M && col < g.ldo;
-            uint4 ah = make_uint4(0, 0, 0, 0), al = ah;
-            if (KIND != kSym && here) {
-              ah = *reinterpret_cast<const uint4*>(g.add + at0);
-              if (g.add_parts > 1) al = *reinterpret_cast<const uint4*>(g.add + at0 + g.part_out);
-            }
+            const uint4 ah = addend[ADDS ? strip % 3 : 0][h][0], al = addend[ADDS ? strip % 3 : 0][h][1];
             const uint32_t h4[4] = {ah.x, ah.y, ah.z, ah.w}, l4[4] = {al.x, al.y, al.z, al.w};
             float v[8];
             uint16_t hi[8], lo[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               v[c] = g.by_sum * __builtin_bit_cast(float, w[c & 3][2 * h + (c >> 2)]);
-              if constexpr (KIND != kSym)
+              if constexpr (ADDS)
                 v[c] += g.by_add * joined16(uint16_t(h4[c >> 1] >> (16 * (c & 1))), uint16_t(l4[c >> 1] >> (16 * (c & 1))));
-              v[c] = row < g.M && col + c < g.N ? v[c] : 0.f;
+              if (!whole()) v[c] = row < g.M && col + c < g.N ? v[c] : 0.f;
               split16(v[c], hi[c], lo[c]);
             }
             auto two = [](const uint16_t(&x)[8], int k) { return x[2 * k] | uint32_t(x[2 * k + 1]) << 16; };
+            parts[0][h] = make_uint4(two(hi, 0), two(hi, 1), two(hi, 2), two(hi, 3));
+            parts[1][h] = make_uint4(two(lo, 0), two(lo, 1), two(lo, 2), two(lo, 3));
+            const bool here = whole() || (row < g.M && col < g.ldo);
             if (KIND == kStep && g.last) {
               if (here) {
                 uint16_t* o = g.last + (int64_t(p.e) * g.M + row) * g.N + col;
                 Half8 t;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) t.v[k] = bf16x2_rne(v[2 * k] * g.by_last, v[2 * k + 1] * g.by_last);
-                if (col + 7 < g.N) {
+                if (whole() || col + 7 < g.N) {
                   *reinterpret_cast<Half8*>(o) = t;
                 } else {
 #pragma unroll
@@ -778,22 +825,41 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
                     if (col + c < g.N) o[c] = uint16_t(t.v[c >> 1] >> (16 * (c & 1)));
                 }
               }
-            } else {
-              uint16_t* o = static_cast<uint16_t*>(g.out);
-              if (here) {
-                *reinterpret_cast<uint4*>(o + at0) = make_uint4(two(hi, 0), two(hi, 1), two(hi, 2), two(hi, 3));
-                if (g.out_parts > 1)
-                  *reinterpret_cast<uint4*>(o + at0 + g.part_out) = make_uint4(two(lo, 0), two(lo, 1), two(lo, 2), two(lo, 3));
-              }
-              if (SYM && p.m0 != p.n0 && row < g.ldo) {
-                // the same value across the diagonal
+            } else if (here) {
+              uint8_t* const to = const_cast<uint8_t*>(strip_at(static_cast<const uint16_t*>(g.out), p, strip));
+              st_16_of(to, lane_at + 16 * h, parts[0][h]);
+              if (g.out_parts > 1) st_16_of(to + 2 * g.part_out, lane_at + 16 * h, parts[1][h]);
+            }
+          }
+          if (SYM && p.m0 != p.n0) {
+            // The same values across the diagonal: 16 rows of 16 JT columns pass through LDS, 16-byte slots XORed with
+            // the row, and come back as 8 rows of a column.
+            constexpr int ROW = JT * 32, SLOTS = ROW / 16;
+            uint8_t* const turn = turned + wave * (16 * ROW);
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                  if (col + c < g.N) {
-                    const int64_t at1 = int64_t(p.e) * g.mat_out + int64_t(col + c) * g.ldo + row;
-                    o[at1] = hi[c];
-                    if (g.out_parts > 1) o[at1 + g.part_out] = lo[c];
-                  }
+            for (int part = 0; part < 2; ++part) {
+              if (part == 1 && g.out_parts == 1) break;
+#pragma unroll
+              for (int h = 0; h < JT / 2; ++h)
+                *reinterpret_cast<uint4*>(turn + r * ROW + ((((col0 - p.n0 - (wn * TN + j0) * 16) / 8 + h) ^ r) % SLOTS) * 16) =
+                    parts[part][h];
+#pragma unroll
+              for (int q = 0; q < JT / 2; ++q) {  // the lane's column of tile jt, 8 rows from 8 half
+                const int jt = JT == 4 ? g4 : g4 & 1, half = JT == 4 ? q : g4 >> 1;
+                v4s t[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const int from = 8 * half + 4 * k + (r >> 2);
+                  const auto at = (__attribute__((address_space(3))) uint8_t*)(turn + from * ROW +
+                                                                               ((2 * jt + (r >> 1 & 1)) ^ from) % SLOTS * 16 +
+                                                                               (r & 1) * 8);
+                  t[k] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)at);
+                }
+                const int col = p.n0 + (wn * TN + j0 + jt) * 16 + r, row8 = p.m0 + (wm * TM + i) * 16 + 8 * half;
+                if (whole() || (col < g.N && row8 < g.ldo))
+                  *reinterpret_cast<v8s*>(static_cast<uint16_t*>(g.out) + int64_t(p.e) * g.mat_out + part * g.part_out +
+                                          int64_t(col) * g.ldo + row8) =
+                      __builtin_shufflevector(t[0], t[1], 0, 1, 2, 3, 4, 5, 6, 7);
               }
             }
           }
@@ -803,16 +869,11 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
   };
   auto store = [&](const Place& p) QB_INLINE {
     const bool whole = p.m0 + B <= p.m_end && p.n0 + B <= g.N;
-    if constexpr (RAGGED) {
-      if (whole)
-        store_some(p, std::true_type{});
-      else
-        store_some(p, std::false_type{});
-      return whole;
-    } else {
+    if (whole)
+      store_some(p, std::true_type{});
+    else
       store_some(p, std::false_type{});
-      return false;
-    }
+    return RAGGED && whole;
   };
 
   // The loads of a wave are waited for in the order of their issue, and a
@@ -914,6 +975,14 @@ __global__ __launch_bounds__(B == 256 ? 512 : 256, 2) void k_gemm16(const Gemm16
     if (--left == 0) {
       behind = store(now) ? S - 1 : 0;
       left = begin();
+      if constexpr (SQUARE) {
+        // What was read of the next tile is read again (an old stage, behind the last one): kept, it would not leave
+        // the registers that the addends need.
+#pragma unroll
+        for (int j = 0; j < TN; ++j) read_b(j, st, first);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) read_a(i, st, first);
+      }
       clear();
     }
   }

@@ -142,7 +142,7 @@ int launch_orthogonalize(const float* x, int G, int N, int C, int steps, float a
     Gemm16 g{};
     g.G = G;
     g.splits = 1;
-    g.add_parts = g.out_parts = 2;
+    g.out_parts = 2;
     // S
     g.A = g.B = now;
     g.lda = g.ldb = w.ldx;
