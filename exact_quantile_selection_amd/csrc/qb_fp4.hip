@@ -103,21 +103,22 @@ int launch_fp4_quantize(const uint16_t* x, int64_t Mx, const int32_t* row_src, i
   return int(hipGetLastError());
 }
 
-// A weight stack in one order or both: a workgroup takes 128 x 128 of one
-// matrix.  Along the rows a thread holds 4 columns of 16 rows, 8 lanes a block;
-// for the other order the values cross through LDS (rows of 129 words), and a
-// thread takes 32 rows of two columns' blocks.
+// A weight stack in one order or both: a workgroup takes 64 rows x 128 columns
+// of one matrix, so that four of them share a CU.  Along the rows a thread holds
+// 4 columns of 8 rows, 8 lanes a block; for the other order the values cross
+// through LDS (rows of 129 words), and a thread takes 32 rows of a column.
 template <bool BOTH>
 __global__ __launch_bounds__(256) void k_fp4_quantize_weight(const float* __restrict__ w, int N, int C, int64_t ldc,
                                                              int64_t sldc, int64_t ldn, int64_t sldn,
                                                              uint8_t* __restrict__ wq, uint8_t* __restrict__ ws,
                                                              uint8_t* __restrict__ wt, uint8_t* __restrict__ wts) {
-  __shared__ float vals[BOTH ? 128 * 129 : 1];
+  constexpr int ROWS = 64;
+  __shared__ float vals[BOTH ? ROWS * 129 : 1];
   const int tid = threadIdx.x, cg = tid & 31, rg = tid >> 5;
-  const int c0 = int(blockIdx.x) * 128 + cg * 4, n0 = int(blockIdx.y) * 128;
+  const int c0 = int(blockIdx.x) * 128 + cg * 4, n0 = int(blockIdx.y) * ROWS;
   const int64_t g = blockIdx.z;
-#pragma unroll 4
-  for (int u = 0; u < 16; ++u) {
+#pragma unroll
+  for (int u = 0; u < ROWS / 8; ++u) {
     const int row = rg + 8 * u, n = n0 + row;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
     if (n < N) {
@@ -151,9 +152,8 @@ __global__ __launch_bounds__(256) void k_fp4_quantize_weight(const float* __rest
   }
   if constexpr (BOTH) {
     __syncthreads();
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      const int i = h * 256 + tid, col = i & 127, blk = i >> 7, c = int(blockIdx.x) * 128 + col;
+    {
+      const int col = tid & 127, blk = tid >> 7, c = int(blockIdx.x) * 128 + col;
       float v[32];
       uint32_t top = 0;
 #pragma unroll
@@ -181,7 +181,7 @@ __global__ __launch_bounds__(256) void k_fp4_quantize_weight(const float* __rest
 int launch_fp4_quantize_weight(const float* w, int G, int N, int C, uint8_t* wq, uint8_t* ws, uint8_t* wt,
                                uint8_t* wts, hipStream_t st) {
   // rows of 256 values, and columns of them in the other order: both whole
-  const dim3 grid{unsigned(fp4_ld(C) / 64), unsigned(wt ? fp4_ld(N) / 64 : (N + 127) / 128), unsigned(G)};
+  const dim3 grid{unsigned(fp4_ld(C) / 64), unsigned(wt ? fp4_ld(N) / 32 : (N + 63) / 64), unsigned(G)};
   if (wt)
     hipLaunchKernelGGL(k_fp4_quantize_weight<true>, grid, dim3(256), 0, st, w, N, C, fp4_ld(C), fp4_sld(C), fp4_ld(N),
                        fp4_sld(N), wq, ws, wt, wts);
@@ -259,6 +259,7 @@ __global__ __launch_bounds__(512) void k_fp4_thin(const uint8_t* __restrict__ A,
         as[u][i] = *reinterpret_cast<const uint16_t*>(asp[i] + int64_t(kc) * 8);
       }
     }
+    __builtin_amdgcn_sched_barrier(0);  // (all of them before the first product)
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (kb + u * KW < KB) {
