@@ -925,9 +925,9 @@ QB_API int qb_fp8_weight_grad(const uint8_t* dyt, const uint8_t* dyts, const uin
                     fn);
 }
 
-// x's rows by number, or all of them in order
+// x's rows by number, or all of them in order (an array of no numbers may be null)
 static int check_rows(const char* fn, const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M, int C) {
-  if (Mx < 0 || Mx > kFp8Most || (!row_src && Mx != M))
+  if (Mx < 0 || Mx > kFp8Most || (!row_src && M > 0 && Mx != M))
     return fail(QB_EINVAL, "%s: x has Mx=%lld rows; expected M=%lld, or row_src (int32 [M])", fn, (long long)Mx,
                 (long long)M);
   if (M > 0 && Mx > 0 && !x)

@@ -159,7 +159,7 @@ static int tiled(Gemm16 g, hipStream_t st) {
   int64_t tm = (g.M + B - 1) / B;
   if (KIND == kRows && g.off) tm = g.M / B + std::min(g.G, g.M);
   const int64_t tiles = KIND == kGrad ? tm * tn * g.G * g.splits : tm * tn;
-  if (tiles > INT32_MAX) return int(hipErrorInvalidValue);
+  if (tiles > INT32_MAX / 2) return int(hipErrorInvalidValue);  // (a tile's number plus a grid's size is an int)
   g.tiles = int(tiles);
   // as many workgroups as run at once (a 256 x 256 tile's ring fills a CU's LDS, the others' half of it)
   const int64_t most = int64_t(device_cu_count()) * (B == 256 ? 1 : B == 64 && !DIRECT ? 4 : 2);

@@ -115,8 +115,9 @@ __global__ __launch_bounds__(256) void k_fp4_quantize_weight(const float* __rest
   constexpr int ROWS = 64;
   __shared__ float vals[BOTH ? ROWS * 129 : 1];
   const int tid = threadIdx.x, cg = tid & 31, rg = tid >> 5;
-  const int c0 = int(blockIdx.x) * 128 + cg * 4, n0 = int(blockIdx.y) * ROWS;
-  const int64_t g = blockIdx.z;
+  const int across = int(ldc / 64), bx = int(blockIdx.x % unsigned(across)), by = int(blockIdx.x / unsigned(across));
+  const int c0 = bx * 128 + cg * 4, n0 = by * ROWS;
+  const int64_t g = blockIdx.y;
 #pragma unroll
   for (int u = 0; u < ROWS / 8; ++u) {
     const int row = rg + 8 * u, n = n0 + row;
@@ -153,7 +154,7 @@ __global__ __launch_bounds__(256) void k_fp4_quantize_weight(const float* __rest
   if constexpr (BOTH) {
     __syncthreads();
     {
-      const int col = tid & 127, blk = tid >> 7, c = int(blockIdx.x) * 128 + col;
+      const int col = tid & 127, blk = tid >> 7, c = bx * 128 + col;
       float v[32];
       uint32_t top = 0;
 #pragma unroll
@@ -181,7 +182,9 @@ __global__ __launch_bounds__(256) void k_fp4_quantize_weight(const float* __rest
 int launch_fp4_quantize_weight(const float* w, int G, int N, int C, uint8_t* wq, uint8_t* ws, uint8_t* wt,
                                uint8_t* wts, hipStream_t st) {
   // rows of 256 values, and columns of them in the other order: both whole
-  const dim3 grid{unsigned(fp4_ld(C) / 64), unsigned(wt ? fp4_ld(N) / 32 : (N + 63) / 64), unsigned(G)};
+  const int64_t blocks = fp4_ld(C) / 64 * (wt ? fp4_ld(N) / 32 : (N + 63) / 64);
+  if (blocks > INT32_MAX / 256) return int(hipErrorInvalidValue);
+  const dim3 grid{unsigned(blocks), unsigned(G)};
   if (wt)
     hipLaunchKernelGGL(k_fp4_quantize_weight<true>, grid, dim3(256), 0, st, w, N, C, fp4_ld(C), fp4_sld(C), fp4_ld(N),
                        fp4_sld(N), wq, ws, wt, wts);
@@ -307,7 +310,7 @@ static int64_t row_tiles(const Gemm16& g, int BM) {
 template <int B, int S>
 static int tiled(Gemm16 g, hipStream_t st) {
   const int64_t tiles = row_tiles(g, B) * ((g.N + B - 1) / B);
-  if (tiles > INT32_MAX) return int(hipErrorInvalidValue);
+  if (tiles > INT32_MAX / 2) return int(hipErrorInvalidValue);
   g.tiles = int(tiles);
   const int64_t most = int64_t(device_cu_count()) * (B == 256 ? 1 : 2);
   hipLaunchKernelGGL((k_gemm16<Fp4, kRows, false, false, B, S, true>), dim3(unsigned(std::min(tiles, most))),

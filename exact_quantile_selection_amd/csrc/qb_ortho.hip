@@ -101,7 +101,7 @@ __global__ __launch_bounds__(256) void k_ortho_scale(const float* __restrict__ x
 
 template <int KIND, bool A_KS, bool B_KS, int PARTS, int PA, int PB, int B, int S>
 static int tiled(Gemm16 g, int64_t tiles, hipStream_t st) {
-  if (tiles > INT32_MAX) return int(hipErrorInvalidValue);
+  if (tiles > INT32_MAX / 2) return int(hipErrorInvalidValue);
   g.tiles = int(tiles);
   const int64_t most = int64_t(device_cu_count()) * (B == 256 ? 1 : 2);
   hipLaunchKernelGGL((k_gemm16<_Float16, KIND, A_KS, B_KS, B, S, true, PARTS, PA, PB>),

@@ -23,6 +23,10 @@ from torch.autograd.graph import increment_version
 from . import qb
 
 
+def _on(stream):
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 class ExpertLayer:
     """Router weight wr bf16 [E, H] (E of 32 to 256, as qb_router_scores takes), expert matrices w float [E, M, H], bias b
     float [E]; buffers for N tokens a call.  `held` says how the matrices are held and their products computed:
@@ -107,7 +111,7 @@ class ExpertLayer:
         else:
             if w.shape != self.w.shape:                # copy_ would broadcast it
                 raise ValueError(f"w has shape {tuple(w.shape)}, expected {tuple(self.w.shape)}")
-            with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            with _on(stream):
                 self.w.copy_(w)
 
     def forward(self, h: torch.Tensor, seq_off=None, valid=None, stream=None) -> torch.Tensor:
@@ -182,7 +186,8 @@ class ExpertLayer:
 
     def orthogonalized(self, update=None, steps: int = 5, poly=(3.4445, -4.7750, 2.0315), stream=None) -> torch.Tensor:
         """o bf16 [E, M, H]: each expert's matrix of `update` float [E, M, H] (a momentum, say; the last backward's dw by
-        default) orthogonalised as qb_orthogonalize does.  Its buffers are made by the first call."""
+        default) orthogonalised as qb_orthogonalize does.  The first call makes its buffers, on its stream; the next one
+        writes o again."""
         if update is None:
             if not self.has_dw:
                 raise RuntimeError("there was no backward")
@@ -190,9 +195,10 @@ class ExpertLayer:
         if update.shape != self.dw.shape:
             raise ValueError(f"update has shape {tuple(update.shape)}, expected {tuple(self.dw.shape)}")
         if self.o is None:
-            self.o = torch.empty_like(self.dw, dtype=torch.bfloat16)
-            self.ortho_ws = torch.empty((qb.qb_orthogonalize_workspace_bytes(*self.dw.shape),), dtype=torch.uint8,
-                                        device=self.dw.device)
+            with _on(stream):
+                self.o = torch.empty_like(self.dw, dtype=torch.bfloat16)
+                self.ortho_ws = torch.empty((qb.qb_orthogonalize_workspace_bytes(*self.dw.shape),), dtype=torch.uint8,
+                                            device=self.dw.device)
         qb.qb_orthogonalize(update, self.o, self.ortho_ws, steps=steps, poly=poly, stream=stream)
         increment_version(self.o)
         return self.o

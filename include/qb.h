@@ -631,7 +631,8 @@ QB_API int qb_fp8_weight_grad(const uint8_t* dyt, const uint8_t* dyts, const uin
  *
  * row_src nullable int32 [M]: row m of x is x[row_src[m]], x bf16 [Mx][C];
  * where row_src[m] is outside [0, Mx) it is zeros in the product, and the row
- * adds nothing to the gradient, whatever dy holds there.  Without it M = Mx.
+ * adds nothing to the gradient, whatever dy holds there.  Without it M = Mx, or
+ * M = 0.
  *
  * bf16 arrays by their element aligned; calls whose rows are multiples of 16
  * bytes and whose arrays are 16-byte aligned are the fastest.  0 <= M, Mx <=
@@ -680,15 +681,17 @@ QB_API int qb_fp4_product(const uint8_t* xq, const uint8_t* xs, const uint8_t* w
  * The orthogonalised update of a stack of matrices, for their optimizer:
  * x <- x / |x| (the root of its squares' sum), then `steps` times x <- a x + (b
  * S + c S S) x with S = x x^T, o = x rounded to bf16.  With a, b, c = 3.4445,
- * -4.7750, 2.0315 five steps take every singular value above 1/100 to between
- * 0.7 and 1.2, so that o is nearly the orthogonal factor of x.  A zero matrix
- * gives zero, one that holds a NaN or an infinity gives NaN throughout.
+ * -4.7750, 2.0315 five steps take every singular value from 1/200 of |x| on to
+ * between 0.68 and 1.16, so that o is nearly the orthogonal factor of x.  A zero
+ * matrix gives zero, one that holds a NaN or an infinity gives NaN throughout.
  *   x float [G][N][C], o bf16 [G][N][C]; 1 <= G <= 65535, 1 <= N, C <= 65536;
  *   1 <= steps <= 64.  ws: at least qb_orthogonalize_workspace_bytes, 16-byte
  *   aligned, its contents do not matter.
- * Inside, values carry 11 to 22 bits and every sum is held in 32: o is within
- * 2e-3 of |o| of the formula's, most of it o's own rounding.  Entries of x
- * beyond 16, and of S and b S + c S S beyond 256, become infinite: polynomials
+ * Inside, values carry 11 to 22 bits and every sum is held in 32, which puts o
+ * off the formula's by about 1e-3 of |o| after five steps of that polynomial
+ * (1.6e-3 for matrices of a few rows; ten steps 2.2e-3; polynomials whose slope
+ * at 0 is 2 or less 4e-4), beside its own rounding to bf16 (1.7e-3).  Entries of
+ * x beyond 16, and of S and b S + c S S beyond 256, become infinite: polynomials
  * that keep singular values below 4 stay clear of both.
  */
 QB_API int64_t qb_orthogonalize_workspace_bytes(int G, int N, int C);

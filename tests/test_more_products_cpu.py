@@ -66,6 +66,7 @@ def test_bf16_refusals(L):
     refused(L, "QB_EINVAL", "4-byte", p(off=FAKE + 2))
     refused(L, "QB_EINVAL", "4-byte", p(src=FAKE + 2))
     assert p(M=0, Mx=0, x=None, w=None, y=None) == 0
+    assert p(M=0, Mx=5) == 0                             # (an array of no numbers may be null)
 
     d = lambda dy=FAKE, x=FAKE, Mx=3000, src=None, M=3000, n=10, c=10, off=None, g=1, o=FAKE, ws=None, b=0: (  # noqa: E731
         L.qb_bf16_weight_grad(dy, x, Mx, src, M, n, c, off, g, o, ws, b, None))
