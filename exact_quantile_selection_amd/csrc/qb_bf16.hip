@@ -30,7 +30,9 @@ __device__ __forceinline__ v8s part_of(const uint4 (&v)[2], int h, int at, int K
 // 16 * 8 / KW columns; KW waves share a column tile's K, 64 at a time, so that
 // the whole weight is in flight at once, and join their sums through LDS in
 // order.  Both operands go from memory to registers: lane l takes 32
-// contiguous bytes of row l % 16, four lanes a line.
+// contiguous bytes of row l % 16, four lanes a line.  128 rows over 256 experts
+// of 1024 x 2048: 81 us, 5.1 TB/s; 8 rows over 64 of 256 x 512: 5.5 us, a launch
+// and one chain of waits.
 template <int MT, int KW, bool SHORT>
 __global__ __launch_bounds__(512) void k_bf16_thin(const uint16_t* __restrict__ A, int Mx,
                                                    const int32_t* __restrict__ src, const uint16_t* __restrict__ Bm,
@@ -129,7 +131,8 @@ __global__ __launch_bounds__(512) void k_bf16_thin(const uint16_t* __restrict__ 
   }
 }
 
-// The parts of a gradient whose sum over rows was split, added in order.
+// The parts of a gradient whose sum over rows was split, added in order: bound
+// by their bytes, 32 MiB at most.
 __global__ __launch_bounds__(256) void k_bf16_join(const float* __restrict__ part, int64_t n, int splits,
                                                    float* __restrict__ out) {
   const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
@@ -168,6 +171,13 @@ static int tiled(Gemm16 g, hipStream_t st) {
   return int(hipGetLastError());
 }
 
+// Which tile.  The smallest while its tiles all run at once: 776 x 2008 x 1000 takes 13.5 us with them, 15.6 with 128 x
+// 128 and 28.8 with 256 x 256; 2048 x 4096 x 1024, of four times as many, 41, 23.6 and 31.  By registers (!DIRECT) one
+// stage is in flight whatever the ring, so that four groups with two stages each share a CU there and the bound is twice
+// as high (1999 rows over 16 experts of 730 x 1163, rows' gradient: 25 us against 34 with 128 x 128 in two rounds).  256 x
+// 256 against 128 x 128 is a matter of whole rounds over the chip, a large tile taking 1.65 times as long as the two pairs
+// of small ones that run in its place (4096 x 4096 x 1024 36 us against 43, 8192 x 8192 x 4096 392 against 490; 2048 x
+// 4096 x 1024, half a round, 31 against 23.6); ragged experts fill a part of their last tiles, `uneven` of a round.
 template <int KIND, bool A_KS, bool B_KS>
 static int gemm(const Gemm16& g, int64_t t256, int64_t t128, int64_t t64, double uneven, bool direct, hipStream_t st) {
   const int64_t cu = device_cu_count();
@@ -197,14 +207,14 @@ template <int MT>
 static int few(const Gemm16& g, hipStream_t st) {
   const int64_t rt = g.off ? g.M / (16 * MT) + std::min(g.G, g.M) : (g.M + 16 * MT - 1) / (16 * MT);
   const int64_t waves = rt * ((g.N + 15) / 16);
-  int kw = g.K >= 8 * 64 ? 2 : 1;
+  // (32 rows come here with two waves a CU at most)
+  int kw = MT == 2 ? 4 : g.K >= 8 * 64 ? 2 : 1;
   while (kw < 8 && waves * kw < 8 * int64_t(device_cu_count())) kw *= 2;
-  switch (kw) {
-    case 1: return thin<MT, 1>(g, rt, st);
-    case 2: return thin<MT, 2>(g, rt, st);
-    case 4: return thin<MT, 4>(g, rt, st);
-    default: return thin<MT, 8>(g, rt, st);
+  if constexpr (MT == 1) {
+    if (kw == 1) return thin<MT, 1>(g, rt, st);
+    if (kw == 2) return thin<MT, 2>(g, rt, st);
   }
+  return kw == 4 ? thin<MT, 4>(g, rt, st) : thin<MT, 8>(g, rt, st);
 }
 
 // Rows of 16-byte multiples at 16-byte addresses, within 32-bit offsets of their array's start where they are taken by
@@ -234,9 +244,17 @@ int launch_bf16_product(const uint16_t* x, int Mx, const int32_t* src, int M, co
   auto tiles = [&](int b) {
     return (off ? int64_t(M / b) + std::min(G, M) : int64_t(M + b - 1) / b) * ((N + b - 1) / b);
   };
-  const int64_t cu = device_cu_count();
-  if (!transposed && rows <= 32 && (off || tiles(64) <= cu)) return rows <= 16 ? few<1>(g, st) : few<2>(g, st);
   const bool direct = C % 8 == 0 && (!transposed || N % 8 == 0) && aligned16(x) && aligned16(w) && by_offset(src, Mx, C);
+  // The kernel of few rows: while a workgroup for each 16 columns, two a CU, shares out K (64 x 1024 x 4096: 13 us against
+  // 28 in tiles of 64 x 64, 64 x 4096 x 4096 24 against 29, 128 x 4096 x 4096 44 against 29), and for very few rows, whose
+  // tiles would multiply little else than padding (1 x 16,384 x 4096 22 against 29; 512 rows over 256 experts of 1024 x
+  // 2048 167 against 179; 8 rows each of 64 experts 53 against 43), unless experts' rows begin anywhere (256 rows over 64
+  // experts of 730 x 1163 60 against 30).
+  const int few_rows = rows <= 16 ? 16 : 32;
+  const int64_t strips =
+      (off ? int64_t(M / few_rows) + std::min(G, M) : int64_t(M + few_rows - 1) / few_rows) * ((N + 15) / 16);
+  if (!transposed && (strips <= 2 * device_cu_count() || (rows <= 4 && (direct || !off))))
+    return rows <= 16 ? few<1>(g, st) : few<2>(g, st);
   const int64_t t256 = rows <= 128 && off ? 0 : tiles(256);
   const int64_t t64 = !off ? tiles(64) : tiles(64) * 2 / 3;
   const double uneven = off ? 0.1 : 0.0;

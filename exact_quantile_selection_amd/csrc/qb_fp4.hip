@@ -88,7 +88,8 @@ __global__ __launch_bounds__(256) void k_fp4_quantize(const uint16_t* __restrict
 int launch_fp4_quantize(const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M, int C, uint8_t* xq,
                         uint8_t* xs, hipStream_t st) {
   const unsigned chunks = unsigned((C + 511) / 512);
-  // four rows a wave once that still gives every CU its waves
+  // Four rows a wave once that still gives every CU its waves: rows by number wait twice, for their numbers and for
+  // themselves (131,072 of 2048 values 91 us against 107 with one; in order 74 against 70).
   const bool four = M * chunks >= 16 * 1024;
   const dim3 grid{unsigned(four ? (M + 15) / 16 : (M + 3) / 4), chunks, 1u};
   if (C < 8 || Mx == 0)
@@ -332,14 +333,14 @@ static int thin(const Gemm16& g, hipStream_t st) {
 template <int MT>
 static int few(const Gemm16& g, hipStream_t st) {
   const int64_t waves = row_tiles(g, 16 * MT) * ((g.N + 15) / 16);
-  int kw = g.K >= 8 * 64 ? 2 : 1;
+  // (32 rows come here with two waves a CU at most)
+  int kw = MT == 2 ? 4 : g.K >= 8 * 64 ? 2 : 1;
   while (kw < 8 && waves * kw < 8 * int64_t(device_cu_count())) kw *= 2;
-  switch (kw) {
-    case 1: return thin<MT, 1>(g, st);
-    case 2: return thin<MT, 2>(g, st);
-    case 4: return thin<MT, 4>(g, st);
-    default: return thin<MT, 8>(g, st);
+  if constexpr (MT == 1) {
+    if (kw == 1) return thin<MT, 1>(g, st);
+    if (kw == 2) return thin<MT, 2>(g, st);
   }
+  return kw == 4 ? thin<MT, 4>(g, st) : thin<MT, 8>(g, st);
 }
 
 int launch_fp4_product(const uint8_t* xq, const uint8_t* xs, const uint8_t* w, const uint8_t* ws, int M, int N, int C,
@@ -363,7 +364,11 @@ int launch_fp4_product(const uint8_t* xq, const uint8_t* xs, const uint8_t* w, c
   const int rows = off ? (M + G - 1) / G : M;  // rows of an expert, on average
   auto tiles = [&](int b) { return row_tiles(g, b) * ((N + b - 1) / b); };
   const int64_t cu = device_cu_count();
-  if (rows <= 32 && (off || tiles(64) <= cu)) return rows <= 16 ? few<1>(g, st) : few<2>(g, st);
+  // The kernel of few rows while a workgroup for each 16 columns, two a CU, shares out K (64 x 1024 x 4096: 6.5 us against
+  // 11 in tiles of 64 x 64, 128 x 4096 x 4096 18 against 11.5; 128 rows over 256 experts of 1024 x 2048 34 against 27), and
+  // for very few rows of one matrix (1 x 16,384 x 4096 8.9 against 11.4).
+  if (row_tiles(g, rows <= 16 ? 16 : 32) * ((N + 15) / 16) <= 2 * cu || (!off && rows <= 4))
+    return rows <= 16 ? few<1>(g, st) : few<2>(g, st);
   const int64_t t256 = rows <= 128 && off ? 0 : tiles(256);
   if ((off ? tiles(64) * 2 / 3 : tiles(64)) <= 2 * cu) return tiled<64, 4>(g, st);
   const double rounds256 = double((t256 + cu - 1) / cu), rounds128 = double((tiles(128) + 2 * cu - 1) / (2 * cu));
