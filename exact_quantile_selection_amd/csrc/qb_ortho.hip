@@ -7,9 +7,13 @@
 // singular vectors; for a matrix with more rows than columns S = x^T x on the
 // other side, the same result from the smaller square.
 //
-// A step is three products, S, P = b S + c S S and a x + P x, bound by the
-// matrix units.  S and P are symmetric: the tiles on and below the diagonal are
-// computed and written to both places.
+// A step is three products, S, P = b S + c S S and a x + P x.  S and P are
+// symmetric: the tiles on and below the diagonal are computed and written to
+// both places.  64 matrices of 1024 x 2048: S 230 us (0.60 PFLOP/s of what is
+// computed), P 173 (336 with three passes), the sum 457 (0.60; 640 with two):
+// its products alone would take 204, and the 1.5 GB that it reads and writes
+// 290, which the addends' and results' share of a tile does not overlap enough.
+// Small matrices are bound by launches of 5 to 7 us, three a step.
 //
 // Roundings.  Values are held as fp16 in two parts, the nearest and the nearest
 // to the rest (22 bits), times 2^12 for x and 2^8 for S and P (entries of x
@@ -32,7 +36,8 @@ namespace qbk {
 
 constexpr float kScaleX = 4096.f, kScaleS = 256.f;
 
-// Sums of squares in 64 bits, one for each of `gridDim.x` stretches of a matrix.
+// Sums of squares in 64 bits, one for each of `gridDim.x` stretches of a matrix: bound by the 4 bytes a value (64 matrices
+// of 1024 x 2048: 105 us, 5.1 TB/s).
 __global__ __launch_bounds__(256) void k_ortho_sums(const float* __restrict__ x, int64_t n, double* __restrict__ sums) {
   __shared__ double part[4];
   const float* p = x + int64_t(blockIdx.y) * n;
@@ -59,7 +64,7 @@ __global__ __launch_bounds__(256) void k_ortho_sums(const float* __restrict__ x,
   if (threadIdx.x == 0) sums[int64_t(blockIdx.y) * kOrthoSums + blockIdx.x] = (part[0] + part[1]) + (part[2] + part[3]);
 }
 
-// x / |x| in two parts, zeros in what rounds a row up.
+// x / |x| in two parts, zeros in what rounds a row up: 4 bytes in and 4 out a value (the same matrices: 255 us, 4.2 TB/s).
 __global__ __launch_bounds__(256) void k_ortho_scale(const float* __restrict__ x, int N, int C, int64_t ld, int parts,
                                                      const double* __restrict__ sums, int64_t part,
                                                      uint16_t* __restrict__ out) {
@@ -109,6 +114,8 @@ static int tiled(Gemm16 g, int64_t tiles, hipStream_t st) {
   return int(hipGetLastError());
 }
 
+// Tiles by whole rounds over the chip, as the bf16 products choose them (64 matrices of 1024 x 2048, five steps: 5.2 ms with
+// 256 x 256, 6.0 with 128 x 128; 5 of 301 x 165 take 64 x 64).
 template <int KIND, bool A_KS, bool B_KS, int PARTS, int PA, int PB>
 static int product(const Gemm16& g, hipStream_t st) {
   const int64_t cu = device_cu_count();
@@ -166,6 +173,7 @@ int launch_orthogonalize(const float* x, int G, int N, int C, int steps, float a
     g.out = p;
     g.by_sum = c / kScaleS;
     g.by_add = b;
+    // (8 matrices of 512 x 1024: 226 us, 262 without it)
     const bool rough = w.R >= 256 && i < 3 && i + 2 < steps;
     g.out_parts = rough ? 1 : 2;
     rc = rough ? product<kSqr, false, false, 1, 0, 0>(g, st) : product<kSqr, false, false, 3, 0b100, 0b010>(g, st);
