@@ -114,8 +114,8 @@ static int tiled(Gemm16 g, int64_t tiles, hipStream_t st) {
   return int(hipGetLastError());
 }
 
-// Tiles by whole rounds over the chip, as the bf16 products choose them (64 matrices of 1024 x 2048, five steps: 5.2 ms with
-// 256 x 256, 6.0 with 128 x 128; 5 of 301 x 165 take 64 x 64).
+// Tiles by whole rounds over the chip, as the bf16 products choose them (64 matrices of 1024 x 2048, five steps, before
+// addends were read ahead: 5.46 ms with 256 x 256, 6.05 with 128 x 128; 5 of 301 x 165 take 64 x 64).
 template <int KIND, bool A_KS, bool B_KS, int PARTS, int PA, int PB>
 static int product(const Gemm16& g, hipStream_t st) {
   const int64_t cu = device_cu_count();
