@@ -1034,9 +1034,8 @@ QB_API int64_t qb_orthogonalize_workspace_bytes(int G, int N, int C) {
   return qbk::ortho_ws_layout(G, N, C).bytes;
 }
 
-QB_API int qb_orthogonalize(const float* x, int G, int N, int C, int steps, float a, float b, float c, uint16_t* o,
-                            void* ws, int64_t ws_bytes, qb_stream_t stream) {
-  const char* fn = "qb_orthogonalize";
+static int orthogonalize(const char* fn, const float* x, int G, int N, int C, int steps, float a, float b, float c,
+                         bool exact, uint16_t* o, void* ws, int64_t ws_bytes, qb_stream_t stream) {
   if (int rc = check_orthogonalize(fn, G, N, C)) return rc;
   if (steps < 1 || steps > 64) return fail(QB_EINVAL, "%s: steps=%d, expected 1 to 64", fn, steps);
   if (!x || !o)
@@ -1048,7 +1047,18 @@ QB_API int qb_orthogonalize(const float* x, int G, int N, int C, int steps, floa
   if (!aligned16(ws)) return fail(QB_EINVAL, "%s: ws must be 16-byte aligned", fn);
   if (!aligned_all(2, {o})) return fail(QB_EINVAL, "%s: o must be 2-byte aligned", fn);
   if (int rc = check_elem_align(fn, {x})) return rc;
-  return hip_status(qbk::launch_orthogonalize(x, G, N, C, steps, a, b, c, o, static_cast<uint8_t*>(ws), stream), fn);
+  return hip_status(
+      qbk::launch_orthogonalize(x, G, N, C, steps, a, b, c, exact, o, static_cast<uint8_t*>(ws), stream), fn);
+}
+
+QB_API int qb_orthogonalize(const float* x, int G, int N, int C, int steps, float a, float b, float c, uint16_t* o,
+                            void* ws, int64_t ws_bytes, qb_stream_t stream) {
+  return orthogonalize("qb_orthogonalize", x, G, N, C, steps, a, b, c, true, o, ws, ws_bytes, stream);
+}
+
+QB_API int qb_orthogonalize_coarse(const float* x, int G, int N, int C, int steps, float a, float b, float c,
+                                   uint16_t* o, void* ws, int64_t ws_bytes, qb_stream_t stream) {
+  return orthogonalize("qb_orthogonalize_coarse", x, G, N, C, steps, a, b, c, false, o, ws, ws_bytes, stream);
 }
 
 QB_API const char* qb_status_string(int status) {

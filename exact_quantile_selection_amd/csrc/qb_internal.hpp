@@ -250,7 +250,7 @@ inline OrthoWs ortho_ws_layout(int64_t G, int64_t N, int64_t C) {
   w.bytes = w.p + s;
   return w;
 }
-int launch_orthogonalize(const float* x, int G, int N, int C, int steps, float a, float b, float c, uint16_t* o,
-                         uint8_t* ws, hipStream_t st);
+int launch_orthogonalize(const float* x, int G, int N, int C, int steps, float a, float b, float c, bool exact,
+                         uint16_t* o, uint8_t* ws, hipStream_t st);
 
 }  // namespace qbk

@@ -18,18 +18,23 @@
 // Roundings.  Values are held as fp16 in two parts, the nearest and the nearest
 // to the rest (22 bits), times 2^12 for x and 2^8 for S and P (entries of x
 // below 16 and of S and P below 256 fit; with the usual polynomials they stay
-// below 1.3 and 3).  What a product reads of them was chosen by what it costs
-// the result (simulated; relative to |result|, random 512 x 1024, five steps; the
-// result's own rounding to bf16 is 1.7e-3): x in one part for S 4.6e-4, S in one
-// part for S S 2.3e-3, P in one part 1.0e-3, x in one part for P x 9e-4, x in one
-// part where it is added 1.4e-3.  What the last two steps round weighs most (the
-// ones before are 6e-4 off with all of that but the last in one part).  So the
-// sum always takes both parts of x, S and P x one part of x; S S both parts of
-// both (three passes: the product of the low parts is below 2^-22) and P x both
-// of P, but for the first three steps of matrices of 256 rows and more (roundings
-// of smaller ones add up less evenly: 2e-3 and more so), unless they are among
-// the last two, which take one: 1.1e-3 in all.  bf16 in one part, as such steps
-// are often run, is 2.1e-2 off.
+// below 1.3 and 3), and every sum in 32 bits.  A product takes both parts of
+// both operands in three passes, without that of the low parts, below 2^-22: the
+// result before its rounding to bf16 is 3e-7 to 8e-7 of |result| off (simulated,
+// 16 x 16 to 1024 x 1024, five steps), where values held in 32 bits are 6e-7 to
+// 2e-6 off.
+//
+// exact = false takes fewer passes.  What a product reads was chosen by what it
+// costs the result (simulated; relative to |result|, random 512 x 1024, five
+// steps; the result's own rounding to bf16 is 1.7e-3): x in one part for S
+// 4.6e-4, S in one part for S S 2.3e-3, P in one part 1.0e-3, x in one part for P
+// x 9e-4, x in one part where it is added 1.4e-3.  What the last two steps round
+// weighs most (the ones before are 6e-4 off with all of that but the last in one
+// part).  So the sum takes both parts of x, S and P x one part of x; S S both
+// parts of both and P x both of P, but for the first three steps of matrices of
+// 256 rows and more (roundings of smaller ones add up less evenly: 2e-3 and more
+// so), unless they are among the last two, which take one: 1.1e-3 in all.  bf16
+// in one part, as such steps are often run, is 2.1e-2 off.
 #include "qb_gemm16.hpp"
 
 namespace qbk {
@@ -130,8 +135,8 @@ static int product(const Gemm16& g, hipStream_t st) {
   return tiled<KIND, A_KS, B_KS, PARTS, PA, PB, 128, 2>(g, t128, st);
 }
 
-int launch_orthogonalize(const float* x, int G, int N, int C, int steps, float a, float b, float c, uint16_t* o,
-                         uint8_t* ws, hipStream_t st) {
+int launch_orthogonalize(const float* x, int G, int N, int C, int steps, float a, float b, float c, bool exact,
+                         uint16_t* o, uint8_t* ws, hipStream_t st) {
   const OrthoWs w = ortho_ws_layout(G, N, C);
   double* sums = reinterpret_cast<double*>(ws);
   uint16_t* xs[2] = {reinterpret_cast<uint16_t*>(ws + w.x0), reinterpret_cast<uint16_t*>(ws + w.x1)};
@@ -154,6 +159,7 @@ int launch_orthogonalize(const float* x, int G, int N, int C, int steps, float a
     g.A = g.B = now;
     g.lda = g.ldb = w.ldx;
     g.mat_a = g.mat_b = mat_x;
+    g.part_a = g.part_b = part_x;
     g.M = g.N = int(w.R);
     g.K = w.tall ? N : C;
     g.out = s;
@@ -161,7 +167,11 @@ int launch_orthogonalize(const float* x, int G, int N, int C, int steps, float a
     g.mat_out = mat_s;
     g.part_out = part_s;
     g.by_sum = kScaleS / (kScaleX * kScaleX);
-    int rc = w.tall ? product<kSym, true, true, 1, 0, 0>(g, st) : product<kSym, false, false, 1, 0, 0>(g, st);
+    int rc;
+    if (exact)
+      rc = w.tall ? product<kSym, true, true, 3, 0b100, 0b010>(g, st) : product<kSym, false, false, 3, 0b100, 0b010>(g, st);
+    else
+      rc = w.tall ? product<kSym, true, true, 1, 0, 0>(g, st) : product<kSym, false, false, 1, 0, 0>(g, st);
     if (rc) return rc;
     // P
     g.A = g.B = s;
@@ -174,7 +184,7 @@ int launch_orthogonalize(const float* x, int G, int N, int C, int steps, float a
     g.by_sum = c / kScaleS;
     g.by_add = b;
     // (8 matrices of 512 x 1024: 226 us, 262 without it)
-    const bool rough = w.R >= 256 && i < 3 && i + 2 < steps;
+    const bool rough = !exact && w.R >= 256 && i < 3 && i + 2 < steps;
     g.out_parts = rough ? 1 : 2;
     rc = rough ? product<kSqr, false, false, 1, 0, 0>(g, st) : product<kSqr, false, false, 3, 0b100, 0b010>(g, st);
     if (rc) return rc;
@@ -196,17 +206,23 @@ int launch_orthogonalize(const float* x, int G, int N, int C, int steps, float a
       g.A = now;
       g.lda = w.ldx;
       g.mat_a = mat_x;
+      g.part_a = part_x;
       g.B = p;
       g.ldb = w.ldr;
       g.mat_b = mat_s;
       g.part_b = part_s;
-      rc = rough ? product<kStep, false, false, 1, 0, 0>(g, st) : product<kStep, false, false, 2, 0, 0b10>(g, st);
+      rc = exact   ? product<kStep, false, false, 3, 0b100, 0b010>(g, st)
+           : rough ? product<kStep, false, false, 1, 0, 0>(g, st)
+                   : product<kStep, false, false, 2, 0, 0b10>(g, st);
     } else {
       g.A = p;
       g.B = now;
       g.ldb = w.ldx;
       g.mat_b = mat_x;
-      rc = rough ? product<kStep, false, true, 1, 0, 0>(g, st) : product<kStep, false, true, 2, 0b10, 0>(g, st);
+      g.part_b = part_x;
+      rc = exact   ? product<kStep, false, true, 3, 0b100, 0b010>(g, st)
+           : rough ? product<kStep, false, true, 1, 0, 0>(g, st)
+                   : product<kStep, false, true, 2, 0b10, 0>(g, st);
     }
     if (rc) return rc;
   }

@@ -184,9 +184,10 @@ class ExpertLayer:
         self.eqb.reset(stream)
         qb.eqb_update(self.s, self.b, self.K, self.alpha, self.eqb, stream=stream, topk=self.topk if masked else None)
 
-    def orthogonalized(self, update=None, steps: int = 5, poly=(3.4445, -4.7750, 2.0315), stream=None) -> torch.Tensor:
+    def orthogonalized(self, update=None, steps: int = 5, poly=(3.4445, -4.7750, 2.0315), stream=None,
+                       exact: bool = True) -> torch.Tensor:
         """o bf16 [E, M, H]: each expert's matrix of `update` float [E, M, H] (a momentum, say; the last backward's dw by
-        default) orthogonalised as qb_orthogonalize does.  The first call makes its buffers, on its stream; the next one
+        default) orthogonalised as qb_orthogonalize does, whose `exact` is this one.  The first call makes its buffers, on its stream; the next one
         writes o again."""
         if update is None:
             if not self.has_dw:
@@ -199,6 +200,6 @@ class ExpertLayer:
                 self.o = torch.empty_like(self.dw, dtype=torch.bfloat16)
                 self.ortho_ws = torch.empty((qb.qb_orthogonalize_workspace_bytes(*self.dw.shape),), dtype=torch.uint8,
                                             device=self.dw.device)
-        qb.qb_orthogonalize(update, self.o, self.ortho_ws, steps=steps, poly=poly, stream=stream)
+        qb.qb_orthogonalize(update, self.o, self.ortho_ws, steps=steps, poly=poly, stream=stream, exact=exact)
         increment_version(self.o)
         return self.o

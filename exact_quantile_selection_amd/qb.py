@@ -93,6 +93,7 @@ def lib() -> C.CDLL:
             "qb_fp4_quantize_weight": [vp, i32, i32, i32, vp, vp, vp, vp, vp],
             "qb_fp4_product": [vp, vp, vp, vp, i64, i32, i32, vp, i32, vp, vp],
             "qb_orthogonalize": [vp, i32, i32, i32, i32, f32, f32, f32, vp, vp, i64, vp],
+            "qb_orthogonalize_coarse": [vp, i32, i32, i32, i32, f32, f32, f32, vp, vp, i64, vp],
             "qb_bf16_product": [vp, i64, vp, i64, vp, i32, i32, vp, i32, i32, vp, vp],
             "qb_bf16_weight_grad": [vp, vp, i64, vp, i64, i32, i32, vp, i32, vp, vp, i64, vp],
         }
@@ -667,17 +668,18 @@ def qb_orthogonalize_workspace_bytes(G, N, C):
     return _bytes(lib().qb_orthogonalize_workspace_bytes(G, N, C))
 
 
-def qb_orthogonalize(x, o, ws, steps=5, poly=(3.4445, -4.7750, 2.0315), stream=None):
+def qb_orthogonalize(x, o, ws, steps=5, poly=(3.4445, -4.7750, 2.0315), stream=None, exact=True):
     """o bf16 = x float [N, C] or [G, N, C], each matrix divided by its norm and
     taken `steps` times through a x + (b S + c S S) x, S = x x^T, (a, b, c) =
-    poly; ws uint8, qb_orthogonalize_workspace_bytes."""
+    poly; ws uint8, qb_orthogonalize_workspace_bytes.  exact=False: fewer
+    products, o about 1e-3 of its norm further off (qb_orthogonalize_coarse)."""
     if not isinstance(x, torch.Tensor) or x.dim() not in (2, 3):
         raise ValueError("x must be [N, C] or [G, N, C]")
     a, b, c = poly
     G, N, Cn = (1,) * (3 - x.dim()) + tuple(x.shape)
-    _check(lib().qb_orthogonalize(_ptr(x, torch.float32, "x"), G, N, Cn, steps, a, b, c,
-                                  _ptr(o, torch.bfloat16, "o", x.shape), _ptr(ws, torch.uint8, "ws"), ws.numel(),
-                                  _stream(stream)))
+    call = lib().qb_orthogonalize if exact else lib().qb_orthogonalize_coarse
+    _check(call(_ptr(x, torch.float32, "x"), G, N, Cn, steps, a, b, c, _ptr(o, torch.bfloat16, "o", x.shape),
+                _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
 
 
 # ---------------------------------------------------------------------------

@@ -687,16 +687,21 @@ QB_API int qb_fp4_product(const uint8_t* xq, const uint8_t* xs, const uint8_t* w
  *   x float [G][N][C], o bf16 [G][N][C]; 1 <= G <= 65535, 1 <= N, C <= 65536;
  *   1 <= steps <= 64.  ws: at least qb_orthogonalize_workspace_bytes, 16-byte
  *   aligned, its contents do not matter.
- * Inside, values carry 11 to 22 bits and every sum is held in 32, which puts o
- * off the formula's by about 1e-3 of |o| after five steps of that polynomial
- * (1.6e-3 for matrices of a few rows; ten steps 2.2e-3; polynomials whose slope
- * at 0 is 2 or less 4e-4), beside its own rounding to bf16 (1.7e-3).  Entries of
- * x beyond 16, and of S and b S + c S S beyond 256, become infinite: polynomials
- * that keep singular values below 4 stay clear of both.
+ * Inside, values carry 22 bits and every sum is held in 32: before its rounding
+ * to bf16 (1.7e-3 of |o|) o is off the formula's by no more than if all were held
+ * in 32 bits (1e-6).  Entries of x beyond 16, and of S and b S + c S S beyond 256,
+ * become infinite: polynomials that keep singular values below 4 stay clear of
+ * both.
+ * qb_orthogonalize_coarse: the same with fewer products, which read 11 bits of
+ * most values; o is off by about 1e-3 of |o| more after five steps of that
+ * polynomial (1.6e-3 for matrices of a few rows; ten steps 2.2e-3; polynomials
+ * whose slope at 0 is 2 or less 4e-4).
  */
 QB_API int64_t qb_orthogonalize_workspace_bytes(int G, int N, int C);
 QB_API int qb_orthogonalize(const float* x, int G, int N, int C, int steps, float a, float b, float c, uint16_t* o,
                             void* ws, int64_t ws_bytes, qb_stream_t stream);
+QB_API int qb_orthogonalize_coarse(const float* x, int G, int N, int C, int steps, float a, float b, float c,
+                                   uint16_t* o, void* ws, int64_t ws_bytes, qb_stream_t stream);
 
 /* Short name of a status code (static storage). */
 QB_API const char* qb_status_string(int status);
