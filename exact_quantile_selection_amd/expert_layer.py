@@ -111,7 +111,7 @@ class ExpertLayer:
         else:
             if w.shape != self.w.shape:                # copy_ would broadcast it
                 raise ValueError(f"w has shape {tuple(w.shape)}, expected {tuple(self.w.shape)}")
-            with _on(stream):
+            with _on(stream), torch.no_grad():         # (of a parameter too)
                 self.w.copy_(w)
 
     def forward(self, h: torch.Tensor, seq_off=None, valid=None, stream=None) -> torch.Tensor:
