@@ -38,8 +38,8 @@ class ExpertLayer:
       computed from the rows in bfloat16.
 
     Results are the layer's own buffers, which its next call writes again.  One forward at a time is followed by its
-    backward, which reads that forward's h, seq_off and valid again: they are not copied, and one that torch or a layer
-    has written since is an error."""
+    backward, which reads that forward's h, seq_off and valid again, and the matrices: they are not copied, and one that
+    torch or a layer has written since is an error."""
 
     def __init__(self, wr: torch.Tensor, w: torch.Tensor, K: int, N: int, coef: float = 0.0, B: int = 1,
                  exact: bool = True, held: str = "e4m3"):
@@ -113,6 +113,8 @@ class ExpertLayer:
                 raise ValueError(f"w has shape {tuple(w.shape)}, expected {tuple(self.w.shape)}")
             with _on(stream), torch.no_grad():         # (of a parameter too)
                 self.w.copy_(w)
+            return
+        increment_version((self.wq, self.ws, self.wt, self.wts))
 
     def forward(self, h: torch.Tensor, seq_off=None, valid=None, stream=None) -> torch.Tensor:
         """out bf16 [N, M] of hidden states h bf16 [N, H]; `loss` and `count`
@@ -136,8 +138,12 @@ class ExpertLayer:
         qb.qb_combine(self.rows, self.pos, self.out, gate=self.gate, stream=stream)
         increment_version(self.out)
         self.h, self.seqs = h, seqs
-        self.versions = {n: t._version for n, t in dict(h=h, **seqs).items() if t is not None and not t.is_inference()}
+        self.versions = {n: t._version for n, t in self._read_again().items() if t is not None and not t.is_inference()}
         return self.out
+
+    def _read_again(self):
+        """What backward reads that its forward read."""
+        return dict(h=self.h, **self.seqs, w=self.w if self.held == "bf16" else self.wt)
 
     def _forward_done(self):
         if self.h is None:
@@ -148,8 +154,9 @@ class ExpertLayer:
         float [E, M, H] and dlogits float [N, E] of the router's logits (whose
         own product with wr is the caller's)."""
         self._forward_done()
+        now = self._read_again()
         for name, version in self.versions.items():
-            if dict(h=self.h, **self.seqs)[name]._version != version:
+            if now[name]._version != version:
                 raise RuntimeError(f"{name} was written after the forward, and backward reads it again")
         qb.qb_combine_backward(dout, self.rows, self.pos, self.row_src, self.drows, gate=self.gate, dgate=self.dgate,
                                stream=stream)
