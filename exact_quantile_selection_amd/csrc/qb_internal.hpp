@@ -216,7 +216,6 @@ int launch_bf16_weight_grad(const uint16_t* dy, const uint16_t* x, int Mx, const
                             const int32_t* off, int G, float* dw, float* ws, hipStream_t st);
 
 // 4-bit products with a power-of-two scale for each block of 32: bytes of a row of n values, and of its scales.
-constexpr int kQBlock4 = 32;
 inline int64_t fp4_ld(int64_t n) { return (n + 255) / 256 * 128; }
 inline int64_t fp4_sld(int64_t n) { return (n + 255) / 256 * 8; }
 int launch_fp4_quantize(const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M, int C, uint8_t* xq,
