@@ -68,7 +68,8 @@ def test_steps_and_polynomials(N, C, steps, poly):
 
 
 # sizes where roundings add up evenly, for every tile and with and without the steps of one pass
-@pytest.mark.parametrize("lead,N,C", [((), 128, 256), ((5,), 301, 165), ((), 512, 1024), ((16,), 640, 520), ((24,), 1024, 1030)])
+@pytest.mark.parametrize("lead,N,C", [((), 128, 256), ((5,), 301, 165), ((), 512, 1024), ((), 1024, 512), ((16,), 520, 640),
+                                      ((16,), 640, 520), ((24,), 1024, 1030), ((24,), 1030, 1024)])
 def test_the_coarse_form(lead, N, C):
     """The roundings inside are of the simulated size, and the result's own is independent of them: the two add up as
     squares (a quarter more inside for what single matrices differ by)."""
@@ -83,6 +84,42 @@ def test_the_coarse_form(lead, N, C):
         off = norm(o[g] - want)
         assert off ** 2 <= own ** 2 + (1.25 * inside) ** 2
         assert off ** 2 >= own ** 2 + (0.75 * inside) ** 2  # (and it is the coarse form that ran)
+
+
+@pytest.mark.parametrize("lead,N,C", [((), 40, 65536), ((), 65536, 40), ((), 4096, 4096), ((2,), 8200, 2000), ((), 1500, 8200),
+                                      ((), 8192, 8192)])
+def test_large_matrices(lead, N, C):
+    rng = np.random.default_rng(N + C)
+    G.say(f"orthogonalize exactly {lead} {N} {C}")
+    x = torch.randn(lead + (N, C), generator=torch.Generator(device=G.DEV).manual_seed(N + C), device=G.DEV)
+    x *= torch.exp(0.5 * randn(rng, N, 1))
+    o = orthogonalized(x)
+    for g in np.ndindex(*lead):
+        keeps(o[g], x[g])
+
+
+# between them they have singular values from 1/200 of their norm to nearly all of it
+@pytest.mark.parametrize("N,C,first", [(64, 200, 1.0), (64, 200, 0.2), (200, 64, 0.1), (300, 300, 0.05)])
+def test_the_singular_values_that_are_promised(N, C, first):
+    """1/200 of the norm and more end between 0.68 and 1.16 (and a bf16 result's
+    rounding, 2^-8 of its norm in all directions together); what the vectors are stays."""
+    rng = np.random.default_rng(N + C)
+    R = min(N, C)
+    u = torch.linalg.qr(randn(rng, N, R).double())[0]
+    v = torch.linalg.qr(randn(rng, C, R).double())[0]
+    s = torch.logspace(0, 0, R, dtype=torch.float64, device=G.DEV) * 0.0055
+    s[0] = first
+    s[1:9] = torch.logspace(-2.2, -1, 8, dtype=torch.float64, device=G.DEV)
+    s /= torch.linalg.vector_norm(s)
+    assert s.min() >= 1 / 200
+    G.say(f"orthogonalize singular values {N} {C} {first}")
+    o = orthogonalized(((u * s) @ v.T).float()).double()
+    d = u.T @ o @ v
+    # o's roundings, each at most 2^-8 of a value, seen along one pair of directions
+    off = torch.sqrt((u.square().T @ (o * 2.0 ** -8).square()) @ v.square())
+    low, high = d.diagonal() + 4 * off.diagonal(), d.diagonal() - 4 * off.diagonal()
+    assert low.min() >= 0.68 and high.max() <= 1.16, (low.min().item(), high.max().item())
+    assert ((d - torch.diag(d.diagonal())).abs() <= 6 * off).all()
 
 
 def test_the_layer_passes_the_choice_on():
