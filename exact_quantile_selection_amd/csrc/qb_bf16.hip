@@ -175,17 +175,13 @@ static int tiled(Gemm16 g, hipStream_t st) {
 // 128 and 28.8 with 256 x 256; 2048 x 4096 x 1024, of four times as many, 41, 23.6 and 31.  By registers (!DIRECT) one
 // stage is in flight whatever the ring, so that four groups with two stages each share a CU there and the bound is twice
 // as high (1999 rows over 16 experts of 730 x 1163, rows' gradient: 25 us against 34 with 128 x 128 in two rounds).  256 x
-// 256 against 128 x 128 is a matter of whole rounds over the chip, a large tile taking 1.65 times as long as the two pairs
-// of small ones that run in its place (4096 x 4096 x 1024 36 us against 43, 8192 x 8192 x 4096 392 against 490; 2048 x
-// 4096 x 1024, half a round, 31 against 23.6); ragged experts fill a part of their last tiles, `uneven` of a round.
+// 256 against 128 x 128: in_large_tiles.
 template <int KIND, bool A_KS, bool B_KS>
 static int gemm(const Gemm16& g, int64_t t256, int64_t t128, int64_t t64, double uneven, bool direct, hipStream_t st) {
   const int64_t cu = device_cu_count();
   if (t64 <= (direct ? 2 : 4) * cu)
     return direct ? tiled<KIND, A_KS, B_KS, 64, 4, true>(g, st) : tiled<KIND, A_KS, B_KS, 64, 2, false>(g, st);
-  const double rounds256 = double((t256 + cu - 1) / cu), rounds128 = double((t128 + 2 * cu - 1) / (2 * cu));
-  if (direct && t256 > 0 && 3.3 * (rounds256 + uneven) < 2 * rounds128)
-    return tiled<KIND, A_KS, B_KS, 256, 2, true>(g, st);
+  if (direct && in_large_tiles(t256, t128, uneven)) return tiled<KIND, A_KS, B_KS, 256, 2, true>(g, st);
   return direct ? tiled<KIND, A_KS, B_KS, 128, 2, true>(g, st) : tiled<KIND, A_KS, B_KS, 128, 2, false>(g, st);
 }
 
@@ -249,13 +245,19 @@ int launch_bf16_product(const uint16_t* x, int Mx, const int32_t* src, int M, co
   // 28 in tiles of 64 x 64, 64 x 4096 x 4096 24 against 29, 128 x 4096 x 4096 44 against 29), and for very few rows, whose
   // tiles would multiply little else than padding (1 x 16,384 x 4096 22 against 29; 512 rows over 256 experts of 1024 x
   // 2048 167 against 179; 8 rows each of 64 experts 53 against 43), unless experts' rows begin anywhere (256 rows over 64
-  // experts of 730 x 1163 60 against 30).
+  // experts of 730 x 1163 60 against 30).  The other order has no such kernel: its few rows run in tiles, K by one workgroup
+  // (the gradient of 1 or 16 rows of 4096 x 4096 28 us where the forward product takes 8 and 10, of 4096 x 16,384 103).
   const int few_rows = rows <= 16 ? 16 : 32;
   const int64_t strips =
       (off ? int64_t(M / few_rows) + std::min(G, M) : int64_t(M + few_rows - 1) / few_rows) * ((N + 15) / 16);
   if (!transposed && (strips <= 2 * device_cu_count() || (rows <= 4 && (direct || !off))))
     return rows <= 16 ? few<1>(g, st) : few<2>(g, st);
+  // Experts of so few rows fill half of a large tile at most (5120 rows over 40 experts of 1024 x 2048 57 us in 128 x 128,
+  // 67 in 256 x 256; 3072 over 48 56 and 65).
   const int64_t t256 = rows <= 128 && off ? 0 : tiles(256);
+  // Of ragged experts' tiles of 64 rows a third is taken to be missing or nearly empty (2000 rows over 16 experts of 700 x
+  // 1160 17 us in 64 x 64, 23 in 128 x 128; of 1400 x 1024 22 and 18; near the border the other is up to 14% faster: of
+  // 1024 x 1024 19 and 16.6, 1500 over 64 of 768 x 1024 22.4 and 25.6).
   const int64_t t64 = !off ? tiles(64) : tiles(64) * 2 / 3;
   const double uneven = off ? 0.1 : 0.0;
   return transposed ? gemm<kRows, false, true>(g, t256, tiles(128), t64, uneven, direct, st)

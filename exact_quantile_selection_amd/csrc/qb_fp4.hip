@@ -37,7 +37,7 @@ __device__ __forceinline__ uint32_t to_e2m1x4(float a, float b, float c, float d
 }
 
 // A wave takes 512 columns of U rows, 4 lanes a block.  Bound by its 2 bytes in
-// and 17/32 out a value: 131,072 rows of 2048 by number of 16,384 91 us (what is
+// and 17/32 out a value: 131,072 rows of 2048 by number of 16,384 98 us (what is
 // read comes from the last cache), 65,536 in order 74 us, 4.6 TB/s.
 template <int U, bool SHORT>
 __global__ __launch_bounds__(256) void k_fp4_quantize(const uint16_t* __restrict__ x, int64_t Mx,
@@ -91,7 +91,7 @@ int launch_fp4_quantize(const uint16_t* x, int64_t Mx, const int32_t* row_src, i
                         uint8_t* xs, hipStream_t st) {
   const unsigned chunks = unsigned((C + 511) / 512);
   // Four rows a wave once that still gives every CU its waves: rows by number wait twice, for their numbers and for
-  // themselves (131,072 of 2048 values 91 us against 107 with one; in order 74 against 70).
+  // themselves (131,072 of 2048 values 91 us against 107 with one, as they were timed together; in order 74 against 70).
   const bool four = M * chunks >= 16 * 1024;
   const dim3 grid{unsigned(four ? (M + 15) / 16 : (M + 3) / 4), chunks, 1u};
   if (C < 8 || Mx == 0)
@@ -206,7 +206,7 @@ int launch_fp4_quantize_weight(const float* w, int G, int N, int C, uint8_t* wq,
 // waits: a workgroup of 8 waves takes 16 MT rows and 16 * 8 / KW columns; KW
 // waves share a column tile's K, 256 values at a time, and join their sums
 // through LDS in order.  Lane l takes 32 contiguous bytes of row l % 16, two
-// blocks of 32 and their two exponents.  1 x 4096 x 4096: 6.4 us.
+// blocks of 32 and their two exponents.  1 x 4096 x 4096: 6.2 us.
 template <int MT, int KW>
 __global__ __launch_bounds__(512) void k_fp4_thin(const uint8_t* __restrict__ A, const uint8_t* __restrict__ As,
                                                   const uint8_t* __restrict__ Bm, const uint8_t* __restrict__ Bs,
@@ -312,8 +312,10 @@ static int64_t row_tiles(const Gemm16& g, int BM) {
   return g.off ? g.M / BM + std::min(g.G, g.M) : (g.M + BM - 1) / BM;
 }
 
-// 8192 x 8192 x 4096: 149 us, 3.7 PFLOP/s, bound by the products at the clock they leave; 131,072 rows over 64 experts of
-// 1024 x 2048 225 us, 2.4 PFLOP/s: 8 rounds of stages too short to hide a tile's way out.
+// 8192 x 8192 x 4096: 151 us, 3.6 PFLOP/s, the matrix units busy 39% of the CUs' cycles (bf16: 64%): a stage has as many
+// products as in bf16, each as long, and twelve reads of exponents a step more, and a tile a fourth of the stages beside
+// which its results leave.  131,072 rows over 64 experts of 1024 x 2048 232 us, 2.4 PFLOP/s, busy 31%: 8 stages a tile
+// (in 128 x 128, two to a CU, 262; 65,536 rows of 2048 x 1024 150 against 170).
 template <int B, int S>
 static int tiled(Gemm16 g, hipStream_t st) {
   const int64_t tiles = row_tiles(g, B) * ((g.N + B - 1) / B);
@@ -375,10 +377,12 @@ int launch_fp4_product(const uint8_t* xq, const uint8_t* xs, const uint8_t* w, c
   // for very few rows of one matrix (1 x 16,384 x 4096 8.9 against 11.4).
   if (row_tiles(g, rows <= 16 ? 16 : 32) * ((N + 15) / 16) <= 2 * cu || (!off && rows <= 4))
     return rows <= 16 ? few<1>(g, st) : few<2>(g, st);
+  // As the bf16 products: experts of so few rows fill half of a large tile at most (5120 rows over 40 experts of 1024 x
+  // 2048 18.6 us in 128 x 128, 23 in 256 x 256), and a third of ragged experts' tiles of 64 rows is taken to be missing
+  // (2000 rows over 16 experts of 700 x 1160 8.9 us in 64 x 64, 10.9 in 128 x 128; of 1400 x 1024 12.1 and 10.8).
   const int64_t t256 = rows <= 128 && off ? 0 : tiles(256);
   if ((off ? tiles(64) * 2 / 3 : tiles(64)) <= 2 * cu) return tiled<64, 4>(g, st);
-  const double rounds256 = double((t256 + cu - 1) / cu), rounds128 = double((tiles(128) + 2 * cu - 1) / (2 * cu));
-  if (t256 > 0 && 3.3 * (rounds256 + (off ? 0.1 : 0.0)) < 2 * rounds128) return tiled<256, 2>(g, st);
+  if (in_large_tiles(t256, tiles(128), off ? 0.1 : 0.0)) return tiled<256, 2>(g, st);
   return tiled<128, 2>(g, st);
 }
 

@@ -18,11 +18,12 @@
 // number made of the bits of k in which the 8 rows that half a wave reads
 // differ (0..3 and 8..11): those 8 slots lie in all banks once.
 //
-// Bound by the matrix units, at the clock that they leave: 8192 x 8192 x 4096 in
-// bf16 392 us KC x KC (1.40 PFLOP/s; the vendor library's product 360), 400 KC x
-// KS, 460 KS x KS, whose transposing reads get half the LDS bandwidth.  With
-// experts' short sums a tile's results leave beside too few products: 131,072
-// rows over 64 experts of 1024 x 2048 take 540, 600 and 715.
+// bf16, 8192 x 8192 x 4096: 432 us KC x KC (1.27 PFLOP/s; the vendor library's
+// product 350 on the same card), 430 KC x KS, 489 KS x KS, whose transposing reads
+// get half the LDS bandwidth.  The matrix units are busy 64% of the CUs' cycles, at
+// the 1.87 GHz that this leaves.  With experts' short sums a tile's results leave
+// beside too few products: 131,072 rows over 64 experts of 1024 x 2048 take 520,
+// 588 and 711, the matrix units busy 50% in the first.
 //
 // What lies outside an operand (K past its end, columns past a KS operand's,
 // rows that were routed nowhere) is read from 16 bytes of zeros, both
@@ -178,6 +179,26 @@ __device__ __forceinline__ void wait_stages(int k) {
     if (k < K) return wait_stages<K - 1, PER, EXTRA>(k);
   }
   __builtin_amdgcn_s_waitcnt(vm_count(K * PER + EXTRA < 63 ? K * PER + EXTRA : 63));
+}
+
+// Whether 256 x 256 tiles (t256 of them) or 128 x 128 (t128).  It is a matter of whole rounds over the chip, one large
+// tile a CU or two small ones: a round of large tiles takes 1.65 times as long as one of small ones and does twice the
+// work.  Measured, us in 128 x 128 and 256 x 256:
+//   two rounds against one: bf16 4096 x 4096 x 1024 40 and 36, 4 bits 4096 x 4096 x 4096 52 and 42, three-pass fp16 (24
+//   updates of 1024 x 1024) 2212 and 2042;
+//   five against three: bf16 5120 x 8192 x 2048 172 and 159, 4 bits 68.5 and 65, fp16 (64 updates of 1024 x 2048) 9847 and
+//   8559;
+//   one against one: bf16 2048 x 4096 x 1024 23.5 and 30, 4 bits 12.7 and 16.4, fp16 (12 of 1024 x 1024) 1118 and 1253.
+// Ragged experts fill a part of their last tiles and are of unequal length: `uneven` of a round, by which they take the
+// small tiles near an even choice.  Rows' products, 0.1: it decides five rounds against three, where either may be ahead
+// (bf16, 16,384 rows over 16 experts of 2048 x 512 57 and 63; 40,000 over 64 of 1024 x 1024 126 and 111, over experts of
+// weights e^2n, n normal, 126 and 134; 4 bits, 16,384 over 16 of 2048 x 2048 61 and 65).  Gradients, 0.25: it decides two
+// against one, where unequal experts lose more than equal ones win (4096 rows over 8 of 2048 x 1024 41 and 34 if equal, 51
+// and 71 with weights e^n).
+inline bool in_large_tiles(int64_t t256, int64_t t128, double uneven) {
+  const int64_t cu = device_cu_count();
+  const double rounds256 = double((t256 + cu - 1) / cu), rounds128 = double((t128 + 2 * cu - 1) / (2 * cu));
+  return t256 > 0 && 3.3 * (rounds256 + uneven) < 2 * rounds128;
 }
 
 #define QB_INLINE __attribute__((always_inline))

@@ -199,9 +199,11 @@ int launch_fp8_product(const uint8_t* xq, const uint8_t* xs, const uint8_t* w, c
 int launch_fp8_weight_grad(const uint8_t* dyt, const uint8_t* dyts, const uint8_t* xt, const uint8_t* xts, int N,
                            int C, int64_t ldm, const int32_t* off, int G, float* dw, hipStream_t st);
 
-// bf16 products.  A gradient of few tiles is split along its rows, while each
-// part keeps 256 of them, into at most 512 parts of tiles of 128 x 128 in all
-// (32 MiB of partial sums).
+// bf16 products.  A gradient of few tiles is split along its rows into at most
+// 16 parts and 512 parts of tiles of 128 x 128 in all (32 MiB of partial sums),
+// as many as leave an expert of average length 256 rows a part: offsets lie on
+// the device, so a longer expert has longer parts, and a shorter one parts that
+// are empty.
 inline int bf16_grad_splits(int64_t M, int64_t N, int64_t C, int G) {
   const int64_t tiles = G * ((N + 127) / 128) * ((C + 127) / 128);
   int64_t s = tiles > 0 && tiles < 256 ? 512 / tiles : 1;

@@ -9,11 +9,13 @@
 //
 // A step is three products, S, P = b S + c S S and a x + P x.  S and P are
 // symmetric: the tiles on and below the diagonal are computed and written to
-// both places.  64 matrices of 1024 x 2048: S 230 us (0.60 PFLOP/s of what is
-// computed), P 173 (336 with three passes), the sum 457 (0.60; 640 with two):
-// its products alone would take 204, and the 1.5 GB that it reads and writes
-// 290, which the addends' and results' share of a tile does not overlap enough.
-// Small matrices are bound by launches of 5 to 7 us, three a step.
+// both places.  64 matrices of 1024 x 2048: S 544 us (0.95 PFLOP/s of what is
+// computed, 10 tiles of 16 a matrix), P 326 (0.79), the sum 800 (1.03), the matrix
+// units busy 57, 47 and 52% of the CUs' cycles: the 640 tiles of S and P take three
+// rounds for two and a half, and the sum's 1.5 GB of addends and results, 290 us by
+// themselves, overlap its products in part.  The coarse form: S 227, P 172 in one
+// pass, the sum 453 in one pass and 634 in two.  Small matrices are bound by
+// launches of 6 to 11 us, three a step.
 //
 // Roundings.  Values are held as fp16 in two parts, the nearest and the nearest
 // to the rest (22 bits), times 2^12 for x and 2^8 for S and P (entries of x
@@ -119,8 +121,8 @@ static int tiled(Gemm16 g, int64_t tiles, hipStream_t st) {
   return int(hipGetLastError());
 }
 
-// Tiles by whole rounds over the chip, as the bf16 products choose them (64 matrices of 1024 x 2048, five steps, before
-// addends were read ahead: 5.46 ms with 256 x 256, 6.05 with 128 x 128; 5 of 301 x 165 take 64 x 64).
+// The smallest tiles while they all run at once (five steps of 2 matrices of 1024 x 1024 409 us, 572 in 128 x 128; of 20
+// of 512 x 512, which are too many for that, 452 and 433), then by whole rounds: in_large_tiles.
 template <int KIND, bool A_KS, bool B_KS, int PARTS, int PA, int PB>
 static int product(const Gemm16& g, hipStream_t st) {
   const int64_t cu = device_cu_count();
@@ -130,8 +132,7 @@ static int product(const Gemm16& g, hipStream_t st) {
   };
   const int64_t t256 = tiles(256), t128 = tiles(128), t64 = tiles(64);
   if (t64 <= 2 * cu) return tiled<KIND, A_KS, B_KS, PARTS, PA, PB, 64, 4>(g, t64, st);
-  const double rounds256 = double((t256 + cu - 1) / cu), rounds128 = double((t128 + 2 * cu - 1) / (2 * cu));
-  if (3.3 * rounds256 < 2 * rounds128) return tiled<KIND, A_KS, B_KS, PARTS, PA, PB, 256, 2>(g, t256, st);
+  if (in_large_tiles(t256, t128, 0.0)) return tiled<KIND, A_KS, B_KS, PARTS, PA, PB, 256, 2>(g, t256, st);
   return tiled<KIND, A_KS, B_KS, PARTS, PA, PB, 128, 2>(g, t128, st);
 }
 
@@ -183,7 +184,7 @@ int launch_orthogonalize(const float* x, int G, int N, int C, int steps, float a
     g.out = p;
     g.by_sum = c / kScaleS;
     g.by_add = b;
-    // (8 matrices of 512 x 1024: 226 us, 262 without it)
+    // (8 matrices of 512 x 1024 coarsely: 226 us, 262 without it)
     const bool rough = !exact && w.R >= 256 && i < 3 && i + 2 < steps;
     g.out_parts = rough ? 1 : 2;
     rc = rough ? product<kSqr, false, false, 1, 0, 0>(g, st) : product<kSqr, false, false, 3, 0b100, 0b010>(g, st);

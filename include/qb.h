@@ -635,7 +635,9 @@ QB_API int qb_fp8_weight_grad(const uint8_t* dyt, const uint8_t* dyts, const uin
  * M = 0.
  *
  * bf16 arrays by their element aligned; calls whose rows are multiples of 16
- * bytes and whose arrays are 16-byte aligned are the fastest.  0 <= M, Mx <=
+ * bytes and whose arrays are 16-byte aligned are the fastest.  One or a few rows
+ * are faster with transposed = 0, where the waves of a workgroup share C out (1 x
+ * 4096 x 4096 8 us, transposed 28).  0 <= M, Mx <=
  * 2^22 rows; 1 <= N, C <= 2^22; 1 <= G <= 256.
  */
 QB_API int qb_bf16_product(const uint16_t* x, int64_t Mx, const int32_t* row_src, int64_t M, const uint16_t* w, int N,
