@@ -44,6 +44,9 @@ std::string shape_name(c10::IntArrayRef s) {
   return o + (s.size() == 1 ? ",)" : ")");
 }
 
+// The device of the call's tensors, -1 before the first.
+thread_local int device;
+
 // A contiguous GPU tensor of this type, or nullptr for None.
 const at::Tensor* tensor_or_none(PyObject* o, ScalarType type, const char* name) {
   if (o == Py_None) return nullptr;
@@ -53,6 +56,10 @@ const at::Tensor* tensor_or_none(PyObject* o, ScalarType type, const char* name)
   if (t.scalar_type() != type)
     throw Bad{std::string(name) + " must be " + type_name(type) + ", got " + type_name(t.scalar_type())};
   if (!t.is_contiguous()) throw Bad{std::string(name) + " must be contiguous"};
+  const int at = t.device().index();
+  if (device >= 0 && at != device)
+    throw Bad{std::string(name) + " is on cuda:" + std::to_string(at) + ", another tensor on cuda:" + std::to_string(device)};
+  device = at;
   return &t;
 }
 const at::Tensor& tensor(PyObject* o, ScalarType type, const char* name, int dims) {
@@ -104,11 +111,15 @@ int narrow(int64_t v, const char* name) {
   return int(v);
 }
 
-PyObject* stream_handle;  // qb.py's: a stream object, or None for the current one, to its raw handle
+// qb.py's: a stream object, or None for the current one, to its raw handle; refuses one of another device than the tensors'
+PyObject* stream_handle;
 
 // The last argument of every call, looked at once the others are sound.
 qb_stream_t stream_of(PyObject* o) {
-  PyObject* h = PyObject_CallOneArg(stream_handle, o);
+  PyObject* const at = PyLong_FromLong(device);
+  if (!at) throw Raised{};
+  PyObject* h = PyObject_CallFunctionObjArgs(stream_handle, o, at, nullptr);
+  Py_DECREF(at);
   if (!h) throw Raised{};
   void* p = PyLong_AsVoidPtr(h);
   Py_DECREF(h);
@@ -419,6 +430,7 @@ int fp4_product(PyObject* const* a) {
 template <int (*F)(PyObject* const*), int N>
 PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != N) return PyErr_Format(PyExc_TypeError, "%d arguments expected, got %zd", N, n);
+  device = -1;
   try {
     return PyLong_FromLong(F(a));
   } catch (const Bad& e) {

@@ -152,10 +152,17 @@ def _check(rc: int):
         raise QBError(rc, f"{L.qb_status_string(rc).decode()}: {L.qb_last_error().decode()}")
 
 
-def _stream(stream) -> int:
+def _stream(stream, device=None) -> int:
+    """The raw handle of `stream` (None: the current one), which has to be of
+    the device that the call's tensors are on, where that is given."""
     if stream is None:
-        # the raw handle of torch.cuda.current_stream(), without making a Stream object of it
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        # without making a Stream object of torch.cuda.current_stream()
+        at = torch._C._cuda_getDevice()
+        if device is not None and device != at:
+            raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{at}")
+        return torch._C._cuda_getCurrentRawStream(at)
+    if device is not None and getattr(stream, "device_index", device) != device:
+        raise ValueError(f"the tensors are on cuda:{device}, the stream is of cuda:{stream.device_index}")
     return int(stream.cuda_stream)
 
 
@@ -678,8 +685,11 @@ def qb_orthogonalize(x, o, ws, steps=5, poly=(3.4445, -4.7750, 2.0315), stream=N
     a, b, c = poly
     G, N, Cn = (1,) * (3 - x.dim()) + tuple(x.shape)
     call = lib().qb_orthogonalize if exact else lib().qb_orthogonalize_coarse
-    _check(call(_ptr(x, torch.float32, "x"), G, N, Cn, steps, a, b, c, _ptr(o, torch.bfloat16, "o", x.shape),
-                _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+    px, po, pw = _ptr(x, torch.float32, "x"), _ptr(o, torch.bfloat16, "o", x.shape), _ptr(ws, torch.uint8, "ws")
+    for name, t in (("o", o), ("ws", ws)):
+        if t.device != x.device:
+            raise ValueError(f"{name} is on {t.device}, x on {x.device}")
+    _check(call(px, G, N, Cn, steps, a, b, c, po, pw, ws.numel(), _stream(stream, x.get_device())))
 
 
 # ---------------------------------------------------------------------------
