@@ -253,7 +253,7 @@ int launch_bf16_product(const uint16_t* x, int Mx, const int32_t* src, int M, co
   if (!transposed && (strips <= 2 * device_cu_count() || (rows <= 4 && (direct || !off))))
     return rows <= 16 ? few<1>(g, st) : few<2>(g, st);
   // Experts of so few rows fill half of a large tile at most (5120 rows over 40 experts of 1024 x 2048 57 us in 128 x 128,
-  // 67 in 256 x 256; 3072 over 48 56 and 65).
+  // 67 in 256 x 256; 5000 over 40 of 1000 x 2048 57 and 65).
   const int64_t t256 = rows <= 128 && off ? 0 : tiles(256);
   // Of ragged experts' tiles of 64 rows a third is taken to be missing or nearly empty (2000 rows over 16 experts of 700 x
   // 1160 17 us in 64 x 64, 23 in 128 x 128; of 1400 x 1024 22 and 18; near the border the other is up to 14% faster: of
