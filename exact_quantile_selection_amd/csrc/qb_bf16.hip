@@ -243,7 +243,7 @@ int launch_bf16_product(const uint16_t* x, int Mx, const int32_t* src, int M, co
   const bool direct = C % 8 == 0 && (!transposed || N % 8 == 0) && aligned16(x) && aligned16(w) && by_offset(src, Mx, C);
   // The kernel of few rows: while a workgroup for each 16 columns, two a CU, shares out K (64 x 1024 x 4096: 13 us against
   // 28 in tiles of 64 x 64, 64 x 4096 x 4096 24 against 29, 128 x 4096 x 4096 44 against 29), and for very few rows, whose
-  // tiles would multiply little else than padding (1 x 16,384 x 4096 22 against 29; 512 rows over 256 experts of 1024 x
+  // tiles would multiply little else than padding (1 x 16,384 x 4096 27 against 32; 512 rows over 256 experts of 1024 x
   // 2048 167 against 179; 8 rows each of 64 experts 53 against 43), unless experts' rows begin anywhere (256 rows over 64
   // experts of 730 x 1163 60 against 30).  The other order has no such kernel: its few rows run in tiles, K by one workgroup
   // (the gradient of 1 or 16 rows of 4096 x 4096 28 us where the forward product takes 8 and 10, of 4096 x 16,384 103).
